@@ -128,6 +128,7 @@ def load():
         lib.gemm_f16_splitk_workspace_bytes.restype = ctypes.c_int
         lib.gemm_f16_device_cus.argtypes = [ctypes.POINTER(i32)]
         lib.gemm_f16_device_cus.restype = ctypes.c_int
+        lowbit._declare(lib)
         _lib = lib
         return lib
 
@@ -560,3 +561,13 @@ def matmul(a, b, out=None, stream=None):
     if m > 0 and n > 0 and k > 0 and a.is_cuda and matmul_splits(lay, m, n, k, a) > 1:
         return gemm_splitk(xa, xb, lay, out=out, stream=stream)
     return gemm(xa, xb, lay, out=out, stream=stream)
+
+
+# Products with an operand in 4 or 8 bits; at the end because that module
+# builds on the names above.
+from . import lowbit  # noqa: E402
+from .lowbit import (  # noqa: E402,F401
+    LOWBIT_DECODE, LowbitPlan, Q8Matrix, W4Matrix, dequantize_q8, dequantize_w4, gemm_f16_nt_w4,
+    gemm_f16_nt_w4_plan, gemm_f16_q8_dequantize, gemm_f16_q8_quantize, gemm_f16_tn_q8,
+    gemm_f16_tn_q8_plan, gemm_f16_w4_dequantize, gemm_f16_w4_pack, gemm_f16_w4_quantize,
+    gemm_f16_w4_sizes, gemm_nt_w4, gemm_tn_q8, pack_w4, quantize_q8, quantize_w4)

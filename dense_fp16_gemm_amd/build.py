@@ -7,9 +7,11 @@ import subprocess
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
-SOURCES = [os.path.join(PKG_DIR, "csrc", "gemm_f16_nt.hip")]
+SOURCES = [os.path.join(PKG_DIR, "csrc", "gemm_f16_nt.hip"),
+           os.path.join(PKG_DIR, "csrc", "lowbit.hip")]
 HEADERS = [os.path.join(PKG_DIR, "csrc", "tile_schedule.h"),
-           os.path.join(ROOT, "include", "gemm_f16_nt.h")]
+           os.path.join(ROOT, "include", "gemm_f16_nt.h"),
+           os.path.join(ROOT, "include", "gemm_f16_lowbit.h")]
 LIB_PATH = os.path.join(PKG_DIR, "libgemm_f16.so")
 # the benchmark's calibration kernel (not part of the GEMM library)
 CALIB_SOURCES = [os.path.join(PKG_DIR, "csrc", "mfma_ceiling.hip")]

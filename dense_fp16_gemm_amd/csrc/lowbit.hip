@@ -1,0 +1,727 @@
+// Operands in 4 and 8 bits for MI355X (gfx950): quantising, reading back, and
+// the products C = A W^T (4-bit weights) and C = A^T X (8-bit activations).
+// The forms, and why every kernel here works on the same exact fp16 matrix,
+// are described in gemm_f16_lowbit.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gemm_f16_lowbit.h"
+
+namespace gemm_f16_lowbit {
+
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+// 16 bytes at any 2-byte alignment (the target's unaligned-access mode)
+typedef _Float16 half8_u_t __attribute__((ext_vector_type(8), aligned(2)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_u_t __attribute__((ext_vector_type(2), aligned(1)));
+
+constexpr int WAVES = 4;            // waves of a workgroup here
+constexpr uint16_t FP16_NAN = 0x7e00;
+
+template <class T, class S>
+__device__ __forceinline__ T bits_as(S s)
+{
+    static_assert(sizeof(T) == sizeof(S), "same size");
+    return __builtin_bit_cast(T, s);
+}
+
+// Eight halves of a row at column c, as dwords; columns at or past `cols` are 0.
+__device__ __forceinline__ u32x4_t load8(const uint16_t *row, int32_t c, int32_t cols)
+{
+    if (c + 8 <= cols) return bits_as<u32x4_t>(half8_t(*reinterpret_cast<const half8_u_t *>(row + c)));
+    u32x4_t v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < cols) v[i / 2] |= static_cast<uint32_t>(row[c + i]) << (16 * (i % 2));
+    return v;
+}
+
+__device__ __forceinline__ void store8(uint16_t *row, int32_t c, int32_t cols, half8_t v)
+{
+    if (c + 8 <= cols) {
+        *reinterpret_cast<half8_u_t *>(row + c) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < cols) row[c + i] = bits_as<uint16_t>(_Float16(v[i]));
+}
+
+// Largest of eight halves by magnitude, as fp16 bits: those of non-negative
+// numbers, infinity and NaN order as integers.
+__device__ __forceinline__ uint32_t largest8(u32x4_t v)
+{
+    u16x2_t m = bits_as<u16x2_t>(v[0] & 0x7fff7fffu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        m = __builtin_elementwise_max(m, bits_as<u16x2_t>(v[i] & 0x7fff7fffu));
+    return m[0] > m[1] ? m[0] : m[1];
+}
+
+// The scale of a group whose largest magnitude has fp16 bits `big`: the
+// smallest s of BITS significant bits, a multiple of 2^-24, with TOP s >= big.
+// big / TOP is taken as a product with (1 - 2^-20) / TOP: big has 11
+// significant bits and TOP s at most 11, so where they differ they do so by
+// more than 2^-12 of their value, and where they are equal the product falls
+// short of s and rounds up to it.  (Checked for every fp16 value.)
+template <int BITS, int TOP>
+__device__ __forceinline__ float group_scale(uint32_t big, float most)
+{
+    const float t = static_cast<float>(bits_as<_Float16>(static_cast<uint16_t>(big))) *
+                    ((1.0f / TOP) * (1.0f - 0x1p-20f));
+    constexpr uint32_t drop = (1u << (24 - BITS)) - 1;
+    const float up = bits_as<float>((bits_as<uint32_t>(t) + drop) & ~drop);
+    const float s = t < 0x1p-24f * (1 << (BITS - 1)) ? __builtin_ceilf(t * 0x1p24f) * 0x1p-24f : up;
+    return fminf(fmaxf(s, 0x1p-24f), most);
+}
+
+// x / s rounded to nearest, ties to even.  The product with the reciprocal can
+// miss a tie by an ulp; one Newton step gives the correctly rounded quotient,
+// and a quotient that is not a tie is further from one than fp32 resolves
+// (checked for every fp16 x and every scale).
+__device__ __forceinline__ float quotient(float x, float s, float r)
+{
+    const float t = x * r;
+    return __builtin_rintf(__builtin_fmaf(__builtin_fmaf(-t, s, x), r, t));
+}
+
+// ---------------------------------------------------------------------------
+// W4: quantise or pack
+// ---------------------------------------------------------------------------
+// One wave per tile of 16 rows by 128 columns, each lane the 32 weights whose
+// words it writes: four loads of 16 bytes (8 for int8 codes), the group's
+// largest magnitude over the four lanes of a row, one 16-byte store.  Memory
+// bounds it.
+struct W4EncodeParams {
+    const uint16_t *W;       // fp16 [N, K], or
+    const int8_t *codes;     // int8 [N, K] and
+    const uint16_t *in_scales;  // fp16 [N, ceil(K / group)]
+    u32x4_t *words;
+    uint16_t *scales;
+    int32_t N, K, kt, tiles;
+    int32_t shift;           // log2 of the group
+};
+
+// Most significant 8 bits of a scale, to nearest with ties to even.
+__device__ __forceinline__ float round_scale(float s)
+{
+    const uint32_t u = bits_as<uint32_t>(s);
+    return bits_as<float>((u + 0x7fffu + ((u >> 16) & 1)) & 0xffff0000u);
+}
+
+template <bool PACK>
+__global__ __launch_bounds__(64 * WAVES) void w4_encode_kernel(W4EncodeParams p)
+{
+    const int lane = threadIdx.x & 63;
+    const int r = lane & 15, kq = lane >> 4;
+    const int per_tile = 128 >> p.shift;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * WAVES;
+    for (int64_t tile = static_cast<int64_t>(blockIdx.x) * WAVES + (threadIdx.x >> 6); tile < p.tiles;
+         tile += step) {
+        const int32_t b = static_cast<int32_t>(tile) / p.kt;
+        const int32_t t = static_cast<int32_t>(tile) - b * p.kt;
+        const int64_t n = static_cast<int64_t>(b) * 16 + r;
+        const int32_t cols = n < p.N ? p.K : 0;     // rows past N are zeros
+        const int64_t row = n < p.N ? n : 0;
+        const int64_t k0 = static_cast<int64_t>(t) * 128 + kq * 8;  // may pass 2^31 in a pad
+        u32x4_t v[4];
+        int32_t q[4][8];
+        uint32_t big[4];
+        // per 32 columns of this lane's row: the eight values, and the largest
+        // magnitude of all 32 (fp16 bits, or of the codes)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t c = k0 + 32 * j;
+            if constexpr (PACK) {
+                const int8_t *src = p.codes + row * p.K + c;
+                uint32_t d[2] = {0, 0};
+                if (c + 8 <= cols) {
+                    const u32x2_u_t w = *reinterpret_cast<const u32x2_u_t *>(src);
+                    d[0] = w[0];
+                    d[1] = w[1];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i < cols)
+                            d[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(src[i])) << (8 * (i % 4));
+                }
+                big[j] = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    q[j][i] = static_cast<int8_t>(d[i / 4] >> (8 * (i % 4)));
+                    // 9 marks a code that four bits do not hold
+                    const uint32_t m = q[j][i] < -8 || q[j][i] > 7 ? 9 : q[j][i] < 0 ? -q[j][i] : q[j][i];
+                    big[j] = m > big[j] ? m : big[j];
+                }
+            } else {
+                v[j] = c < cols ? load8(p.W + row * p.K, static_cast<int32_t>(c), cols)
+                                : u32x4_t{0, 0, 0, 0};
+                big[j] = largest8(v[j]);
+            }
+            uint32_t o = __shfl_xor(big[j], 16);
+            big[j] = o > big[j] ? o : big[j];
+            o = __shfl_xor(big[j], 32);
+            big[j] = o > big[j] ? o : big[j];
+        }
+        if (p.shift >= 6) {
+            big[0] = big[1] = big[0] > big[1] ? big[0] : big[1];
+            big[2] = big[3] = big[2] > big[3] ? big[2] : big[3];
+        }
+        if (p.shift == 7) big[0] = big[1] = big[2] = big[3] = big[0] > big[2] ? big[0] : big[2];
+        u32x4_t out;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float s;
+            bool bad;
+            if constexpr (PACK) {
+                const int64_t k = static_cast<int64_t>(t) * 128 + 32 * j;
+                s = 0.0f;
+                if (k < cols) {
+                    const int64_t groups = (static_cast<int64_t>(p.K) + (1 << p.shift) - 1) >> p.shift;
+                    s = round_scale(static_cast<float>(
+                        bits_as<_Float16>(p.in_scales[row * groups + (k >> p.shift)])));
+                }
+                bad = !(__builtin_fabsf(s) <= 65504.0f) || big[j] > 8 ||
+                      __builtin_fabsf(s) * static_cast<float>(big[j]) > 65504.0f;
+            } else {
+                s = group_scale<8, 7>(big[j], 9344.0f);
+                bad = big[j] >= 0x7c00;
+                const float rcp = 1.0f / s;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint16_t h = static_cast<uint16_t>(v[j][i / 2] >> (16 * (i % 2)));
+                    const float x = bad ? 0.0f : static_cast<float>(bits_as<_Float16>(h));
+                    const int32_t c = static_cast<int32_t>(quotient(x, s, rcp));
+                    q[j][i] = c > 7 ? 7 : c < -7 ? -7 : c;   // past 7 only where s is capped
+                }
+            }
+            uint32_t word = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                word |= static_cast<uint32_t>((bad ? 0 : q[j][i]) + 8) << (16 * (i % 2) + 4 * (i / 2));
+            out[j] = word;
+            if (kq == 0 && ((32 * j) & ((1 << p.shift) - 1)) == 0) {
+                const int64_t g = static_cast<int64_t>(t) * per_tile + ((32 * j) >> p.shift);
+                uint16_t *to = p.scales + (static_cast<int64_t>(b) * p.kt * per_tile + g) * 16 + r;
+                *to = bad ? FP16_NAN : bits_as<uint16_t>(static_cast<_Float16>(s));
+            }
+        }
+        p.words[tile * 64 + lane] = out;
+    }
+}
+
+// Elements 2 p and 2 p + 1 of a word, as the halves q: the four bits become
+// the low bits of 1024 + (q + 8), which is exact in fp16.
+__device__ __forceinline__ half2_t w4_pair(uint32_t word, int p)
+{
+    const uint32_t u = ((word >> (4 * p)) & 0x000f000fu) | 0x64006400u;
+    const half2_t off = {_Float16(1032.0f), _Float16(1032.0f)};
+    return bits_as<half2_t>(u) - off;
+}
+
+// A word's eight weights times their scale.
+__device__ __forceinline__ half8_t w4_scaled(uint32_t word, _Float16 s)
+{
+    const half2_t s2 = {s, s};
+    half8_t h;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const half2_t x = w4_pair(word, p) * s2;
+        h[2 * p] = x[0];
+        h[2 * p + 1] = x[1];
+    }
+    return h;
+}
+
+struct W4DecodeParams {
+    const u32x4_t *words;
+    const uint16_t *scales;
+    uint16_t *W;
+    int32_t N, K, kt, tiles;
+    int32_t shift;
+};
+
+// W4 back to fp16, one wave per tile; memory bounds it.
+__global__ __launch_bounds__(64 * WAVES) void w4_decode_kernel(W4DecodeParams p)
+{
+    const int lane = threadIdx.x & 63;
+    const int r = lane & 15, kq = lane >> 4;
+    const int per_tile = 128 >> p.shift;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * WAVES;
+    for (int64_t tile = static_cast<int64_t>(blockIdx.x) * WAVES + (threadIdx.x >> 6); tile < p.tiles;
+         tile += step) {
+        const int32_t b = static_cast<int32_t>(tile) / p.kt;
+        const int32_t t = static_cast<int32_t>(tile) - b * p.kt;
+        const int64_t n = static_cast<int64_t>(b) * 16 + r;
+        if (n >= p.N) continue;
+        const u32x4_t w = p.words[tile * 64 + lane];
+        const uint16_t *s = p.scales + tile * per_tile * 16 + r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t c = static_cast<int64_t>(t) * 128 + 32 * j + kq * 8;
+            const _Float16 sj = bits_as<_Float16>(s[((32 * j) >> p.shift) * 16]);
+            if (c < p.K) store8(p.W + n * p.K, static_cast<int32_t>(c), p.K, w4_scaled(w[j], sj));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Q8: quantise and read back
+// ---------------------------------------------------------------------------
+// A thread handles eight neighbouring columns, four neighbouring threads the
+// 32 of a group, 2^tx_shift threads (at most a wave: 512 columns) a row, and
+// each thread ROWS rows, so that several loads are in flight.  Memory bounds
+// both kernels.
+constexpr int Q8_ROWS = 4;
+
+struct Q8Params {
+    const uint16_t *X;        // quantise: from X to codes and scales
+    uint16_t *out;            // dequantise: from codes and scales to out
+    u32x2_t *codes;           // 8 codes each, 4 Ng a row
+    uint16_t *scales;
+    int32_t R, N, chunks;     // chunks of 8 columns a row: 4 Ng
+    int32_t tx_shift, col_blocks;
+};
+
+__device__ __forceinline__ uint32_t quad_max(uint32_t v)
+{
+    uint32_t o = __builtin_amdgcn_update_dpp(0, v, 0xb1, 0xf, 0xf, true);   // lane ^ 1
+    v = o > v ? o : v;
+    o = __builtin_amdgcn_update_dpp(0, v, 0x4e, 0xf, 0xf, true);            // lane ^ 2
+    return o > v ? o : v;
+}
+
+__global__ __launch_bounds__(64 * WAVES) void q8_encode_kernel(Q8Params p)
+{
+    const int32_t rb = blockIdx.x / p.col_blocks, cb = blockIdx.x - rb * p.col_blocks;
+    const int32_t chunk = (cb << p.tx_shift) + (threadIdx.x & ((1 << p.tx_shift) - 1));
+    const int32_t ty = (64 * WAVES) >> p.tx_shift;
+    const int64_t row0 = static_cast<int64_t>(rb) * ty * Q8_ROWS + (threadIdx.x >> p.tx_shift);
+    if (chunk >= p.chunks) return;    // whole groups: chunks is a multiple of 4
+    const int64_t c = static_cast<int64_t>(chunk) * 8;
+    u32x4_t v[Q8_ROWS];
+#pragma unroll
+    for (int i = 0; i < Q8_ROWS; ++i) {
+        const int64_t row = row0 + i * ty;
+        v[i] = u32x4_t{0, 0, 0, 0};
+        if (row < p.R && c < p.N) v[i] = load8(p.X + row * p.N, static_cast<int32_t>(c), p.N);
+    }
+#pragma unroll
+    for (int i = 0; i < Q8_ROWS; ++i) {
+        const int64_t row = row0 + i * ty;
+        const uint32_t big = quad_max(largest8(v[i]));
+        const bool bad = big >= 0x7c00;
+        const float s = group_scale<4, 127>(big, 576.0f);
+        const float rcp = 1.0f / s;
+        // 576 (the only scale past 512) times 114 would pass fp16's largest
+        const int32_t most = s > 512.0f ? 113 : 127;
+        u32x2_t q = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint16_t h = static_cast<uint16_t>(v[i][e / 2] >> (16 * (e % 2)));
+            const float x = bad ? 0.0f : static_cast<float>(bits_as<_Float16>(h));
+            int32_t k = static_cast<int32_t>(quotient(x, s, rcp));
+            k = k > most ? most : k < -most ? -most : k;
+            q[e / 4] |= (static_cast<uint32_t>(k) & 0xffu) << (8 * (e % 4));
+        }
+        if (row < p.R) {
+            p.codes[row * p.chunks + chunk] = q;
+            if ((chunk & 3) == 0)
+                p.scales[row * (p.chunks >> 2) + (chunk >> 2)] =
+                    bad ? FP16_NAN : bits_as<uint16_t>(static_cast<_Float16>(s));
+        }
+    }
+}
+
+// Four int8 codes of a dword times their scale: a byte b biased by 128 becomes
+// the low bits of 1024 + (b + 128), which is exact in fp16.
+__device__ __forceinline__ void q8_scaled(uint32_t codes, half2_t s2, half2_t *lo, half2_t *hi)
+{
+    const uint32_t u = codes ^ 0x80808080u;
+    const half2_t off = {_Float16(1152.0f), _Float16(1152.0f)};
+    // v_perm_b32: bytes of u spread to the low bytes of two halves, 0x64 above
+    const uint32_t a = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
+    const uint32_t b = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
+    *lo = (bits_as<half2_t>(a) - off) * s2;
+    *hi = (bits_as<half2_t>(b) - off) * s2;
+}
+
+__global__ __launch_bounds__(64 * WAVES) void q8_decode_kernel(Q8Params p)
+{
+    const int32_t rb = blockIdx.x / p.col_blocks, cb = blockIdx.x - rb * p.col_blocks;
+    const int32_t chunk = (cb << p.tx_shift) + (threadIdx.x & ((1 << p.tx_shift) - 1));
+    const int32_t ty = (64 * WAVES) >> p.tx_shift;
+    const int64_t row0 = static_cast<int64_t>(rb) * ty * Q8_ROWS + (threadIdx.x >> p.tx_shift);
+    const int64_t c = static_cast<int64_t>(chunk) * 8;
+    if (chunk >= p.chunks || c >= p.N) return;
+    u32x2_t q[Q8_ROWS];
+    uint16_t s[Q8_ROWS];
+#pragma unroll
+    for (int i = 0; i < Q8_ROWS; ++i) {
+        const int64_t row = row0 + i * ty < p.R ? row0 + i * ty : 0;
+        q[i] = p.codes[row * p.chunks + chunk];
+        s[i] = p.scales[row * (p.chunks >> 2) + (chunk >> 2)];
+    }
+#pragma unroll
+    for (int i = 0; i < Q8_ROWS; ++i) {
+        const int64_t row = row0 + i * ty;
+        if (row >= p.R) continue;
+        const half2_t s2 = {bits_as<_Float16>(s[i]), bits_as<_Float16>(s[i])};
+        half2_t x[4];
+        q8_scaled(q[i][0], s2, &x[0], &x[1]);
+        q8_scaled(q[i][1], s2, &x[2], &x[3]);
+        half8_t h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = x[e / 2][e % 2];
+        store8(p.out + row * p.N, static_cast<int32_t>(c), p.N, h);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+static int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+struct Array {
+    const void *p;
+    int64_t bytes;
+    int64_t align;
+    bool written;
+};
+
+// NULL, alignment and overlap of a call's arrays (any with one that is written).
+static int check_arrays(const Array *arrays, int count)
+{
+    for (int i = 0; i < count; ++i)
+        if (arrays[i].bytes > 0 && !arrays[i].p) return GEMM_F16_INVALID_ARG;
+    for (int i = 0; i < count; ++i)
+        for (int j = 0; j < i; ++j) {
+            if (!(arrays[i].written || arrays[j].written)) continue;
+            if (arrays[i].bytes <= 0 || arrays[j].bytes <= 0) continue;
+            const uintptr_t a = reinterpret_cast<uintptr_t>(arrays[i].p);
+            const uintptr_t b = reinterpret_cast<uintptr_t>(arrays[j].p);
+            if (a < b + static_cast<uintptr_t>(arrays[j].bytes) &&
+                b < a + static_cast<uintptr_t>(arrays[i].bytes))
+                return GEMM_F16_INVALID_ARG;
+        }
+    for (int i = 0; i < count; ++i)
+        if (arrays[i].bytes > 0 && reinterpret_cast<uintptr_t>(arrays[i].p) % arrays[i].align != 0)
+            return GEMM_F16_UNSUPPORTED;
+    return GEMM_F16_OK;
+}
+
+static int launch(const void *fn, int64_t grid, int threads, void *params, hipStream_t stream)
+{
+    // the launch's own status only: the thread's sticky error state is neither
+    // read nor cleared
+    void *args[] = {params};
+    const hipError_t err = hipLaunchKernel(fn, dim3(static_cast<uint32_t>(grid)),
+                                           dim3(static_cast<uint32_t>(threads)), args, 0, stream);
+    return err == hipSuccess ? GEMM_F16_OK : GEMM_F16_LAUNCH_FAILED;
+}
+
+struct W4Shape {
+    int64_t nb, kt, tiles, words, scales;   // blocks, tiles a block, all tiles, bytes
+    int32_t shift;
+};
+
+static int w4_shape(int64_t N, int64_t K, int32_t group, W4Shape *s)
+{
+    if (N < 0 || K < 0) return GEMM_F16_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return GEMM_F16_INVALID_ARG;
+    if (N > INT32_MAX || K > INT32_MAX) return GEMM_F16_UNSUPPORTED;
+    s->nb = cdiv(N, 16);
+    s->kt = cdiv(K, 128);
+    s->tiles = s->nb * s->kt;
+    if (s->tiles > INT32_MAX) return GEMM_F16_UNSUPPORTED;
+    s->words = s->tiles * 1024;
+    s->scales = s->tiles * (128 / group) * 32;
+    s->shift = group == 32 ? 5 : group == 64 ? 6 : 7;
+    return GEMM_F16_OK;
+}
+
+// workgroups for `tiles` waves of work: the loops take the rest
+static int64_t wave_grid(int64_t tiles) { return std::min<int64_t>(cdiv(tiles, WAVES), 1 << 20); }
+
+static int w4_encode(int64_t N, int64_t K, int32_t group, const void *W, const void *codes,
+                     const void *in_scales, void *words, void *scales, hipStream_t stream)
+{
+    W4Shape s;
+    const int v = w4_shape(N, K, group, &s);
+    if (v != GEMM_F16_OK) return v;
+    const bool pack = W == nullptr && codes != nullptr;
+    const Array in[2] = {pack ? Array{codes, N * K, 1, false} : Array{W, N * K * 2, 2, false},
+                         Array{in_scales, pack ? N * cdiv(K, group) * 2 : 0, 2, false}};
+    const Array arrays[4] = {in[0], in[1], {words, s.words, 16, true}, {scales, s.scales, 8, true}};
+    const int a = check_arrays(arrays, 4);
+    if (a != GEMM_F16_OK || s.tiles == 0) return a;
+    W4EncodeParams p;
+    p.W = static_cast<const uint16_t *>(W);
+    p.codes = static_cast<const int8_t *>(codes);
+    p.in_scales = static_cast<const uint16_t *>(in_scales);
+    p.words = static_cast<u32x4_t *>(words);
+    p.scales = static_cast<uint16_t *>(scales);
+    p.N = static_cast<int32_t>(N);
+    p.K = static_cast<int32_t>(K);
+    p.kt = static_cast<int32_t>(s.kt);
+    p.tiles = static_cast<int32_t>(s.tiles);
+    p.shift = s.shift;
+    const void *fn = pack ? reinterpret_cast<const void *>(&w4_encode_kernel<true>)
+                          : reinterpret_cast<const void *>(&w4_encode_kernel<false>);
+    return launch(fn, wave_grid(s.tiles), 64 * WAVES, &p, stream);
+}
+
+static int w4_decode(int64_t N, int64_t K, const W4Shape &s, const void *words,
+                     const void *scales, void *W, hipStream_t stream)
+{
+    W4DecodeParams p;
+    p.words = static_cast<const u32x4_t *>(words);
+    p.scales = static_cast<const uint16_t *>(scales);
+    p.W = static_cast<uint16_t *>(W);
+    p.N = static_cast<int32_t>(N);
+    p.K = static_cast<int32_t>(K);
+    p.kt = static_cast<int32_t>(s.kt);
+    p.tiles = static_cast<int32_t>(s.tiles);
+    p.shift = s.shift;
+    return launch(reinterpret_cast<const void *>(&w4_decode_kernel), wave_grid(s.tiles), 64 * WAVES,
+                  &p, stream);
+}
+
+struct Q8Shape {
+    int64_t groups, codes, scales;   // groups a row, bytes
+};
+
+static int q8_shape(int64_t R, int64_t N, Q8Shape *s)
+{
+    if (R < 0 || N < 0) return GEMM_F16_INVALID_ARG;
+    if (R > INT32_MAX - 31 || N > INT32_MAX - 31) return GEMM_F16_UNSUPPORTED;
+    s->groups = cdiv(N, GEMM_F16_Q8_GROUP);
+    s->codes = R * s->groups * GEMM_F16_Q8_GROUP;
+    s->scales = R * s->groups * 2;
+    return GEMM_F16_OK;
+}
+
+static int q8_launch(const void *fn, int64_t R, int64_t N, const Q8Shape &s, const void *X,
+                     void *out, const void *codes, const void *scales, hipStream_t stream)
+{
+    Q8Params p;
+    p.X = static_cast<const uint16_t *>(X);
+    p.out = static_cast<uint16_t *>(out);
+    p.codes = static_cast<u32x2_t *>(const_cast<void *>(codes));
+    p.scales = static_cast<uint16_t *>(const_cast<void *>(scales));
+    p.R = static_cast<int32_t>(R);
+    p.N = static_cast<int32_t>(N);
+    p.chunks = static_cast<int32_t>(s.groups * 4);
+    p.tx_shift = 2;
+    while (p.tx_shift < 6 && (1 << p.tx_shift) < p.chunks) ++p.tx_shift;
+    const int64_t col_blocks = cdiv(p.chunks, int64_t(1) << p.tx_shift);
+    p.col_blocks = static_cast<int32_t>(col_blocks);
+    const int64_t grid = col_blocks * cdiv(R, int64_t((64 * WAVES) >> p.tx_shift) * Q8_ROWS);
+    if (grid > INT32_MAX) return GEMM_F16_UNSUPPORTED;
+    return launch(fn, grid, 64 * WAVES, &p, stream);
+}
+
+// ---- products ---------------------------------------------------------------
+// Decode: the operand in fp16 at the workspace's start, then what the GEMM's
+// own split over K needs.
+static int decode_plan(int64_t M, int64_t N, int64_t K, int32_t num_cus, bool tn,
+                       gemm_f16_lowbit_plan_t *plan)
+{
+    gemm_f16_nt_plan_t g;
+    int32_t splits = 1;
+    int64_t ws = 0;
+    const int v = tn ? gemm_f16_tn_splitk_plan(M, N, K, num_cus, 0, &g, &splits, &ws)
+                     : gemm_f16_nt_splitk_plan(M, N, K, num_cus, 0, &g, &splits, &ws);
+    if (v != GEMM_F16_OK) return v;
+    plan->kernel = GEMM_F16_LOWBIT_DECODE;
+    plan->block_m = g.block_m;
+    plan->block_n = g.block_n;
+    plan->waves = g.waves;
+    plan->splits = splits;
+    plan->grid = g.grid;
+    plan->workspace_bytes = round_up(N * K * 2, 256) + ws;
+    return GEMM_F16_OK;
+}
+
+static int w4_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t num_cus,
+                   gemm_f16_lowbit_plan_t *plan)
+{
+    W4Shape s;
+    const int v = w4_shape(N, K, group, &s);
+    if (v != GEMM_F16_OK) return v;
+    if (M < 0 || num_cus <= 0) return GEMM_F16_INVALID_ARG;
+    if (M > INT32_MAX) return GEMM_F16_UNSUPPORTED;
+    *plan = gemm_f16_lowbit_plan_t{};
+    plan->splits = 1;
+    if (M == 0 || N == 0 || K == 0) return GEMM_F16_OK;
+    return decode_plan(M, N, K, num_cus, false, plan);
+}
+
+static int q8_plan(int64_t M, int64_t N, int64_t K, int32_t num_cus, gemm_f16_lowbit_plan_t *plan)
+{
+    Q8Shape s;
+    const int v = q8_shape(K, N, &s);
+    if (v != GEMM_F16_OK) return v;
+    if (M < 0 || num_cus <= 0) return GEMM_F16_INVALID_ARG;
+    if (M > INT32_MAX) return GEMM_F16_UNSUPPORTED;
+    *plan = gemm_f16_lowbit_plan_t{};
+    plan->splits = 1;
+    if (M == 0 || N == 0 || K == 0) return GEMM_F16_OK;
+    return decode_plan(M, N, K, num_cus, true, plan);
+}
+
+}  // namespace gemm_f16_lowbit
+
+// ---------------------------------------------------------------------------
+// C ABI
+// ---------------------------------------------------------------------------
+using namespace gemm_f16_lowbit;
+
+extern "C" int gemm_f16_w4_sizes(int64_t N, int64_t K, int32_t group, int64_t *words_bytes,
+                                 int64_t *scales_bytes)
+{
+    if (!words_bytes || !scales_bytes) return GEMM_F16_INVALID_ARG;
+    W4Shape s;
+    const int v = w4_shape(N, K, group, &s);
+    if (v != GEMM_F16_OK) return v;
+    *words_bytes = s.words;
+    *scales_bytes = s.scales;
+    return GEMM_F16_OK;
+}
+
+extern "C" int gemm_f16_w4_quantize(int64_t N, int64_t K, int32_t group, const void *W,
+                                    void *words, void *scales, hipStream_t stream)
+{
+    return w4_encode(N, K, group, W, nullptr, nullptr, words, scales, stream);
+}
+
+extern "C" int gemm_f16_w4_pack(int64_t N, int64_t K, int32_t group, const void *codes,
+                                const void *in_scales, void *words, void *scales,
+                                hipStream_t stream)
+{
+    if (N > 0 && K > 0 && !codes) return GEMM_F16_INVALID_ARG;
+    return w4_encode(N, K, group, nullptr, codes, in_scales, words, scales, stream);
+}
+
+extern "C" int gemm_f16_w4_dequantize(int64_t N, int64_t K, int32_t group, const void *words,
+                                      const void *scales, void *W, hipStream_t stream)
+{
+    W4Shape s;
+    const int v = w4_shape(N, K, group, &s);
+    if (v != GEMM_F16_OK) return v;
+    const Array arrays[3] = {
+        {words, s.words, 16, false}, {scales, s.scales, 8, false}, {W, N * K * 2, 2, true}};
+    const int a = check_arrays(arrays, 3);
+    if (a != GEMM_F16_OK || s.tiles == 0) return a;
+    return w4_decode(N, K, s, words, scales, W, stream);
+}
+
+extern "C" int gemm_f16_nt_w4_plan(int64_t M, int64_t N, int64_t K, int32_t group,
+                                   int32_t num_cus, gemm_f16_lowbit_plan_t *plan)
+{
+    return plan ? w4_plan(M, N, K, group, num_cus, plan) : GEMM_F16_INVALID_ARG;
+}
+
+extern "C" int gemm_f16_nt_w4(int64_t M, int64_t N, int64_t K, int32_t group, const void *A,
+                              const void *words, const void *scales, void *C, void *workspace,
+                              int64_t workspace_bytes, hipStream_t stream)
+{
+    W4Shape s;
+    int v = w4_shape(N, K, group, &s);
+    if (v != GEMM_F16_OK) return v;
+    if (M < 0 || workspace_bytes < 0) return GEMM_F16_INVALID_ARG;
+    if (M > INT32_MAX) return GEMM_F16_UNSUPPORTED;
+    const Array arrays[5] = {{A, M * K * 2, 2, false},
+                             {words, s.words, 16, false},
+                             {scales, s.scales, 8, false},
+                             {C, M * N * 2, 2, true},
+                             {workspace, workspace ? workspace_bytes : 0, 256, true}};
+    v = check_arrays(arrays, 5);
+    if (v != GEMM_F16_OK || M == 0 || N == 0) return v;
+    if (K == 0) return gemm_f16_nt(M, N, 0, A, nullptr, C, stream);
+    int32_t cus = 0;
+    v = gemm_f16_device_cus(&cus);
+    if (v != GEMM_F16_OK) return v;
+    gemm_f16_lowbit_plan_t plan;
+    v = w4_plan(M, N, K, group, cus, &plan);
+    if (v != GEMM_F16_OK) return v;
+    if (plan.workspace_bytes > (workspace ? workspace_bytes : 0)) return GEMM_F16_INVALID_ARG;
+    v = w4_decode(N, K, s, words, scales, workspace, stream);
+    if (v != GEMM_F16_OK) return v;
+    const int64_t used = round_up(N * K * 2, 256);
+    return gemm_f16_nt_splitk(M, N, K, A, workspace, C, 0, static_cast<char *>(workspace) + used,
+                              workspace_bytes - used, stream);
+}
+
+extern "C" int gemm_f16_q8_quantize(int64_t R, int64_t N, const void *X, void *codes,
+                                    void *scales, hipStream_t stream)
+{
+    Q8Shape s;
+    const int v = q8_shape(R, N, &s);
+    if (v != GEMM_F16_OK) return v;
+    const Array arrays[3] = {
+        {X, R * N * 2, 2, false}, {codes, s.codes, 16, true}, {scales, s.scales, 2, true}};
+    const int a = check_arrays(arrays, 3);
+    if (a != GEMM_F16_OK || s.codes == 0) return a;
+    return q8_launch(reinterpret_cast<const void *>(&q8_encode_kernel), R, N, s, X, nullptr, codes,
+                     scales, stream);
+}
+
+extern "C" int gemm_f16_q8_dequantize(int64_t R, int64_t N, const void *codes, const void *scales,
+                                      void *X, hipStream_t stream)
+{
+    Q8Shape s;
+    const int v = q8_shape(R, N, &s);
+    if (v != GEMM_F16_OK) return v;
+    const Array arrays[3] = {
+        {codes, s.codes, 16, false}, {scales, s.scales, 2, false}, {X, R * N * 2, 2, true}};
+    const int a = check_arrays(arrays, 3);
+    if (a != GEMM_F16_OK || s.codes == 0) return a;
+    return q8_launch(reinterpret_cast<const void *>(&q8_decode_kernel), R, N, s, nullptr, X, codes,
+                     scales, stream);
+}
+
+extern "C" int gemm_f16_tn_q8_plan(int64_t M, int64_t N, int64_t K, int32_t num_cus,
+                                   gemm_f16_lowbit_plan_t *plan)
+{
+    return plan ? q8_plan(M, N, K, num_cus, plan) : GEMM_F16_INVALID_ARG;
+}
+
+extern "C" int gemm_f16_tn_q8(int64_t M, int64_t N, int64_t K, const void *A, const void *codes,
+                              const void *scales, void *C, void *workspace,
+                              int64_t workspace_bytes, hipStream_t stream)
+{
+    Q8Shape s;
+    int v = q8_shape(K, N, &s);
+    if (v != GEMM_F16_OK) return v;
+    if (M < 0 || workspace_bytes < 0) return GEMM_F16_INVALID_ARG;
+    if (M > INT32_MAX) return GEMM_F16_UNSUPPORTED;
+    const Array arrays[5] = {{A, K * M * 2, 2, false},
+                             {codes, s.codes, 16, false},
+                             {scales, s.scales, 2, false},
+                             {C, M * N * 2, 2, true},
+                             {workspace, workspace ? workspace_bytes : 0, 256, true}};
+    v = check_arrays(arrays, 5);
+    if (v != GEMM_F16_OK || M == 0 || N == 0) return v;
+    if (K == 0) return gemm_f16_tn(M, N, 0, A, nullptr, C, stream);
+    int32_t cus = 0;
+    v = gemm_f16_device_cus(&cus);
+    if (v != GEMM_F16_OK) return v;
+    gemm_f16_lowbit_plan_t plan;
+    v = q8_plan(M, N, K, cus, &plan);
+    if (v != GEMM_F16_OK) return v;
+    if (plan.workspace_bytes > (workspace ? workspace_bytes : 0)) return GEMM_F16_INVALID_ARG;
+    v = q8_launch(reinterpret_cast<const void *>(&q8_decode_kernel), K, N, s, nullptr, workspace,
+                  codes, scales, stream);
+    if (v != GEMM_F16_OK) return v;
+    const int64_t used = round_up(N * K * 2, 256);
+    return gemm_f16_tn_splitk(M, N, K, A, workspace, C, 0, static_cast<char *>(workspace) + used,
+                              workspace_bytes - used, stream);
+}

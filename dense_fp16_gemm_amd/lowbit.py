@@ -1,0 +1,414 @@
+"""Products with one operand held in 4 or 8 bits (``include/gemm_f16_lowbit.h``).
+
+``W4Matrix``: a weight matrix in 4-bit codes with a scale for each group of
+32, 64 or 128 weights of a row; ``gemm_nt_w4(a, w)`` is a @ w.T from one row
+of a (one token) to long prompts.  ``Q8Matrix``: a matrix of activations in
+8-bit codes with a scale for each 32 values of a row, kept from the forward to
+the backward pass; ``gemm_tn_q8(dy, x)`` is dy.T @ x, a linear layer's weight
+gradient.
+
+As in the rest of the package, every arithmetic step runs in the library's HIP
+kernels and torch gives device memory and streams only.  Each function works
+on the current stream, or on `stream`: what it allocates then belongs to that
+stream, and the tensors passed in are recorded on it, so that the caller may
+drop them at once.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _check, _on_device, _stream_handle, gemm_f16_device_cus, load
+
+LOWBIT_DECODE = 0
+Q8_GROUP = 32
+W4_GROUPS = (32, 64, 128)
+
+
+class LowbitPlan(ctypes.Structure):
+    """What a low-bit product runs (gemm_f16_lowbit_plan_t)."""
+    _fields_ = [(name, ctypes.c_int32) for name in
+                ("kernel", "block_m", "block_n", "waves", "splits", "grid")] + \
+               [("workspace_bytes", ctypes.c_int64)]
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+def _declare(lib) -> None:
+    """Argument types of the functions of gemm_f16_lowbit.h."""
+    i64, i32, p = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
+    pi64, plan = ctypes.POINTER(i64), ctypes.POINTER(LowbitPlan)
+    for name, args in {
+        "gemm_f16_w4_sizes": [i64, i64, i32, pi64, pi64],
+        "gemm_f16_w4_quantize": [i64, i64, i32, p, p, p, p],
+        "gemm_f16_w4_pack": [i64, i64, i32, p, p, p, p, p],
+        "gemm_f16_w4_dequantize": [i64, i64, i32, p, p, p, p],
+        "gemm_f16_nt_w4_plan": [i64, i64, i64, i32, i32, plan],
+        "gemm_f16_nt_w4": [i64, i64, i64, i32, p, p, p, p, p, i64, p],
+        "gemm_f16_q8_quantize": [i64, i64, p, p, p, p],
+        "gemm_f16_q8_dequantize": [i64, i64, p, p, p, p],
+        "gemm_f16_tn_q8_plan": [i64, i64, i64, i32, plan],
+        "gemm_f16_tn_q8": [i64, i64, i64, p, p, p, p, p, i64, p],
+    }.items():
+        f = getattr(lib, name)
+        f.argtypes = args
+        f.restype = ctypes.c_int
+
+
+# ---- C ABI, same names -----------------------------------------------------
+def gemm_f16_w4_sizes(N: int, K: int, group: int) -> tuple[int, int]:
+    """(bytes of words, bytes of scales) of an [N, K] matrix in W4 storage."""
+    words, scales = ctypes.c_int64(), ctypes.c_int64()
+    _check(load().gemm_f16_w4_sizes(N, K, group, ctypes.byref(words), ctypes.byref(scales)),
+           "gemm_f16_w4_sizes")
+    return words.value, scales.value
+
+
+def gemm_f16_w4_quantize(N: int, K: int, group: int, W: int, words: int, scales: int,
+                         stream: int = 0) -> None:
+    _check(load().gemm_f16_w4_quantize(N, K, group, W, words, scales, stream),
+           "gemm_f16_w4_quantize")
+
+
+def gemm_f16_w4_pack(N: int, K: int, group: int, codes: int, in_scales: int, words: int,
+                     scales: int, stream: int = 0) -> None:
+    _check(load().gemm_f16_w4_pack(N, K, group, codes, in_scales, words, scales, stream),
+           "gemm_f16_w4_pack")
+
+
+def gemm_f16_w4_dequantize(N: int, K: int, group: int, words: int, scales: int, W: int,
+                           stream: int = 0) -> None:
+    _check(load().gemm_f16_w4_dequantize(N, K, group, words, scales, W, stream),
+           "gemm_f16_w4_dequantize")
+
+
+def gemm_f16_nt_w4_plan(M: int, N: int, K: int, group: int, num_cus: int) -> LowbitPlan:
+    plan = LowbitPlan()
+    _check(load().gemm_f16_nt_w4_plan(M, N, K, group, num_cus, ctypes.byref(plan)),
+           "gemm_f16_nt_w4_plan")
+    return plan
+
+
+def gemm_f16_nt_w4(M: int, N: int, K: int, group: int, A: int, words: int, scales: int, C: int,
+                   workspace: int = 0, workspace_bytes: int = 0, stream: int = 0) -> None:
+    _check(load().gemm_f16_nt_w4(M, N, K, group, A, words, scales, C, workspace, workspace_bytes,
+                                 stream), "gemm_f16_nt_w4")
+
+
+def gemm_f16_q8_quantize(R: int, N: int, X: int, codes: int, scales: int, stream: int = 0) -> None:
+    _check(load().gemm_f16_q8_quantize(R, N, X, codes, scales, stream), "gemm_f16_q8_quantize")
+
+
+def gemm_f16_q8_dequantize(R: int, N: int, codes: int, scales: int, X: int,
+                           stream: int = 0) -> None:
+    _check(load().gemm_f16_q8_dequantize(R, N, codes, scales, X, stream),
+           "gemm_f16_q8_dequantize")
+
+
+def gemm_f16_tn_q8_plan(M: int, N: int, K: int, num_cus: int) -> LowbitPlan:
+    plan = LowbitPlan()
+    _check(load().gemm_f16_tn_q8_plan(M, N, K, num_cus, ctypes.byref(plan)),
+           "gemm_f16_tn_q8_plan")
+    return plan
+
+
+def gemm_f16_tn_q8(M: int, N: int, K: int, A: int, codes: int, scales: int, C: int,
+                   workspace: int = 0, workspace_bytes: int = 0, stream: int = 0) -> None:
+    _check(load().gemm_f16_tn_q8(M, N, K, A, codes, scales, C, workspace, workspace_bytes, stream),
+           "gemm_f16_tn_q8")
+
+
+# ---- the two forms -----------------------------------------------------------
+class W4Matrix:
+    """An [n, k] matrix in W4 storage: words int32 [ceil(n / 16), ceil(k / 128),
+    64, 4] and scales fp16 [ceil(n / 16), 128 ceil(k / 128) / group, 16], as
+    quantize_w4() and pack_w4() make them.  The tensors are kept, not copied."""
+
+    __slots__ = ("words", "scales", "n", "k", "group")
+
+    def __init__(self, words, scales, n: int, k: int, group: int):
+        import torch
+
+        if group not in W4_GROUPS:
+            raise ValueError(f"group must be one of {W4_GROUPS}, not {group!r}")
+        if n < 0 or k < 0:
+            raise ValueError(f"negative size: n={n}, k={k}")
+        if words.dtype != torch.int32 or scales.dtype != torch.float16:
+            raise TypeError("words must be torch.int32 and scales torch.float16")
+        nb, kt = -(-n // 16), -(-k // 128)
+        if tuple(words.shape) != (nb, kt, 64, 4) or \
+                tuple(scales.shape) != (nb, 128 * kt // group, 16):
+            raise ValueError(f"words{tuple(words.shape)} and scales{tuple(scales.shape)} are not "
+                             f"those of a {n} x {k} matrix with groups of {group}")
+        if not words.is_cuda or words.device != scales.device:
+            raise ValueError("words and scales must be on the same GPU")
+        if not (words.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("words and scales must be contiguous")
+        self.words, self.scales = words, scales
+        self.n, self.k, self.group = int(n), int(k), int(group)
+
+    @property
+    def shape(self) -> tuple[int, int]:
+        return self.n, self.k
+
+    @property
+    def device(self):
+        return self.words.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.words.numel() * 4 + self.scales.numel() * 2
+
+    def __repr__(self) -> str:
+        return f"W4Matrix({self.n} x {self.k}, group={self.group}, device={self.device})"
+
+
+class Q8Matrix:
+    """An [r, n] matrix in Q8 storage: codes int8 [r, 32 ceil(n / 32)] and
+    scales fp16 [r, ceil(n / 32)], as quantize_q8() makes them.  The tensors
+    are kept, not copied; a range of rows of both is a Q8Matrix too."""
+
+    __slots__ = ("codes", "scales", "r", "n")
+
+    def __init__(self, codes, scales, n: int):
+        import torch
+
+        if n < 0:
+            raise ValueError(f"negative size: n={n}")
+        if codes.dtype != torch.int8 or scales.dtype != torch.float16:
+            raise TypeError("codes must be torch.int8 and scales torch.float16")
+        groups = -(-n // Q8_GROUP)
+        if codes.dim() != 2 or codes.shape[1] != Q8_GROUP * groups or \
+                tuple(scales.shape) != (codes.shape[0], groups):
+            raise ValueError(f"codes{tuple(codes.shape)} and scales{tuple(scales.shape)} are not "
+                             f"those of a matrix with {n} columns")
+        if not codes.is_cuda or codes.device != scales.device:
+            raise ValueError("codes and scales must be on the same GPU")
+        if not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous")
+        self.codes, self.scales = codes, scales
+        self.r, self.n = int(codes.shape[0]), int(n)
+
+    @property
+    def shape(self) -> tuple[int, int]:
+        return self.r, self.n
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel() * 2
+
+    def __repr__(self) -> str:
+        return f"Q8Matrix({self.r} x {self.n}, device={self.device})"
+
+
+# ---- torch convenience -------------------------------------------------------
+def _matrix(x, dtype, what: str):
+    if x.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{what} must be a matrix")
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be on a GPU")
+    if not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous (row-major)")
+    return x.shape
+
+
+def _check_stream(stream, device) -> None:
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory that belongs to the stream it will be used on."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _record(stream, *tensors) -> None:
+    """Tensors of other streams, used on `stream`: not to be reused before it is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _output(out, shape, device, stream):
+    import torch
+
+    if out is None:
+        return _empty(shape, torch.float16, device, stream)
+    if out.dtype != torch.float16 or tuple(out.shape) != tuple(shape) or \
+            not out.is_contiguous() or out.device != device:
+        raise ValueError(f"out must be a contiguous float16 {list(shape)} tensor on {device}")
+    return out
+
+
+def _empty_w4(n: int, k: int, group: int, device, stream):
+    import torch
+
+    if group not in W4_GROUPS:
+        raise ValueError(f"group must be one of {W4_GROUPS}, not {group!r}")
+    nb, kt = -(-n // 16), -(-k // 128)
+    return W4Matrix(_empty((nb, kt, 64, 4), torch.int32, device, stream),
+                    _empty((nb, 128 * kt // group, 16), torch.float16, device, stream), n, k, group)
+
+
+def quantize_w4(w, group: int = 128, stream=None) -> W4Matrix:
+    """w [N, K] fp16 in 4-bit codes, a scale for each `group` weights of a row."""
+    import torch
+
+    n, k = _matrix(w, torch.float16, "w")
+    _check_stream(stream, w.device)
+    q = _empty_w4(n, k, group, w.device, stream)
+    with _on_device(w):
+        gemm_f16_w4_quantize(n, k, group, w.data_ptr(), q.words.data_ptr(), q.scales.data_ptr(),
+                             _stream_handle(w, stream))
+    _record(stream, w)
+    return q
+
+
+def pack_w4(codes, scales, group: int = 128, stream=None) -> W4Matrix:
+    """A W4Matrix from another quantiser's codes [N, K] int8 in -8..7 and scales
+    [N, ceil(K / group)] fp16, weight = code * scale.  Scales are rounded to 8
+    significant bits; a group that cannot be held (a code out of range, a scale
+    that is not finite, a weight past 65504) becomes NaN."""
+    import torch
+
+    n, k = _matrix(codes, torch.int8, "codes")
+    _check_stream(stream, codes.device)
+    q = _empty_w4(n, k, group, codes.device, stream)
+    if tuple(_matrix(scales, torch.float16, "scales")) != (n, -(-k // group)):
+        raise ValueError(f"scales{tuple(scales.shape)} do not fit codes{tuple(codes.shape)} in "
+                         f"groups of {group}")
+    if scales.device != codes.device:
+        raise ValueError("codes and scales must be on the same GPU")
+    with _on_device(codes):
+        gemm_f16_w4_pack(n, k, group, codes.data_ptr(), scales.data_ptr(), q.words.data_ptr(),
+                         q.scales.data_ptr(), _stream_handle(codes, stream))
+    _record(stream, codes, scales)
+    return q
+
+
+def dequantize_w4(w: W4Matrix, out=None, stream=None):
+    """The [n, k] fp16 matrix that w stands for, exactly."""
+    if not isinstance(w, W4Matrix):
+        raise TypeError("w must be a W4Matrix")
+    _check_stream(stream, w.device)
+    out = _output(out, (w.n, w.k), w.device, stream)
+    with _on_device(w.words):
+        gemm_f16_w4_dequantize(w.n, w.k, w.group, w.words.data_ptr(), w.scales.data_ptr(),
+                               out.data_ptr(), _stream_handle(w.words, stream))
+    _record(stream, w.words, w.scales, out)
+    return out
+
+
+def quantize_q8(x, stream=None) -> Q8Matrix:
+    """x [R, N] fp16 in 8-bit codes, a scale for each 32 values of a row."""
+    import torch
+
+    r, n = _matrix(x, torch.float16, "x")
+    _check_stream(stream, x.device)
+    groups = -(-n // Q8_GROUP)
+    q = Q8Matrix(_empty((r, groups * Q8_GROUP), torch.int8, x.device, stream),
+                 _empty((r, groups), torch.float16, x.device, stream), n)
+    with _on_device(x):
+        gemm_f16_q8_quantize(r, n, x.data_ptr(), q.codes.data_ptr(), q.scales.data_ptr(),
+                             _stream_handle(x, stream))
+    _record(stream, x)
+    return q
+
+
+def dequantize_q8(x: Q8Matrix, out=None, stream=None):
+    """The [r, n] fp16 matrix that x stands for, exactly."""
+    if not isinstance(x, Q8Matrix):
+        raise TypeError("x must be a Q8Matrix")
+    _check_stream(stream, x.device)
+    out = _output(out, (x.r, x.n), x.device, stream)
+    with _on_device(x.codes):
+        gemm_f16_q8_dequantize(x.r, x.n, x.codes.data_ptr(), x.scales.data_ptr(), out.data_ptr(),
+                               _stream_handle(x.codes, stream))
+    _record(stream, x.codes, x.scales, out)
+    return out
+
+
+# workspace bytes of a product, per (kind, sizes, device): a repeated call
+# costs a dictionary lookup
+_workspace_bytes: dict = {}
+
+
+def _workspace(plan, key, on, workspace, stream):
+    """(tensor or None, its bytes) for a product planned by plan(*key[1:-1], num_cus)."""
+    import torch
+
+    need = _workspace_bytes.get(key)
+    if need is None:
+        with _on_device(on):
+            need = plan(*key[1:-1], gemm_f16_device_cus()).workspace_bytes
+        if len(_workspace_bytes) >= 1024:
+            _workspace_bytes.clear()
+        _workspace_bytes[key] = need
+    if workspace is None:
+        return (_empty(need, torch.uint8, on.device, stream), need) if need else (None, 0)
+    if not workspace.is_cuda or workspace.device != on.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the operands' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def gemm_nt_w4(a, w: W4Matrix, out=None, workspace=None, stream=None):
+    """C = a @ W.T for a [M, K] fp16 and W [N, K] in 4 bits, fp16 [M, N]
+    (gemm_f16_nt_w4).  The workspace that some sizes need (see
+    gemm_f16_nt_w4_plan) is allocated with torch unless `workspace` is given."""
+    import torch
+
+    if not isinstance(w, W4Matrix):
+        raise TypeError("w must be a W4Matrix")
+    m, k = _matrix(a, torch.float16, "a")
+    if k != w.k:
+        raise ValueError(f"shape mismatch: a{tuple(a.shape)} w{w.shape}")
+    if a.device != w.device:
+        raise ValueError("a and w must be on the same GPU")
+    _check_stream(stream, a.device)
+    out = _output(out, (m, w.n), a.device, stream)
+    ws, ws_bytes = _workspace(gemm_f16_nt_w4_plan, ("w4", m, w.n, k, w.group, a.get_device()), a,
+                              workspace, stream)
+    with _on_device(a):
+        gemm_f16_nt_w4(m, w.n, k, w.group, a.data_ptr(), w.words.data_ptr(), w.scales.data_ptr(),
+                       out.data_ptr(), ws.data_ptr() if ws is not None else 0, ws_bytes,
+                       _stream_handle(a, stream))
+    _record(stream, a, w.words, w.scales, out, ws)
+    return out
+
+
+def gemm_tn_q8(a, x: Q8Matrix, out=None, workspace=None, stream=None):
+    """C = a.T @ X for a [K, M] fp16 and X [K, N] in 8 bits, fp16 [M, N]
+    (gemm_f16_tn_q8): with a the gradient of a linear layer's output and X its
+    kept input, the gradient of its [M, N] weight.  Workspace as for
+    gemm_nt_w4."""
+    import torch
+
+    if not isinstance(x, Q8Matrix):
+        raise TypeError("x must be a Q8Matrix")
+    k, m = _matrix(a, torch.float16, "a")
+    if k != x.r:
+        raise ValueError(f"shape mismatch: a{tuple(a.shape)} x{x.shape}")
+    if a.device != x.device:
+        raise ValueError("a and x must be on the same GPU")
+    _check_stream(stream, a.device)
+    out = _output(out, (m, x.n), a.device, stream)
+    ws, ws_bytes = _workspace(gemm_f16_tn_q8_plan, ("q8", m, x.n, k, a.get_device()), a, workspace,
+                              stream)
+    with _on_device(a):
+        gemm_f16_tn_q8(m, x.n, k, a.data_ptr(), x.codes.data_ptr(), x.scales.data_ptr(),
+                       out.data_ptr(), ws.data_ptr() if ws is not None else 0, ws_bytes,
+                       _stream_handle(a, stream))
+    _record(stream, a, x.codes, x.scales, out, ws)
+    return out
