@@ -16,6 +16,7 @@ typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 // 16 bytes at any 2-byte alignment (the target's unaligned-access mode)
 typedef _Float16 half8_u_t __attribute__((ext_vector_type(8), aligned(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
@@ -268,6 +269,152 @@ __global__ __launch_bounds__(64 * WAVES) void w4_decode_kernel(W4DecodeParams p)
             const _Float16 sj = bits_as<_Float16>(s[((32 * j) >> p.shift) * 16]);
             if (c < p.K) store8(p.W + n * p.K, static_cast<int32_t>(c), p.K, w4_scaled(w[j], sj));
         }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// C = A W^T for at most 16 rows of A: the words streamed through registers
+// ---------------------------------------------------------------------------
+// One workgroup computes NB blocks of 16 columns of C (rows of W).  Its waves
+// take the blocks' tiles in turn (wave w the tiles w, w + W, ..: together they
+// read each block's words front to back) and add up their sums in LDS at the
+// end, so a small N still puts W waves' loads in flight on each CU, and no sum
+// crosses a workgroup.  HBM bounds it: a tile's KB is one load for each lane.
+//
+// The MFMA's rows are rows of W, straight from the words; its 16 columns are
+// rows of A.  With few rows those columns would stand empty while the loads of
+// A, a KB for each 32 columns of k whatever M is, cost four times the words'
+// own.  So MC = 16 / JC columns are rows of A, and JC sets of them hold the
+// fragments of JC different steps j of the tile: one load brings them all.
+// Each of the JC accumulators multiplies the words of its own step with the
+// whole register, and of its results only the columns of that step are used.
+struct W4Params {
+    const uint16_t *A;
+    const u32x4_t *words;
+    const uint16_t *scales;
+    uint16_t *C;
+    int32_t M, N, K, kt, nb;   // kt: tiles of 128 columns, nb: blocks of 16 rows of W
+};
+
+template <int SH, int JC, int NB, int W, int D>
+__global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
+{
+    constexpr int MC = 16 / JC;      // rows of A
+    constexpr int AL = 4 / JC;       // loads of A a tile
+    constexpr int NS = 128 >> SH;    // scales a tile and row
+    __shared__ float red[W][NB][16][20];   // 20: rows of 16 sums apart in the banks
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
+    const int r = lane & 15, kq = lane >> 4;
+    const int m = r & (MC - 1), jj = r / MC;
+    const int32_t b0 = blockIdx.x * NB;
+    const uint16_t *arow = p.A + static_cast<int64_t>(m < p.M ? m : 0) * p.K + 32 * jj + 8 * kq;
+    const u32x4_t *words[NB];
+    const uint16_t *scales[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int64_t b = b0 + nb < p.nb ? b0 + nb : p.nb - 1;   // the last again: not stored
+        words[nb] = p.words + b * p.kt * 64 + lane;
+        scales[nb] = p.scales + b * p.kt * NS * 16 + r;
+    }
+    f32x4_t acc[NB][JC] = {};
+    u32x4_t wv[2][D][NB];
+    half8_t af[2][D][AL];
+    _Float16 sc[2][D][NB][NS];
+    auto load_w = [&](int buf, int d, int64_t t) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            wv[buf][d][nb] = __builtin_nontemporal_load(words[nb] + t * 64);
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+                sc[buf][d][nb][s] = bits_as<_Float16>(scales[nb][(t * NS + s) * 16]);
+        }
+    };
+    auto load = [&](int buf, int d, int64_t t) {
+        load_w(buf, d, t);
+#pragma unroll
+        for (int i = 0; i < AL; ++i)
+            af[buf][d][i] = *reinterpret_cast<const half8_u_t *>(arow + t * 128 + 32 * JC * i);
+    };
+    auto mma = [&](int buf, int d) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[nb][j % JC] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    w4_scaled(wv[buf][d][nb][j], sc[buf][d][nb][(32 * j) >> SH]), af[buf][d][j / JC],
+                    acc[nb][j % JC], 0, 0, 0);
+    };
+    // whole tiles, in two buffers of D: one's loads fly while the other's are
+    // multiplied.  Loads are unconditional (past the end the last tile again),
+    // so that the waits on one buffer leave the other's in flight.
+    const int32_t full = p.K / 128;
+    const int32_t count = full > wave ? (full - wave + W - 1) / W : 0;
+    auto at = [&](int32_t i) { return static_cast<int64_t>(wave) + static_cast<int64_t>(i < count ? i : count - 1) * W; };
+    if (count > 0) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(0, d, at(d));
+        int32_t i = 0;
+        for (; i + 2 * D <= count; i += 2 * D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) load(1, d, at(i + D + d));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int d = 0; d < D; ++d) mma(0, d);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int d = 0; d < D; ++d) load(0, d, at(i + 2 * D + d));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int d = 0; d < D; ++d) mma(1, d);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // fewer than 2 D left: those of buffer 0 first
+        if (i + D < count) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) load(1, d, at(i + D + d));
+        }
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (i + d < count) mma(0, d);
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (i + D + d < count) mma(1, d);
+    }
+    // the tile that K ends in: columns past K are zeros
+    if (full < p.kt && full % W == wave) {
+        load_w(0, 0, full);
+#pragma unroll
+        for (int i = 0; i < AL; ++i) {
+            const int64_t c = static_cast<int64_t>(full) * 128 + 32 * (jj + JC * i) + 8 * kq;
+            af[0][0][i] = half8_t{};
+            if (c < p.K)
+                af[0][0][i] = bits_as<half8_t>(load8(p.A + static_cast<int64_t>(m < p.M ? m : 0) * p.K,
+                                                     static_cast<int32_t>(c), p.K));
+        }
+        mma(0, 0);
+    }
+    // lane l holds rows 4 (l / 16) .. + 3 of the block and column l % 16
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        f32x4_t v = acc[nb][0];
+#pragma unroll
+        for (int j = 1; j < JC; ++j)
+            if (jj == j) v = acc[nb][j];
+        *reinterpret_cast<f32x4_t *>(&red[wave][nb][r][kq * 4]) = v;
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < NB * MC * 16; o += 64 * W) {
+        const int n = o & 15, mm = (o >> 4) & (MC - 1), nb = o / (16 * MC);
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int j = 0; j < JC; ++j) sum += red[w][nb][j * MC + mm][n];
+        const int64_t col = static_cast<int64_t>(b0 + nb) * 16 + n;
+        if (mm < p.M && col < p.N)
+            reinterpret_cast<_Float16 *>(p.C)[static_cast<int64_t>(mm) * p.N + col] =
+                static_cast<_Float16>(sum);
     }
 }
 
@@ -550,6 +697,33 @@ static int decode_plan(int64_t M, int64_t N, int64_t K, int32_t num_cus, bool tn
     return GEMM_F16_OK;
 }
 
+// The kernels of the product with 4-bit weights that read the words directly,
+// for each group size.
+struct W4Kernel {
+    int32_t kernel, rows, blocks, waves;   // rows of A, blocks of 16 rows of W a workgroup
+    const void *fn[3];                     // group 32, 64, 128
+};
+#define W4_STREAM(JC, NB, W, D)                                                       \
+    W4Kernel{GEMM_F16_LOWBIT_STREAM, 16 / JC, NB, W,                                  \
+             {reinterpret_cast<const void *>(&w4_stream_kernel<5, JC, NB, W, D>),     \
+              reinterpret_cast<const void *>(&w4_stream_kernel<6, JC, NB, W, D>),     \
+              reinterpret_cast<const void *>(&w4_stream_kernel<7, JC, NB, W, D>)}}
+static const W4Kernel kW4Kernels[] = {
+    W4_STREAM(4, 1, 8, 2), W4_STREAM(2, 1, 8, 1), W4_STREAM(2, 2, 8, 1),
+};
+#undef W4_STREAM
+
+// The index into kW4Kernels, or -1: decode.
+static int w4_choose(int64_t M, int64_t N, int32_t cus)
+{
+    if (M <= 4) return 0;
+    // two blocks a workgroup halve the loads of A, where that still gives
+    // every CU a workgroup (8 x 4096 x 14336: 10.3 us with one block, 13.0
+    // with two; 8 x 16384 x 16384: 38.3 and 28.8)
+    if (M <= 8) return cdiv(N, 16) >= 2 * cus ? 2 : 1;
+    return -1;
+}
+
 static int w4_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t num_cus,
                    gemm_f16_lowbit_plan_t *plan)
 {
@@ -561,7 +735,15 @@ static int w4_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t num_c
     *plan = gemm_f16_lowbit_plan_t{};
     plan->splits = 1;
     if (M == 0 || N == 0 || K == 0) return GEMM_F16_OK;
-    return decode_plan(M, N, K, num_cus, false, plan);
+    const int id = w4_choose(M, N, num_cus);
+    if (id < 0) return decode_plan(M, N, K, num_cus, false, plan);
+    const W4Kernel &e = kW4Kernels[id];
+    plan->kernel = e.kernel;
+    plan->block_m = e.rows;
+    plan->block_n = 16 * e.blocks;
+    plan->waves = e.waves;
+    plan->grid = static_cast<int32_t>(cdiv(s.nb, e.blocks));
+    return GEMM_F16_OK;
 }
 
 static int q8_plan(int64_t M, int64_t N, int64_t K, int32_t num_cus, gemm_f16_lowbit_plan_t *plan)
@@ -653,6 +835,20 @@ extern "C" int gemm_f16_nt_w4(int64_t M, int64_t N, int64_t K, int32_t group, co
     v = w4_plan(M, N, K, group, cus, &plan);
     if (v != GEMM_F16_OK) return v;
     if (plan.workspace_bytes > (workspace ? workspace_bytes : 0)) return GEMM_F16_INVALID_ARG;
+    if (plan.kernel == GEMM_F16_LOWBIT_STREAM) {
+        W4Params p;
+        p.A = static_cast<const uint16_t *>(A);
+        p.words = static_cast<const u32x4_t *>(words);
+        p.scales = static_cast<const uint16_t *>(scales);
+        p.C = static_cast<uint16_t *>(C);
+        p.M = static_cast<int32_t>(M);
+        p.N = static_cast<int32_t>(N);
+        p.K = static_cast<int32_t>(K);
+        p.kt = static_cast<int32_t>(s.kt);
+        p.nb = static_cast<int32_t>(s.nb);
+        const W4Kernel &e = kW4Kernels[w4_choose(M, N, cus)];
+        return launch(e.fn[s.shift - 5], plan.grid, 64 * e.waves, &p, stream);
+    }
     v = w4_decode(N, K, s, words, scales, workspace, stream);
     if (v != GEMM_F16_OK) return v;
     const int64_t used = round_up(N * K * 2, 256);

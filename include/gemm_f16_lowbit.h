@@ -95,7 +95,10 @@ int gemm_f16_w4_dequantize(int64_t N, int64_t K, int32_t group, const void *word
 enum {
     /* the operand is written out in fp16 into the workspace and the library's
      * fp16 GEMM (with its own split over K) runs on it */
-    GEMM_F16_LOWBIT_DECODE = 0
+    GEMM_F16_LOWBIT_DECODE = 0,
+    /* the codes go from memory to the matrix units through registers, one
+     * pass, no workspace */
+    GEMM_F16_LOWBIT_STREAM = 1
 };
 typedef struct {
     int32_t kernel;           /* one of the values above                      */
