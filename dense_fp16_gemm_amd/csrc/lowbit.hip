@@ -279,15 +279,10 @@ __global__ __launch_bounds__(64 * WAVES) void w4_decode_kernel(W4DecodeParams p)
 // take the blocks' tiles in turn (wave w the tiles w, w + W, ..: together they
 // read each block's words front to back) and add up their sums in LDS at the
 // end, so a small N still puts W waves' loads in flight on each CU, and no sum
-// crosses a workgroup.  HBM bounds it: a tile's KB is one load for each lane.
-//
-// The MFMA's rows are rows of W, straight from the words; its 16 columns are
-// rows of A.  With few rows those columns would stand empty while the loads of
-// A, a KB for each 32 columns of k whatever M is, cost four times the words'
-// own.  So MC = 16 / JC columns are rows of A, and JC sets of them hold the
-// fragments of JC different steps j of the tile: one load brings them all.
-// Each of the JC accumulators multiplies the words of its own step with the
-// whole register, and of its results only the columns of that step are used.
+// crosses a workgroup.  The MFMA's rows are rows of W, straight from the words;
+// its 16 columns are rows of A.  HBM bounds it (a tile's KB is one load for
+// each lane), and next the loads of A, a KB of lanes' data for four rows of a
+// tile: the two kernels differ in how they keep those few.
 struct W4Params {
     const uint16_t *A;
     const u32x4_t *words;
@@ -296,6 +291,78 @@ struct W4Params {
     int32_t M, N, K, kt, nb;   // kt: tiles of 128 columns, nb: blocks of 16 rows of W
 };
 
+// Sums of the waves (W x JC sets of them) in order, rounded once.
+template <int NB, int W, int JC>
+__device__ __forceinline__ void w4_join_waves(const W4Params &p, int32_t b0,
+                                              const float (*red)[NB][16][20])
+{
+    constexpr int MC = 16 / JC;
+    __syncthreads();
+    for (int o = threadIdx.x; o < NB * MC * 16; o += 64 * W) {
+        const int n = o & 15, m = (o >> 4) & (MC - 1), nb = o / (16 * MC);
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int j = 0; j < JC; ++j) sum += red[w][nb][j * MC + m][n];
+        const int64_t col = static_cast<int64_t>(b0 + nb) * 16 + n;
+        if (m < p.M && col < p.N)
+            reinterpret_cast<_Float16 *>(p.C)[static_cast<int64_t>(m) * p.N + col] =
+                static_cast<_Float16>(sum);
+    }
+}
+
+// Runs a wave's whole tiles in two buffers of D: one's loads fly while the
+// other's are multiplied.  Loads are unconditional (past the end the last tile
+// again), so that the waits on one buffer leave the other's in flight.
+template <int W, int D, class Load, class Mma>
+__device__ __forceinline__ void w4_run_tiles(int32_t full, int wave, Load load, Mma mma)
+{
+    const int32_t count = full > wave ? (full - wave + W - 1) / W : 0;
+    auto at = [&](int32_t i) {
+        return static_cast<int64_t>(wave) + static_cast<int64_t>(i < count ? i : count - 1) * W;
+    };
+    if (count == 0) return;
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(0, d, at(d));
+    int32_t i = 0;
+    for (; i + 2 * D <= count; i += 2 * D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(1, d, at(i + D + d));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = 0; d < D; ++d) mma(0, d);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(0, d, at(i + 2 * D + d));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int d = 0; d < D; ++d) mma(1, d);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // fewer than 2 D left: those of buffer 0 first
+    if (i + D < count) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(1, d, at(i + D + d));
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (i + d < count) mma(0, d);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (i + D + d < count) mma(1, d);
+}
+
+// At most 16 / JC rows of A.  With so few the MFMA's columns would stand empty
+// while the loads of A cost four times the words' own.  So MC = 16 / JC
+// columns are rows of A, and JC sets of them hold the fragments of JC
+// different steps j of the tile: one load brings them all.  Each of the JC
+// accumulators multiplies the words of its own step with the whole register,
+// and of its results only the columns of that step are used.
+//
+// JC = 4, eight waves with two tiles a buffer: 1 x 4096 x 14336 takes 8.0 us
+// from HBM (2.3 us of it an empty kernel's), 1 x 16384 x 16384 25.2 us (5.3
+// TB/s); one tile a buffer 9.1 and 27.1, four 9.8 and 35.6.
 template <int SH, int JC, int NB, int W, int D>
 __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
 {
@@ -308,7 +375,8 @@ __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
     const int r = lane & 15, kq = lane >> 4;
     const int m = r & (MC - 1), jj = r / MC;
     const int32_t b0 = blockIdx.x * NB;
-    const uint16_t *arow = p.A + static_cast<int64_t>(m < p.M ? m : 0) * p.K + 32 * jj + 8 * kq;
+    const uint16_t *row = p.A + static_cast<int64_t>(m < p.M ? m : 0) * p.K;
+    const uint16_t *arow = row + 32 * jj + 8 * kq;
     const u32x4_t *words[NB];
     const uint16_t *scales[NB];
 #pragma unroll
@@ -342,45 +410,11 @@ __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc[nb][j % JC] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    w4_scaled(wv[buf][d][nb][j], sc[buf][d][nb][(32 * j) >> SH]), af[buf][d][j / JC],
-                    acc[nb][j % JC], 0, 0, 0);
+                    w4_scaled(wv[buf][d][nb][j], sc[buf][d][nb][(32 * j) >> SH]),
+                    af[buf][d][j / JC], acc[nb][j % JC], 0, 0, 0);
     };
-    // whole tiles, in two buffers of D: one's loads fly while the other's are
-    // multiplied.  Loads are unconditional (past the end the last tile again),
-    // so that the waits on one buffer leave the other's in flight.
     const int32_t full = p.K / 128;
-    const int32_t count = full > wave ? (full - wave + W - 1) / W : 0;
-    auto at = [&](int32_t i) { return static_cast<int64_t>(wave) + static_cast<int64_t>(i < count ? i : count - 1) * W; };
-    if (count > 0) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) load(0, d, at(d));
-        int32_t i = 0;
-        for (; i + 2 * D <= count; i += 2 * D) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) load(1, d, at(i + D + d));
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int d = 0; d < D; ++d) mma(0, d);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int d = 0; d < D; ++d) load(0, d, at(i + 2 * D + d));
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int d = 0; d < D; ++d) mma(1, d);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        // fewer than 2 D left: those of buffer 0 first
-        if (i + D < count) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) load(1, d, at(i + D + d));
-        }
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-            if (i + d < count) mma(0, d);
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-            if (i + D + d < count) mma(1, d);
-    }
+    w4_run_tiles<W, D>(full, wave, load, mma);
     // the tile that K ends in: columns past K are zeros
     if (full < p.kt && full % W == wave) {
         load_w(0, 0, full);
@@ -388,9 +422,7 @@ __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
         for (int i = 0; i < AL; ++i) {
             const int64_t c = static_cast<int64_t>(full) * 128 + 32 * (jj + JC * i) + 8 * kq;
             af[0][0][i] = half8_t{};
-            if (c < p.K)
-                af[0][0][i] = bits_as<half8_t>(load8(p.A + static_cast<int64_t>(m < p.M ? m : 0) * p.K,
-                                                     static_cast<int32_t>(c), p.K));
+            if (c < p.K) af[0][0][i] = bits_as<half8_t>(load8(row, static_cast<int32_t>(c), p.K));
         }
         mma(0, 0);
     }
@@ -403,19 +435,93 @@ __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
             if (jj == j) v = acc[nb][j];
         *reinterpret_cast<f32x4_t *>(&red[wave][nb][r][kq * 4]) = v;
     }
-    __syncthreads();
-    for (int o = threadIdx.x; o < NB * MC * 16; o += 64 * W) {
-        const int n = o & 15, mm = (o >> 4) & (MC - 1), nb = o / (16 * MC);
-        float sum = 0.0f;
+    w4_join_waves<NB, W, JC>(p, b0, red);
+}
+
+// At most 4 RL rows of A.  Loads of A in the MFMA's own layout touch 64 bytes
+// of each of 16 rows, and at 16 rows they, not the words, bound the kernel (16
+// x 4096 x 14336: 16.4 us).  Here each load covers 256 bytes of four rows, and
+// the wave turns the tile round in LDS of its own, with the 16-byte chunks of
+// row r XORed with r to spread the reads over the banks: 12.3 us, and 5.4 us
+// against 6.9 at K = 4096.  Several blocks a workgroup use the rows of A more
+// than once, where N still gives nearly every CU a workgroup (16 x 16384 x
+// 16384: 45 us with one, 33 with two, 29.2 with four; 16 x 4096 x 14336: 12.5,
+// 14.9, 22.5).
+template <int SH, int RL, int NB, int W>
+__global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
+{
+    constexpr int NS = 128 >> SH;
+    __shared__ float red[W][NB][16][20];
+    __shared__ half8_t abuf[W][RL * 4][16];
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
+    const int r = lane & 15, kq = lane >> 4;
+    const int32_t b0 = blockIdx.x * NB;
+    const uint16_t *arow[RL];
 #pragma unroll
-        for (int w = 0; w < W; ++w)
+    for (int i = 0; i < RL; ++i)
+        arow[i] = p.A + static_cast<int64_t>(min(4 * i + kq, p.M - 1)) * p.K;
+    half8_t *ab = abuf[wave][0];
+    const u32x4_t *words[NB];
+    const uint16_t *scales[NB];
 #pragma unroll
-            for (int j = 0; j < JC; ++j) sum += red[w][nb][j * MC + mm][n];
-        const int64_t col = static_cast<int64_t>(b0 + nb) * 16 + n;
-        if (mm < p.M && col < p.N)
-            reinterpret_cast<_Float16 *>(p.C)[static_cast<int64_t>(mm) * p.N + col] =
-                static_cast<_Float16>(sum);
+    for (int nb = 0; nb < NB; ++nb) {
+        const int64_t b = b0 + nb < p.nb ? b0 + nb : p.nb - 1;
+        words[nb] = p.words + b * p.kt * 64 + lane;
+        scales[nb] = p.scales + b * p.kt * NS * 16 + r;
     }
+    f32x4_t acc[NB] = {};
+    u32x4_t wv[2][NB];
+    half8_t af[2][RL];
+    _Float16 sc[2][NB][NS];
+    auto load_w = [&](int buf, int64_t t) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            wv[buf][nb] = __builtin_nontemporal_load(words[nb] + t * 64);
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+                sc[buf][nb][s] = bits_as<_Float16>(scales[nb][(t * NS + s) * 16]);
+        }
+    };
+    auto load = [&](int buf, int, int64_t t) {
+        load_w(buf, t);
+#pragma unroll
+        for (int i = 0; i < RL; ++i)
+            af[buf][i] = *reinterpret_cast<const half8_u_t *>(arow[i] + t * 128 + 8 * r);
+    };
+    // columns past 4 RL repeat the last row, like rows past M: not stored
+    const int rr = r < RL * 4 ? r : RL * 4 - 1;
+    auto mma = [&](int buf, int) {
+        half8_t a[4];
+        // the wave alone uses these 4 RL rows, and its LDS operations keep
+        // their order
+#pragma unroll
+        for (int i = 0; i < RL; ++i) ab[(4 * i + kq) * 16 + (r ^ (4 * i + kq))] = af[buf][i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = ab[rr * 16 + ((4 * j + kq) ^ rr)];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    w4_scaled(wv[buf][nb][j], sc[buf][nb][(32 * j) >> SH]), a[j], acc[nb], 0, 0, 0);
+    };
+    const int32_t full = p.K / 128;
+    w4_run_tiles<W, 1>(full, wave, load, mma);
+    if (full < p.kt && full % W == wave) {
+        load_w(0, full);
+#pragma unroll
+        for (int i = 0; i < RL; ++i) {
+            const int64_t c = static_cast<int64_t>(full) * 128 + 8 * r;
+            af[0][i] = half8_t{};
+            if (c < p.K) af[0][i] = bits_as<half8_t>(load8(arow[i], static_cast<int32_t>(c), p.K));
+        }
+        mma(0, 0);
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+        *reinterpret_cast<f32x4_t *>(&red[wave][nb][r][kq * 4]) = acc[nb];
+    w4_join_waves<NB, W, 1>(p, b0, red);
 }
 
 // ---------------------------------------------------------------------------
@@ -703,24 +809,30 @@ struct W4Kernel {
     int32_t kernel, rows, blocks, waves;   // rows of A, blocks of 16 rows of W a workgroup
     const void *fn[3];                     // group 32, 64, 128
 };
+#define W4_KERNEL(KIND, ROWS, NB, W, K5, K6, K7)                                      \
+    W4Kernel{KIND, ROWS, NB, W,                                                       \
+             {reinterpret_cast<const void *>(&K5), reinterpret_cast<const void *>(&K6), \
+              reinterpret_cast<const void *>(&K7)}}
 #define W4_STREAM(JC, NB, W, D)                                                       \
-    W4Kernel{GEMM_F16_LOWBIT_STREAM, 16 / JC, NB, W,                                  \
-             {reinterpret_cast<const void *>(&w4_stream_kernel<5, JC, NB, W, D>),     \
-              reinterpret_cast<const void *>(&w4_stream_kernel<6, JC, NB, W, D>),     \
-              reinterpret_cast<const void *>(&w4_stream_kernel<7, JC, NB, W, D>)}}
+    W4_KERNEL(GEMM_F16_LOWBIT_STREAM, 16 / JC, NB, W, (w4_stream_kernel<5, JC, NB, W, D>), \
+              (w4_stream_kernel<6, JC, NB, W, D>), (w4_stream_kernel<7, JC, NB, W, D>))
+#define W4_ROWS(RL, NB, W)                                                            \
+    W4_KERNEL(GEMM_F16_LOWBIT_STREAM, 4 * RL, NB, W, (w4_rows_kernel<5, RL, NB, W>),  \
+              (w4_rows_kernel<6, RL, NB, W>), (w4_rows_kernel<7, RL, NB, W>))
 static const W4Kernel kW4Kernels[] = {
-    W4_STREAM(4, 1, 8, 2), W4_STREAM(2, 1, 8, 1), W4_STREAM(2, 2, 8, 1),
+    W4_STREAM(4, 1, 8, 2),
+    W4_ROWS(2, 1, 8), W4_ROWS(2, 2, 8),
+    W4_ROWS(4, 1, 8), W4_ROWS(4, 2, 8), W4_ROWS(4, 4, 8),
 };
-#undef W4_STREAM
 
 // The index into kW4Kernels, or -1: decode.
-static int w4_choose(int64_t M, int64_t N, int32_t cus)
+static int w4_choose(int64_t M, int64_t nb, int32_t cus)
 {
     if (M <= 4) return 0;
-    // two blocks a workgroup halve the loads of A, where that still gives
-    // every CU a workgroup (8 x 4096 x 14336: 10.3 us with one block, 13.0
-    // with two; 8 x 16384 x 16384: 38.3 and 28.8)
-    if (M <= 8) return cdiv(N, 16) >= 2 * cus ? 2 : 1;
+    // the most blocks a workgroup that still give three CUs in four one
+    const int64_t most = nb / std::max<int64_t>(1, 3 * static_cast<int64_t>(cus) / 4);
+    if (M <= 8) return most >= 2 ? 2 : 1;
+    if (M <= 16) return most >= 4 ? 5 : most >= 2 ? 4 : 3;
     return -1;
 }
 
@@ -735,7 +847,7 @@ static int w4_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t num_c
     *plan = gemm_f16_lowbit_plan_t{};
     plan->splits = 1;
     if (M == 0 || N == 0 || K == 0) return GEMM_F16_OK;
-    const int id = w4_choose(M, N, num_cus);
+    const int id = w4_choose(M, s.nb, num_cus);
     if (id < 0) return decode_plan(M, N, K, num_cus, false, plan);
     const W4Kernel &e = kW4Kernels[id];
     plan->kernel = e.kernel;
@@ -846,7 +958,7 @@ extern "C" int gemm_f16_nt_w4(int64_t M, int64_t N, int64_t K, int32_t group, co
         p.K = static_cast<int32_t>(K);
         p.kt = static_cast<int32_t>(s.kt);
         p.nb = static_cast<int32_t>(s.nb);
-        const W4Kernel &e = kW4Kernels[w4_choose(M, N, cus)];
+        const W4Kernel &e = kW4Kernels[w4_choose(M, s.nb, cus)];
         return launch(e.fn[s.shift - 5], plan.grid, 64 * e.waves, &p, stream);
     }
     v = w4_decode(N, K, s, words, scales, workspace, stream);
