@@ -567,7 +567,8 @@ def matmul(a, b, out=None, stream=None):
 # builds on the names above.
 from . import lowbit  # noqa: E402
 from .lowbit import (  # noqa: E402,F401
-    LOWBIT_DECODE, LOWBIT_STREAM, LowbitPlan, Q8Matrix, W4Matrix, dequantize_q8, dequantize_w4, gemm_f16_nt_w4,
+    LOWBIT_DECODE, LOWBIT_STREAM, LOWBIT_TILE, LowbitPlan, Q8Matrix, W4Matrix, dequantize_q8,
+    dequantize_w4, gemm_f16_nt_w4,
     gemm_f16_nt_w4_plan, gemm_f16_q8_dequantize, gemm_f16_q8_quantize, gemm_f16_tn_q8,
     gemm_f16_tn_q8_plan, gemm_f16_w4_dequantize, gemm_f16_w4_pack, gemm_f16_w4_quantize,
     gemm_f16_w4_sizes, gemm_nt_w4, gemm_tn_q8, pack_w4, quantize_q8, quantize_w4)

@@ -19,7 +19,7 @@ import ctypes
 
 from . import _check, _on_device, _stream_handle, gemm_f16_device_cus, load
 
-LOWBIT_DECODE, LOWBIT_STREAM = 0, 1
+LOWBIT_DECODE, LOWBIT_STREAM, LOWBIT_TILE = 0, 1, 2
 Q8_GROUP = 32
 W4_GROUPS = (32, 64, 128)
 

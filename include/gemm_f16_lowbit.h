@@ -98,7 +98,10 @@ enum {
     GEMM_F16_LOWBIT_DECODE = 0,
     /* the codes go from memory to the matrix units through registers, one
      * pass, no workspace */
-    GEMM_F16_LOWBIT_STREAM = 1
+    GEMM_F16_LOWBIT_STREAM = 1,
+    /* tiles of the codes and of A through LDS; where K is split, the ranges'
+     * fp32 sums through the workspace */
+    GEMM_F16_LOWBIT_TILE = 2
 };
 typedef struct {
     int32_t kernel;           /* one of the values above                      */
