@@ -955,6 +955,255 @@ __global__ __launch_bounds__(64 * WAVES) void q8_decode_kernel(Q8Params p)
 }
 
 // ---------------------------------------------------------------------------
+// C = A^T X for few columns of A (rows of C): the codes streamed once
+// ---------------------------------------------------------------------------
+// A workgroup computes 16 MT rows of C by 16 CB columns over a range of the
+// rows of X.  Its waves take steps of 32 rows in turn, and lane l of a wave CB
+// neighbouring columns of rows 8 (l / 16) .. + 7: byte e of its eight rows is,
+// as it lies in its registers, what the MFMA wants from one lane for the
+// column (l % 16) CB + e, so the codes need no turning round.  A byte becomes
+// an fp16 number by v_perm_b32, one XOR (its bias and the magic exponent), one
+// subtraction and the product with its scale: exact, two operations a value.
+// A's rows and the scales of a step go through LDS of the wave's own, which
+// turns them round.  The waves' sums meet in LDS, the ranges' in the workspace;
+// q8_join_kernel adds those up in order.
+//
+// HBM bounds it, after the launches' 5 us.  CB = 16 reads the most a step
+// (268 MB of codes at 4.8 TB/s, with CB = 8 4.1), CB = 8 makes fewer ranges of
+// a small matrix (16 x 4096 over 8192 rows: 14.1 us, 15.4).  One workgroup a
+// CU is best; eight waves instead of four cost 1 us, three or four buffers
+// instead of two as much.  Neighbouring blocks of columns share cache lines of
+// scales, so each XCD takes a contiguous range of units (8192 columns over
+// 32768 rows: 68.6 to 56.8 us).
+struct Q8TnParams {
+    const uint16_t *A;         // [T, M]
+    const uint8_t *codes;      // [T, 32 ng]
+    const uint16_t *scales;    // [T, ng]
+    float *partial;
+    int64_t stride;            // values between two ranges' sums
+    int32_t T, M, ng;
+    int32_t blocks, m_tiles;   // blocks of 16 CB columns, tiles of 16 MT rows of C
+    int32_t t_split;           // rows of X a range, a multiple of 32
+};
+
+// 16-bit elements turned round in LDS: within 16 lanes, lane i addresses 4
+// elements of row i / 4 at columns 4 (i % 4) .., and gets column i of the 4 rows.
+__device__ __forceinline__ half4_t lds_read_tr16(const _Float16 *p)
+{
+    typedef short s4_t __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s4_t lds_s4_t;
+    return bits_as<half4_t>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t *)(p)));
+}
+
+template <int MT, int CB, int W>
+__global__ __launch_bounds__(64 * W, 2) void q8_tn_kernel(Q8TnParams p)
+{
+    constexpr int D = CB / 4;               // dwords of codes a lane and row
+    constexpr int G = CB / 2;               // groups of 32 columns a block
+    constexpr int AC = 2 * MT;              // 8-column chunks of A's rows
+    constexpr int AP = 16 * MT + 8;         // pitch of A's rows in LDS
+    // sums of a wave: [mt][e][reg] of 64 lanes; the waves' are joined in rounds
+    constexpr int SUMS = MT * CB * 4, ROUND = SUMS < 64 ? SUMS : 64;
+    struct Wave {
+        _Float16 a[32 * AP];
+        _Float16 s[G][32 + 8];
+    };
+    union Lds {
+        Wave wave[W];
+        float red[W][ROUND][64];
+    };
+    __shared__ __attribute__((aligned(16))) Lds lds;
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
+    const int r = lane & 15, kq = lane >> 4;
+    int32_t u = blockIdx.x;
+    {
+        const int32_t q = gridDim.x >> 3, rem = gridDim.x & 7, x = u & 7;
+        u = x * q + (x < rem ? x : rem) + (u >> 3);
+    }
+    const int32_t mtile = u % p.m_tiles;
+    u /= p.m_tiles;
+    const int32_t block = u % p.blocks, sp = u / p.blocks;
+    const int32_t m0 = mtile * 16 * MT;
+    const int32_t t0 = sp * p.t_split;
+    const int32_t t1 = min(p.T - t0, p.t_split) + t0;
+    const int64_t np = 32 * static_cast<int64_t>(p.ng);
+    const int64_t col = (static_cast<int64_t>(block) * 16 + r) * CB;   // this lane's columns of X
+    const uint8_t *cp = p.codes + (col < np ? col : 0);   // past the end: sums not stored
+    // scales: lane l fetches groups (l % 2) G / 2 .. of row l / 2
+    const int32_t g0 = block * G + (lane & 1) * (G / 2);
+    Wave &my = lds.wave[wave];
+    uint32_t q[2][8][D];
+    u32x4_t av[2][MT];
+    uint16_t sv[2][G / 2];
+    // whole steps of 32 rows that lie so far from X's last row that 8-column
+    // loads of A stay inside it: unconditional loads
+    const int32_t steps = (t1 - t0 + 31) / 32;
+    const int32_t safe = min((t1 - t0) / 32, max(p.T - 8 - t0, 0) / 32);
+    const int32_t count = safe > wave ? (safe - wave + W - 1) / W : 0;
+    auto load_codes = [&](int buf, int k, int64_t row) {
+        const uint8_t *c = cp + row * np;
+        if constexpr (D == 4) {
+            const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(c));
+#pragma unroll
+            for (int d = 0; d < 4; ++d) q[buf][k][d] = v[d];
+        } else {
+            const u32x2_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t *>(c));
+            q[buf][k][0] = v[0];
+            q[buf][k][1] = v[1];
+        }
+    };
+    auto load = [&](int buf, int32_t i) {
+        const int64_t t = t0 + (wave + static_cast<int64_t>(min(i, count - 1)) * W) * 32;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) load_codes(buf, k, t + kq * 8 + k);
+        const uint16_t *srow = p.scales + (t + (lane >> 1)) * p.ng;
+#pragma unroll
+        for (int g = 0; g < G / 2; ++g) sv[buf][g] = srow[min(g0 + g, p.ng - 1)];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int c = j * 64 + lane, m = m0 + c % AC * 8;
+            av[buf][j] = bits_as<u32x4_t>(half8_t(*reinterpret_cast<const half8_u_t *>(
+                p.A + (t + c / AC) * p.M + (m < p.M ? m : 0))));
+        }
+    };
+    // any step: rows past the range are zeros
+    auto load_guarded = [&](int32_t step) {
+        const int32_t t = t0 + step * 32;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) load_codes(0, k, min(t + kq * 8 + k, t1 - 1));
+        const int32_t ts = t + (lane >> 1);
+#pragma unroll
+        for (int g = 0; g < G / 2; ++g)
+            sv[0][g] = ts < t1 ? p.scales[static_cast<int64_t>(ts) * p.ng + min(g0 + g, p.ng - 1)] : 0;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int c = j * 64 + lane, ta = t + c / AC, m = m0 + c % AC * 8;
+            av[0][j] = u32x4_t{0, 0, 0, 0};
+            if (ta < t1 && m < p.M) av[0][j] = load8(p.A + static_cast<int64_t>(ta) * p.M, m, p.M);
+        }
+    };
+    f32x4_t acc[MT][CB] = {};
+    auto mma = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int c = j * 64 + lane;
+            *reinterpret_cast<u32x4_t *>(&my.a[c / AC * AP + c % AC * 8]) = av[buf][j];
+        }
+#pragma unroll
+        for (int g = 0; g < G / 2; ++g)
+            my.s[(lane & 1) * (G / 2) + g][lane >> 1] = bits_as<_Float16>(sv[buf][g]);
+        half8_t a[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const _Float16 *src = &my.a[(kq * 8 + (r >> 2)) * AP + mt * 16 + 4 * (r & 3)];
+            const half4_t lo = lds_read_tr16(src), hi = lds_read_tr16(src + 4 * AP);
+            a[mt] = half8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        }
+        const half8_t s = *reinterpret_cast<const half8_t *>(&my.s[r * CB / 32][kq * 8]);
+        const half2_t off = {_Float16(1152.0f), _Float16(1152.0f)};
+#pragma unroll
+        for (int e = 0; e < CB; ++e) {
+            half8_t x;
+            constexpr uint32_t sel[4] = {0x0c040c00u, 0x0c050c01u, 0x0c060c02u, 0x0c070c03u};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // bytes e of rows 2 i and 2 i + 1, biased by 128, under 0x64
+                const uint32_t b = __builtin_amdgcn_perm(q[buf][2 * i + 1][e / 4],
+                                                         q[buf][2 * i][e / 4], sel[e % 4]) ^ 0x64806480u;
+                const half2_t v = (bits_as<half2_t>(b) - off) * half2_t{s[2 * i], s[2 * i + 1]};
+                x[2 * i] = v[0];
+                x[2 * i + 1] = v[1];
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                acc[mt][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, a[mt], acc[mt][e], 0, 0, 0);
+        }
+    };
+    // one buffer's loads fly while the other's are multiplied; past the end
+    // the last step's again
+    if (count > 0) {
+        load(0, 0);
+        int32_t i = 0;
+        for (; i + 2 <= count; i += 2) {
+            load(1, i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            mma(0);
+            __builtin_amdgcn_sched_barrier(0);
+            load(0, i + 2);
+            __builtin_amdgcn_sched_barrier(0);
+            mma(1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (i < count) mma(0);
+    }
+    for (int32_t step = safe; step < steps; ++step)
+        if (step % W == wave) {
+            load_guarded(step);
+            mma(0);
+        }
+    // sum idx = (mt, e, reg) of lane l: row m0 + 16 mt + r of C, column (block 16 + 4 kq + reg) CB + e
+    constexpr int ROUNDS = SUMS / ROUND, PER = ROUND / W;
+    static_assert(SUMS % ROUND == 0 && ROUND % W == 0, "rounds");
+    float *to = p.partial + sp * p.stride +
+                (static_cast<int64_t>(block) * p.m_tiles + mtile) * (SUMS * 64) + lane;
+#pragma unroll
+    for (int rd = 0; rd < ROUNDS; ++rd) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < ROUND; ++k) {
+            const int idx = rd * ROUND + k;
+            lds.red[wave][k][lane] = acc[idx / (4 * CB)][idx / 4 % CB][idx % 4];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) sum += lds.red[w][wave * PER + k][lane];
+            to[(rd * ROUND + wave * PER + k) * 64] = sum;
+        }
+    }
+}
+
+// C from the ranges' sums, in order: a thread the four columns e .. e + 3 of one
+// (block, tile of rows, mt, e / 4, reg, lane).
+struct Q8JoinParams {
+    const float *partial;
+    uint16_t *C;
+    int64_t stride;
+    int32_t M, N, m_tiles, splits, mt, cb;
+};
+
+__global__ __launch_bounds__(256) void q8_join_kernel(Q8JoinParams p)
+{
+    const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (idx * 4 >= p.stride) return;
+    const int lane = threadIdx.x & 63, r = lane & 15, kq = lane >> 4;
+    int64_t k = idx >> 6;
+    const int reg = static_cast<int>(k & 3);
+    k >>= 2;
+    const int e4 = static_cast<int>(k % (p.cb / 4));
+    k /= p.cb / 4;
+    const int mt = static_cast<int>(k % p.mt);
+    k /= p.mt;
+    const int32_t mtile = static_cast<int32_t>(k % p.m_tiles);
+    const int64_t block = k / p.m_tiles;
+    const int32_t m = (mtile * p.mt + mt) * 16 + r;
+    const int64_t n = (block * 16 + 4 * kq + reg) * p.cb + 4 * e4;
+    if (m >= p.M || n >= p.N) return;
+    const float *from = p.partial + (block * p.m_tiles + mtile) * (static_cast<int64_t>(p.mt) * p.cb * 256) +
+                        ((mt * p.cb + 4 * e4) * 4 + reg) * 64 + lane;
+    f32x4_t sum = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int32_t s = 0; s < p.splits; ++s) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += from[s * p.stride + e * 256];
+    }
+    store4(p.C, p.M, p.N, m, static_cast<int32_t>(n), sum);
+}
+
+// ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1355,6 +1604,63 @@ static int w4_run(const W4Choice &c, const gemm_f16_lowbit_plan_t &plan, int64_t
                   stream);
 }
 
+// The kernels of the product with 8-bit activations that read the codes.
+struct Q8Kernel {
+    int32_t mt, cb, waves;
+    const void *fn;
+};
+#define Q8_TN(MT, CB, W) Q8Kernel{MT, CB, W, reinterpret_cast<const void *>(&q8_tn_kernel<MT, CB, W>)}
+static const Q8Kernel kQ8Kernels[] = {
+    Q8_TN(1, 8, 4), Q8_TN(1, 16, 4), Q8_TN(2, 8, 4), Q8_TN(4, 8, 4),
+};
+#undef Q8_TN
+
+// What a product runs: an index into kQ8Kernels (-1: decode), tiles and ranges.
+struct Q8Choice {
+    int32_t id;
+    int64_t blocks, m_tiles, t_split, splits;
+};
+
+static Q8Choice q8_layout(int32_t id, int64_t M, int64_t K, const Q8Shape &s, int32_t cus)
+{
+    const Q8Kernel &e = kQ8Kernels[id];
+    Q8Choice c;
+    c.id = id;
+    c.blocks = cdiv(s.groups * GEMM_F16_Q8_GROUP, 16 * e.cb);
+    c.m_tiles = cdiv(M, 16 * e.mt);
+    // one workgroup a CU, where the rows suffice for a step for each wave
+    const int64_t steps = cdiv(K, 32);
+    const int64_t want = std::max<int64_t>(1, cus / (c.blocks * c.m_tiles));
+    const int64_t per = cdiv(steps, std::min(want, cdiv(steps, e.waves)));
+    c.t_split = per * 32;
+    c.splits = cdiv(steps, per);
+    return c;
+}
+
+static Q8Choice q8_choose(int64_t M, int64_t K, const Q8Shape &s, int32_t cus)
+{
+    const Q8Choice decode = {-1, 0, 0, 0, 0};
+    if (M > 256 || s.groups > (1 << 20) || M * s.groups > (1 << 22)) return decode;
+    if (M > 32) return q8_layout(3, M, K, s, cus);
+    if (M > 16) return q8_layout(2, M, K, s, cus);
+    return q8_layout(s.codes > (int64_t(64) << 20) ? 1 : 0, M, K, s, cus);
+}
+
+static int q8_plan_choice(const Q8Choice &c, int64_t M, int64_t N, int64_t K, int32_t num_cus,
+                          gemm_f16_lowbit_plan_t *plan)
+{
+    if (c.id < 0) return decode_plan(M, N, K, num_cus, true, plan);
+    const Q8Kernel &e = kQ8Kernels[c.id];
+    plan->kernel = GEMM_F16_LOWBIT_STREAM;
+    plan->block_m = 16 * e.mt;
+    plan->block_n = 16 * e.cb;
+    plan->waves = e.waves;
+    plan->splits = static_cast<int32_t>(c.splits);
+    plan->grid = static_cast<int32_t>(c.blocks * c.m_tiles * c.splits);
+    plan->workspace_bytes = c.blocks * c.m_tiles * c.splits * e.mt * e.cb * 1024;
+    return GEMM_F16_OK;
+}
+
 static int q8_plan(int64_t M, int64_t N, int64_t K, int32_t num_cus, gemm_f16_lowbit_plan_t *plan)
 {
     Q8Shape s;
@@ -1365,7 +1671,49 @@ static int q8_plan(int64_t M, int64_t N, int64_t K, int32_t num_cus, gemm_f16_lo
     *plan = gemm_f16_lowbit_plan_t{};
     plan->splits = 1;
     if (M == 0 || N == 0 || K == 0) return GEMM_F16_OK;
-    return decode_plan(M, N, K, num_cus, true, plan);
+    return q8_plan_choice(q8_choose(M, K, s, num_cus), M, N, K, num_cus, plan);
+}
+
+static int q8_run(const Q8Choice &c, int64_t M, int64_t N, int64_t K, const Q8Shape &s,
+                  const void *A, const void *codes, const void *scales, void *C, void *workspace,
+                  int64_t workspace_bytes, hipStream_t stream)
+{
+    if (c.id < 0) {
+        const int v = q8_launch(reinterpret_cast<const void *>(&q8_decode_kernel), K, N, s, nullptr,
+                                workspace, codes, scales, stream);
+        if (v != GEMM_F16_OK) return v;
+        const int64_t used = round_up(N * K * 2, 256);
+        return gemm_f16_tn_splitk(M, N, K, A, workspace, C, 0,
+                                  static_cast<char *>(workspace) + used, workspace_bytes - used,
+                                  stream);
+    }
+    const Q8Kernel &e = kQ8Kernels[c.id];
+    Q8TnParams p;
+    p.A = static_cast<const uint16_t *>(A);
+    p.codes = static_cast<const uint8_t *>(codes);
+    p.scales = static_cast<const uint16_t *>(scales);
+    p.partial = static_cast<float *>(workspace);
+    p.stride = c.blocks * c.m_tiles * e.mt * e.cb * 256;
+    p.T = static_cast<int32_t>(K);
+    p.M = static_cast<int32_t>(M);
+    p.ng = static_cast<int32_t>(s.groups);
+    p.blocks = static_cast<int32_t>(c.blocks);
+    p.m_tiles = static_cast<int32_t>(c.m_tiles);
+    p.t_split = static_cast<int32_t>(c.t_split);
+    const int v = launch(e.fn, c.blocks * c.m_tiles * c.splits, 64 * e.waves, &p, stream);
+    if (v != GEMM_F16_OK) return v;
+    Q8JoinParams q;
+    q.partial = p.partial;
+    q.C = static_cast<uint16_t *>(C);
+    q.stride = p.stride;
+    q.M = p.M;
+    q.N = static_cast<int32_t>(N);
+    q.m_tiles = p.m_tiles;
+    q.splits = static_cast<int32_t>(c.splits);
+    q.mt = e.mt;
+    q.cb = e.cb;
+    return launch(reinterpret_cast<const void *>(&q8_join_kernel), cdiv(p.stride, 1024), 256, &q,
+                  stream);
 }
 
 }  // namespace gemm_f16_lowbit
@@ -1504,14 +1852,10 @@ extern "C" int gemm_f16_tn_q8(int64_t M, int64_t N, int64_t K, const void *A, co
     int32_t cus = 0;
     v = gemm_f16_device_cus(&cus);
     if (v != GEMM_F16_OK) return v;
-    gemm_f16_lowbit_plan_t plan;
-    v = q8_plan(M, N, K, cus, &plan);
+    const Q8Choice choice = q8_choose(M, K, s, cus);
+    gemm_f16_lowbit_plan_t plan{};
+    v = q8_plan_choice(choice, M, N, K, cus, &plan);
     if (v != GEMM_F16_OK) return v;
     if (plan.workspace_bytes > (workspace ? workspace_bytes : 0)) return GEMM_F16_INVALID_ARG;
-    v = q8_launch(reinterpret_cast<const void *>(&q8_decode_kernel), K, N, s, nullptr, workspace,
-                  codes, scales, stream);
-    if (v != GEMM_F16_OK) return v;
-    const int64_t used = round_up(N * K * 2, 256);
-    return gemm_f16_tn_splitk(M, N, K, A, workspace, C, 0, static_cast<char *>(workspace) + used,
-                              workspace_bytes - used, stream);
+    return q8_run(choice, M, N, K, s, A, codes, scales, C, workspace, workspace_bytes, stream);
 }
