@@ -84,14 +84,32 @@ __device__ __forceinline__ float group_scale(uint32_t big, float most)
     return fminf(fmaxf(s, 0x1p-24f), most);
 }
 
-// x / s rounded to nearest, ties to even.  The product with the reciprocal can
-// miss a tie by an ulp; one Newton step gives the correctly rounded quotient,
-// and a quotient that is not a tie is further from one than fp32 resolves
-// (checked for every fp16 x and every scale).
-__device__ __forceinline__ float quotient(float x, float s, float r)
+// 1 / s as a sum of two numbers, to far below fp32's resolution.
+struct Reciprocal {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Reciprocal reciprocal(float s)
 {
-    const float t = x * r;
-    return __builtin_rintf(__builtin_fmaf(__builtin_fmaf(-t, s, x), r, t));
+    const float r = __builtin_amdgcn_rcpf(s);
+    return Reciprocal{r, __builtin_fmaf(-s, r, 1.0f) * r};
+}
+
+// x / s rounded to nearest, ties to even, as the low bits of a float: below
+// 2^22 in magnitude, adding 1.5 2^23 leaves the rounded integer in the low 22
+// bits (two's complement).  A product with one fp32 reciprocal can miss a tie
+// by an ulp; with the second part a tie comes out exact, and a quotient that
+// is not a tie is further from one than fp32 resolves (checked for every fp16
+// x and every scale, with hi an ulp off either way).
+__device__ __forceinline__ uint32_t quotient(float x, Reciprocal r, float bias)
+{
+    return bits_as<uint32_t>(__builtin_fmaf(x, r.hi, x * r.lo) + (0x1.8p23f + bias));
+}
+
+// The eight halves of four dwords, as floats.
+__device__ __forceinline__ float half_of(u32x4_t v, int i)
+{
+    return static_cast<float>(bits_as<half2_t>(v[i / 2])[i % 2]);
 }
 
 // ---------------------------------------------------------------------------
@@ -133,38 +151,60 @@ __global__ __launch_bounds__(64 * WAVES) void w4_encode_kernel(W4EncodeParams p)
         const int32_t cols = n < p.N ? p.K : 0;     // rows past N are zeros
         const int64_t row = n < p.N ? n : 0;
         const int64_t k0 = static_cast<int64_t>(t) * 128 + kq * 8;  // may pass 2^31 in a pad
+        // A tile wholly inside the matrix takes the loads all at once; one at
+        // its edge takes each under its own conditions (which make the loads
+        // wait for each other: all tiles that way took 57.6 us at 8192 x 8192).
+        const bool inside = (static_cast<int64_t>(t) + 1) * 128 <= p.K &&
+                            (static_cast<int64_t>(b) + 1) * 16 <= p.N;
         u32x4_t v[4];
+        u32x2_t d[4];
         int32_t q[4][8];
         uint32_t big[4];
-        // per 32 columns of this lane's row: the eight values, and the largest
-        // magnitude of all 32 (fp16 bits, or of the codes)
+        if constexpr (PACK) {
+            const int8_t *src = p.codes + row * p.K + k0;
+            if (inside) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = k0 + 32 * j;
-            if constexpr (PACK) {
-                const int8_t *src = p.codes + row * p.K + c;
-                uint32_t d[2] = {0, 0};
-                if (c + 8 <= cols) {
-                    const u32x2_u_t w = *reinterpret_cast<const u32x2_u_t *>(src);
-                    d[0] = w[0];
-                    d[1] = w[1];
-                } else {
+                for (int j = 0; j < 4; ++j)
+                    d[j] = u32x2_t(*reinterpret_cast<const u32x2_u_t *>(src + 32 * j));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    d[j] = u32x2_t{0, 0};
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        if (c + i < cols)
-                            d[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(src[i])) << (8 * (i % 4));
+                        if (k0 + 32 * j + i < cols)
+                            d[j][i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(src[32 * j + i]))
+                                           << (8 * (i % 4));
                 }
+            }
+        } else {
+            const uint16_t *src = p.W + row * p.K;
+            if (inside) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = bits_as<u32x4_t>(
+                        half8_t(*reinterpret_cast<const half8_u_t *>(src + k0 + 32 * j)));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = k0 + 32 * j < cols ? load8(src, static_cast<int32_t>(k0 + 32 * j), cols)
+                                              : u32x4_t{0, 0, 0, 0};
+            }
+        }
+        // per 32 columns of this lane's row the largest magnitude, as fp16 bits
+        // or of the codes
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (PACK) {
                 big[j] = 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    q[j][i] = static_cast<int8_t>(d[i / 4] >> (8 * (i % 4)));
+                    q[j][i] = static_cast<int8_t>(d[j][i / 4] >> (8 * (i % 4)));
                     // 9 marks a code that four bits do not hold
                     const uint32_t m = q[j][i] < -8 || q[j][i] > 7 ? 9 : q[j][i] < 0 ? -q[j][i] : q[j][i];
                     big[j] = m > big[j] ? m : big[j];
                 }
             } else {
-                v[j] = c < cols ? load8(p.W + row * p.K, static_cast<int32_t>(c), cols)
-                                : u32x4_t{0, 0, 0, 0};
                 big[j] = largest8(v[j]);
             }
             uint32_t o = __shfl_xor(big[j], 16);
@@ -182,6 +222,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_encode_kernel(W4EncodeParams p)
         for (int j = 0; j < 4; ++j) {
             float s;
             bool bad;
+            uint32_t word = 0;
             if constexpr (PACK) {
                 const int64_t k = static_cast<int64_t>(t) * 128 + 32 * j;
                 s = 0.0f;
@@ -192,22 +233,24 @@ __global__ __launch_bounds__(64 * WAVES) void w4_encode_kernel(W4EncodeParams p)
                 }
                 bad = !(__builtin_fabsf(s) <= 65504.0f) || big[j] > 8 ||
                       __builtin_fabsf(s) * static_cast<float>(big[j]) > 65504.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    word |= (static_cast<uint32_t>(q[j][i] + 8) & 15u) << (16 * (i % 2) + 4 * (i / 2));
             } else {
                 s = group_scale<8, 7>(big[j], 9344.0f);
                 bad = big[j] >= 0x7c00;
-                const float rcp = 1.0f / s;
+                const Reciprocal rcp = reciprocal(s);
+                // a quotient is at most 7.01, also where s is capped; 8 more is
+                // the code, alone in the low 16 bits
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint16_t h = static_cast<uint16_t>(v[j][i / 2] >> (16 * (i % 2)));
-                    const float x = bad ? 0.0f : static_cast<float>(bits_as<_Float16>(h));
-                    const int32_t c = static_cast<int32_t>(quotient(x, s, rcp));
-                    q[j][i] = c > 7 ? 7 : c < -7 ? -7 : c;   // past 7 only where s is capped
+                for (int i = 0; i < 8; i += 2) {
+                    const uint32_t pair = __builtin_amdgcn_perm(
+                        quotient(half_of(v[j], i + 1), rcp, 8.0f),
+                        quotient(half_of(v[j], i), rcp, 8.0f), 0x05040100u);
+                    word |= pair << (2 * i);
                 }
             }
-            uint32_t word = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                word |= static_cast<uint32_t>((bad ? 0 : q[j][i]) + 8) << (16 * (i % 2) + 4 * (i / 2));
+            if (bad) word = 0x88888888u;
             out[j] = word;
             if (kq == 0 && ((32 * j) & ((1 << p.shift) - 1)) == 0) {
                 const int64_t g = static_cast<int64_t>(t) * per_tile + ((32 * j) >> p.shift);
@@ -877,11 +920,20 @@ __global__ __launch_bounds__(64 * WAVES) void q8_encode_kernel(Q8Params p)
     if (chunk >= p.chunks) return;    // whole groups: chunks is a multiple of 4
     const int64_t c = static_cast<int64_t>(chunk) * 8;
     u32x4_t v[Q8_ROWS];
+    // a workgroup wholly inside the matrix takes the loads all at once
+    if ((static_cast<int64_t>(cb + 1) << p.tx_shift) * 8 <= p.N &&
+        (static_cast<int64_t>(rb) + 1) * ty * Q8_ROWS <= p.R) {
 #pragma unroll
-    for (int i = 0; i < Q8_ROWS; ++i) {
-        const int64_t row = row0 + i * ty;
-        v[i] = u32x4_t{0, 0, 0, 0};
-        if (row < p.R && c < p.N) v[i] = load8(p.X + row * p.N, static_cast<int32_t>(c), p.N);
+        for (int i = 0; i < Q8_ROWS; ++i)
+            v[i] = bits_as<u32x4_t>(
+                half8_t(*reinterpret_cast<const half8_u_t *>(p.X + (row0 + i * ty) * p.N + c)));
+    } else {
+#pragma unroll
+        for (int i = 0; i < Q8_ROWS; ++i) {
+            const int64_t row = row0 + i * ty;
+            v[i] = u32x4_t{0, 0, 0, 0};
+            if (row < p.R && c < p.N) v[i] = load8(p.X + row * p.N, static_cast<int32_t>(c), p.N);
+        }
     }
 #pragma unroll
     for (int i = 0; i < Q8_ROWS; ++i) {
@@ -889,17 +941,24 @@ __global__ __launch_bounds__(64 * WAVES) void q8_encode_kernel(Q8Params p)
         const uint32_t big = quad_max(largest8(v[i]));
         const bool bad = big >= 0x7c00;
         const float s = group_scale<4, 127>(big, 576.0f);
-        const float rcp = 1.0f / s;
-        // 576 (the only scale past 512) times 114 would pass fp16's largest
-        const int32_t most = s > 512.0f ? 113 : 127;
-        u32x2_t q = {0, 0};
+        const Reciprocal rcp = reciprocal(s);
+        uint32_t k[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint16_t h = static_cast<uint16_t>(v[i][e / 2] >> (16 * (e % 2)));
-            const float x = bad ? 0.0f : static_cast<float>(bits_as<_Float16>(h));
-            int32_t k = static_cast<int32_t>(quotient(x, s, rcp));
-            k = k > most ? most : k < -most ? -most : k;
-            q[e / 4] |= (static_cast<uint32_t>(k) & 0xffu) << (8 * (e % 4));
+        for (int e = 0; e < 8; ++e) k[e] = quotient(half_of(v[i], e), rcp, 0.0f);
+        // 576 (the only scale past 512) times 114 would pass fp16's largest
+        if (__builtin_expect(s > 512.0f, 0)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float f = bits_as<float>(k[e]) - 0x1.8p23f;
+                k[e] = bits_as<uint32_t>(fminf(fmaxf(f, -113.0f), 113.0f) + 0x1.8p23f);
+            }
+        }
+        u32x2_t q;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t lo = __builtin_amdgcn_perm(k[4 * h + 1], k[4 * h], 0x0c0c0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(k[4 * h + 3], k[4 * h + 2], 0x04000c0cu);
+            q[h] = bad ? 0 : lo | hi;
         }
         if (row < p.R) {
             p.codes[row * p.chunks + chunk] = q;
@@ -1637,13 +1696,26 @@ static Q8Choice q8_layout(int32_t id, int64_t M, int64_t K, const Q8Shape &s, in
     return c;
 }
 
-static Q8Choice q8_choose(int64_t M, int64_t K, const Q8Shape &s, int32_t cus)
+// Up to 64 rows of C the codes are read once, and streaming them won on all 54
+// shapes measured (16 to 64 rows, 256 to 14336 columns, 512 to 8192 rows of X;
+// 1.1 to 3.2 times faster than decoding).  With more rows each tile of 64
+// reads them again.  It still won where the tiles fill whole rounds of the CUs
+// to three quarters, and the sums and their join (rows times columns of C) are
+// small beside the rows of X: 128 x 4096 over 8192 rows 27 us (decoding 44),
+// 256 x 4096 over 8192 43 (49); but 320 x 4096 over 8192 68 (57), 192 x 4096
+// over 512 13 (11).
+static Q8Choice q8_choose(int64_t M, int64_t N, int64_t K, const Q8Shape &s, int32_t cus)
 {
     const Q8Choice decode = {-1, 0, 0, 0, 0};
-    if (M > 256 || s.groups > (1 << 20) || M * s.groups > (1 << 22)) return decode;
-    if (M > 32) return q8_layout(3, M, K, s, cus);
-    if (M > 16) return q8_layout(2, M, K, s, cus);
-    return q8_layout(s.codes > (int64_t(64) << 20) ? 1 : 0, M, K, s, cus);
+    // 32-bit counts of tiles and values in the kernels
+    if (M > 512 || s.groups > (1 << 20) || M * s.groups > (1 << 22)) return decode;
+    if (M <= 16) return q8_layout(s.codes > (int64_t(64) << 20) ? 1 : 0, M, K, s, cus);
+    if (M <= 32) return q8_layout(2, M, K, s, cus);
+    const Q8Choice c = q8_layout(3, M, K, s, cus);
+    if (M <= 64) return c;
+    const int64_t tiles = c.blocks * c.m_tiles;
+    const bool fills = tiles <= cus && 4 * (cus / tiles * tiles) >= 3 * static_cast<int64_t>(cus);
+    return fills && M * N <= 512 * K ? c : decode;
 }
 
 static int q8_plan_choice(const Q8Choice &c, int64_t M, int64_t N, int64_t K, int32_t num_cus,
@@ -1671,7 +1743,7 @@ static int q8_plan(int64_t M, int64_t N, int64_t K, int32_t num_cus, gemm_f16_lo
     *plan = gemm_f16_lowbit_plan_t{};
     plan->splits = 1;
     if (M == 0 || N == 0 || K == 0) return GEMM_F16_OK;
-    return q8_plan_choice(q8_choose(M, K, s, num_cus), M, N, K, num_cus, plan);
+    return q8_plan_choice(q8_choose(M, N, K, s, num_cus), M, N, K, num_cus, plan);
 }
 
 static int q8_run(const Q8Choice &c, int64_t M, int64_t N, int64_t K, const Q8Shape &s,
@@ -1852,7 +1924,7 @@ extern "C" int gemm_f16_tn_q8(int64_t M, int64_t N, int64_t K, const void *A, co
     int32_t cus = 0;
     v = gemm_f16_device_cus(&cus);
     if (v != GEMM_F16_OK) return v;
-    const Q8Choice choice = q8_choose(M, K, s, cus);
+    const Q8Choice choice = q8_choose(M, N, K, s, cus);
     gemm_f16_lowbit_plan_t plan{};
     v = q8_plan_choice(choice, M, N, K, cus, &plan);
     if (v != GEMM_F16_OK) return v;

@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _on_device, _stream_handle, gemm_f16_device_cus, load
+from . import GemmError, _check, _on_device, _stream_handle, gemm_f16_device_cus, load
 
 LOWBIT_DECODE, LOWBIT_STREAM, LOWBIT_TILE = 0, 1, 2
 Q8_GROUP = 32
@@ -206,6 +206,9 @@ class Q8Matrix:
 
 
 # ---- torch convenience -------------------------------------------------------
+# A call for one token is a few microseconds on the GPU, so the path to it is
+# kept short: one call into the library, no wrapper objects, no device switch
+# where the device is current.
 def _matrix(x, dtype, what: str):
     if x.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}")
@@ -218,48 +221,59 @@ def _matrix(x, dtype, what: str):
     return x.shape
 
 
-def _check_stream(stream, device) -> None:
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+def _same_device(x, y, what: str) -> None:
+    if x.get_device() != y.get_device():
+        raise ValueError(f"{what} must be on the same GPU")
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory that belongs to the stream it will be used on."""
+def _call(on, stream, fn, *args) -> None:
+    """fn(*args, stream) on the device of the tensor `on`."""
+    with _on_device(on):
+        status = fn(*args, _stream_handle(on, stream))
+    if status:
+        raise GemmError(status, fn.__name__)
+
+
+def _new(on, stream, shape, dtype):
+    """Memory on the device of `on` that belongs to the stream it will be used on."""
+    if stream is None:
+        return on.new_empty(shape, dtype=dtype)
     import torch
 
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+    if stream.device != on.device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {on.device}")
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return on.new_empty(shape, dtype=dtype)
 
 
 def _record(stream, *tensors) -> None:
     """Tensors of other streams, used on `stream`: not to be reused before it is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
-def _output(out, shape, device, stream):
+def _output(out, on, stream, shape):
     import torch
 
     if out is None:
-        return _empty(shape, torch.float16, device, stream)
-    if out.dtype != torch.float16 or tuple(out.shape) != tuple(shape) or \
-            not out.is_contiguous() or out.device != device:
-        raise ValueError(f"out must be a contiguous float16 {list(shape)} tensor on {device}")
+        return _new(on, stream, shape, torch.float16)
+    if stream is not None and stream.device != on.device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {on.device}")
+    if out.dtype != torch.float16 or tuple(out.shape) != shape or not out.is_contiguous() or \
+            out.device != on.device:
+        raise ValueError(f"out must be a contiguous float16 {list(shape)} tensor on {on.device}")
     return out
 
 
-def _empty_w4(n: int, k: int, group: int, device, stream):
+def _new_w4(on, stream, n: int, k: int, group: int) -> W4Matrix:
     import torch
 
     if group not in W4_GROUPS:
         raise ValueError(f"group must be one of {W4_GROUPS}, not {group!r}")
     nb, kt = -(-n // 16), -(-k // 128)
-    return W4Matrix(_empty((nb, kt, 64, 4), torch.int32, device, stream),
-                    _empty((nb, 128 * kt // group, 16), torch.float16, device, stream), n, k, group)
+    return W4Matrix(_new(on, stream, (nb, kt, 64, 4), torch.int32),
+                    _new(on, stream, (nb, 128 * kt // group, 16), torch.float16), n, k, group)
 
 
 def quantize_w4(w, group: int = 128, stream=None) -> W4Matrix:
@@ -267,12 +281,11 @@ def quantize_w4(w, group: int = 128, stream=None) -> W4Matrix:
     import torch
 
     n, k = _matrix(w, torch.float16, "w")
-    _check_stream(stream, w.device)
-    q = _empty_w4(n, k, group, w.device, stream)
-    with _on_device(w):
-        gemm_f16_w4_quantize(n, k, group, w.data_ptr(), q.words.data_ptr(), q.scales.data_ptr(),
-                             _stream_handle(w, stream))
-    _record(stream, w)
+    q = _new_w4(w, stream, n, k, group)
+    _call(w, stream, load().gemm_f16_w4_quantize, n, k, group, w.data_ptr(), q.words.data_ptr(),
+          q.scales.data_ptr())
+    if stream is not None:
+        _record(stream, w)
     return q
 
 
@@ -284,17 +297,15 @@ def pack_w4(codes, scales, group: int = 128, stream=None) -> W4Matrix:
     import torch
 
     n, k = _matrix(codes, torch.int8, "codes")
-    _check_stream(stream, codes.device)
-    q = _empty_w4(n, k, group, codes.device, stream)
+    q = _new_w4(codes, stream, n, k, group)
     if tuple(_matrix(scales, torch.float16, "scales")) != (n, -(-k // group)):
         raise ValueError(f"scales{tuple(scales.shape)} do not fit codes{tuple(codes.shape)} in "
                          f"groups of {group}")
-    if scales.device != codes.device:
-        raise ValueError("codes and scales must be on the same GPU")
-    with _on_device(codes):
-        gemm_f16_w4_pack(n, k, group, codes.data_ptr(), scales.data_ptr(), q.words.data_ptr(),
-                         q.scales.data_ptr(), _stream_handle(codes, stream))
-    _record(stream, codes, scales)
+    _same_device(codes, scales, "codes and scales")
+    _call(codes, stream, load().gemm_f16_w4_pack, n, k, group, codes.data_ptr(),
+          scales.data_ptr(), q.words.data_ptr(), q.scales.data_ptr())
+    if stream is not None:
+        _record(stream, codes, scales)
     return q
 
 
@@ -302,12 +313,12 @@ def dequantize_w4(w: W4Matrix, out=None, stream=None):
     """The [n, k] fp16 matrix that w stands for, exactly."""
     if not isinstance(w, W4Matrix):
         raise TypeError("w must be a W4Matrix")
-    _check_stream(stream, w.device)
-    out = _output(out, (w.n, w.k), w.device, stream)
-    with _on_device(w.words):
-        gemm_f16_w4_dequantize(w.n, w.k, w.group, w.words.data_ptr(), w.scales.data_ptr(),
-                               out.data_ptr(), _stream_handle(w.words, stream))
-    _record(stream, w.words, w.scales, out)
+    words = w.words
+    out = _output(out, words, stream, (w.n, w.k))
+    _call(words, stream, load().gemm_f16_w4_dequantize, w.n, w.k, w.group, words.data_ptr(),
+          w.scales.data_ptr(), out.data_ptr())
+    if stream is not None:
+        _record(stream, words, w.scales, out)
     return out
 
 
@@ -316,14 +327,13 @@ def quantize_q8(x, stream=None) -> Q8Matrix:
     import torch
 
     r, n = _matrix(x, torch.float16, "x")
-    _check_stream(stream, x.device)
     groups = -(-n // Q8_GROUP)
-    q = Q8Matrix(_empty((r, groups * Q8_GROUP), torch.int8, x.device, stream),
-                 _empty((r, groups), torch.float16, x.device, stream), n)
-    with _on_device(x):
-        gemm_f16_q8_quantize(r, n, x.data_ptr(), q.codes.data_ptr(), q.scales.data_ptr(),
-                             _stream_handle(x, stream))
-    _record(stream, x)
+    q = Q8Matrix(_new(x, stream, (r, groups * Q8_GROUP), torch.int8),
+                 _new(x, stream, (r, groups), torch.float16), n)
+    _call(x, stream, load().gemm_f16_q8_quantize, r, n, x.data_ptr(), q.codes.data_ptr(),
+          q.scales.data_ptr())
+    if stream is not None:
+        _record(stream, x)
     return q
 
 
@@ -331,36 +341,40 @@ def dequantize_q8(x: Q8Matrix, out=None, stream=None):
     """The [r, n] fp16 matrix that x stands for, exactly."""
     if not isinstance(x, Q8Matrix):
         raise TypeError("x must be a Q8Matrix")
-    _check_stream(stream, x.device)
-    out = _output(out, (x.r, x.n), x.device, stream)
-    with _on_device(x.codes):
-        gemm_f16_q8_dequantize(x.r, x.n, x.codes.data_ptr(), x.scales.data_ptr(), out.data_ptr(),
-                               _stream_handle(x.codes, stream))
-    _record(stream, x.codes, x.scales, out)
+    codes = x.codes
+    out = _output(out, codes, stream, (x.r, x.n))
+    _call(codes, stream, load().gemm_f16_q8_dequantize, x.r, x.n, codes.data_ptr(),
+          x.scales.data_ptr(), out.data_ptr())
+    if stream is not None:
+        _record(stream, codes, x.scales, out)
     return out
 
 
-# workspace bytes of a product, per (kind, sizes, device): a repeated call
+# workspace bytes of a product, per (planner, sizes, device): a repeated call
 # costs a dictionary lookup
 _workspace_bytes: dict = {}
 
 
-def _workspace(plan, key, on, workspace, stream):
-    """(tensor or None, its bytes) for a product planned by plan(*key[1:-1], num_cus)."""
-    import torch
-
+def _workspace(key, on, workspace, stream):
+    """(tensor or None, its address, its bytes) for a product planned by
+    key[0](*key[1:-1], compute units)."""
     need = _workspace_bytes.get(key)
     if need is None:
         with _on_device(on):
-            need = plan(*key[1:-1], gemm_f16_device_cus()).workspace_bytes
+            need = key[0](*key[1:-1], gemm_f16_device_cus()).workspace_bytes
         if len(_workspace_bytes) >= 1024:
             _workspace_bytes.clear()
         _workspace_bytes[key] = need
     if workspace is None:
-        return (_empty(need, torch.uint8, on.device, stream), need) if need else (None, 0)
+        if not need:
+            return None, 0, 0
+        import torch
+
+        workspace = _new(on, stream, (need,), torch.uint8)
+        return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != on.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the operands' device")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def gemm_nt_w4(a, w: W4Matrix, out=None, workspace=None, stream=None):
@@ -372,19 +386,17 @@ def gemm_nt_w4(a, w: W4Matrix, out=None, workspace=None, stream=None):
     if not isinstance(w, W4Matrix):
         raise TypeError("w must be a W4Matrix")
     m, k = _matrix(a, torch.float16, "a")
+    n, words = w.n, w.words
     if k != w.k:
         raise ValueError(f"shape mismatch: a{tuple(a.shape)} w{w.shape}")
-    if a.device != w.device:
-        raise ValueError("a and w must be on the same GPU")
-    _check_stream(stream, a.device)
-    out = _output(out, (m, w.n), a.device, stream)
-    ws, ws_bytes = _workspace(gemm_f16_nt_w4_plan, ("w4", m, w.n, k, w.group, a.get_device()), a,
-                              workspace, stream)
-    with _on_device(a):
-        gemm_f16_nt_w4(m, w.n, k, w.group, a.data_ptr(), w.words.data_ptr(), w.scales.data_ptr(),
-                       out.data_ptr(), ws.data_ptr() if ws is not None else 0, ws_bytes,
-                       _stream_handle(a, stream))
-    _record(stream, a, w.words, w.scales, out, ws)
+    _same_device(a, words, "a and w")
+    out = _output(out, a, stream, (m, n))
+    ws, ws_ptr, ws_bytes = _workspace((gemm_f16_nt_w4_plan, m, n, k, w.group, a.get_device()), a,
+                                      workspace, stream)
+    _call(a, stream, load().gemm_f16_nt_w4, m, n, k, w.group, a.data_ptr(), words.data_ptr(),
+          w.scales.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes)
+    if stream is not None:
+        _record(stream, a, words, w.scales, out, ws)
     return out
 
 
@@ -398,17 +410,15 @@ def gemm_tn_q8(a, x: Q8Matrix, out=None, workspace=None, stream=None):
     if not isinstance(x, Q8Matrix):
         raise TypeError("x must be a Q8Matrix")
     k, m = _matrix(a, torch.float16, "a")
+    n, codes = x.n, x.codes
     if k != x.r:
         raise ValueError(f"shape mismatch: a{tuple(a.shape)} x{x.shape}")
-    if a.device != x.device:
-        raise ValueError("a and x must be on the same GPU")
-    _check_stream(stream, a.device)
-    out = _output(out, (m, x.n), a.device, stream)
-    ws, ws_bytes = _workspace(gemm_f16_tn_q8_plan, ("q8", m, x.n, k, a.get_device()), a, workspace,
-                              stream)
-    with _on_device(a):
-        gemm_f16_tn_q8(m, x.n, k, a.data_ptr(), x.codes.data_ptr(), x.scales.data_ptr(),
-                       out.data_ptr(), ws.data_ptr() if ws is not None else 0, ws_bytes,
-                       _stream_handle(a, stream))
-    _record(stream, a, x.codes, x.scales, out, ws)
+    _same_device(a, codes, "a and x")
+    out = _output(out, a, stream, (m, n))
+    ws, ws_ptr, ws_bytes = _workspace((gemm_f16_tn_q8_plan, m, n, k, a.get_device()), a, workspace,
+                                      stream)
+    _call(a, stream, load().gemm_f16_tn_q8, m, n, k, a.data_ptr(), codes.data_ptr(),
+          x.scales.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes)
+    if stream is not None:
+        _record(stream, a, codes, x.scales, out, ws)
     return out

@@ -258,7 +258,8 @@ def test_tn_q8(g, m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(16, 4096, 8192), (64, 1024, 4999), (1024, 1056, 3000),
-                                   (2048, 512, 1111)])
+                                   (2048, 512, 1111), (5, 14336, 8192), (24, 2000, 8000),
+                                   (256, 1000, 4097), (400, 256, 3001)])
 def test_tn_q8_large(g, m, n, k):
     rng = np.random.default_rng(m + n + k)
     codes, scales, x = q8_case(rng, k, n, False)
