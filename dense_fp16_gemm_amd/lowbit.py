@@ -17,7 +17,24 @@ from __future__ import annotations
 
 import ctypes
 
-from . import GemmError, _check, _on_device, _stream_handle, gemm_f16_device_cus, load
+from . import GemmError, _check, gemm_f16_device_cus, load
+
+# torch, and what the calls below use of it: bound with the first matrix, since
+# importing this package does not import torch
+torch = None
+
+
+def _bind_torch() -> None:
+    global torch, _f16, _current_device, _raw_stream
+    import torch as t
+
+    _f16 = t.float16
+    _current_device = t.cuda.current_device
+    # the raw handle without building a Stream object, where torch has the query
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: t.cuda.current_stream(index).cuda_stream)
+    torch = t
+
 
 LOWBIT_DECODE, LOWBIT_STREAM, LOWBIT_TILE = 0, 1, 2
 Q8_GROUP = 32
@@ -127,25 +144,27 @@ class W4Matrix:
     __slots__ = ("words", "scales", "n", "k", "group")
 
     def __init__(self, words, scales, n: int, k: int, group: int):
-        import torch
-
+        if torch is None:
+            _bind_torch()
         if group not in W4_GROUPS:
             raise ValueError(f"group must be one of {W4_GROUPS}, not {group!r}")
         if n < 0 or k < 0:
             raise ValueError(f"negative size: n={n}, k={k}")
         if words.dtype != torch.int32 or scales.dtype != torch.float16:
             raise TypeError("words must be torch.int32 and scales torch.float16")
-        nb, kt = -(-n // 16), -(-k // 128)
-        if tuple(words.shape) != (nb, kt, 64, 4) or \
-                tuple(scales.shape) != (nb, 128 * kt // group, 16):
+        words_shape, scales_shape = _w4_shapes(n, k, group)
+        if tuple(words.shape) != words_shape or tuple(scales.shape) != scales_shape:
             raise ValueError(f"words{tuple(words.shape)} and scales{tuple(scales.shape)} are not "
                              f"those of a {n} x {k} matrix with groups of {group}")
         if not words.is_cuda or words.device != scales.device:
             raise ValueError("words and scales must be on the same GPU")
         if not (words.is_contiguous() and scales.is_contiguous()):
             raise ValueError("words and scales must be contiguous")
-        self.words, self.scales = words, scales
-        self.n, self.k, self.group = int(n), int(k), int(group)
+        self._set(words, scales, int(n), int(k), int(group))
+
+    def _set(self, words, scales, n, k, group):
+        self.words, self.scales, self.n, self.k, self.group = words, scales, n, k, group
+        return self
 
     @property
     def shape(self) -> tuple[int, int]:
@@ -163,6 +182,11 @@ class W4Matrix:
         return f"W4Matrix({self.n} x {self.k}, group={self.group}, device={self.device})"
 
 
+def _w4_shapes(n: int, k: int, group: int) -> tuple[tuple, tuple]:
+    nb, kt = -(-n // 16), -(-k // 128)
+    return (nb, kt, 64, 4), (nb, 128 * kt // group, 16)
+
+
 class Q8Matrix:
     """An [r, n] matrix in Q8 storage: codes int8 [r, 32 ceil(n / 32)] and
     scales fp16 [r, ceil(n / 32)], as quantize_q8() makes them.  The tensors
@@ -171,8 +195,8 @@ class Q8Matrix:
     __slots__ = ("codes", "scales", "r", "n")
 
     def __init__(self, codes, scales, n: int):
-        import torch
-
+        if torch is None:
+            _bind_torch()
         if n < 0:
             raise ValueError(f"negative size: n={n}")
         if codes.dtype != torch.int8 or scales.dtype != torch.float16:
@@ -186,8 +210,11 @@ class Q8Matrix:
             raise ValueError("codes and scales must be on the same GPU")
         if not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        self.codes, self.scales = codes, scales
-        self.r, self.n = int(codes.shape[0]), int(n)
+        self._set(codes, scales, int(codes.shape[0]), int(n))
+
+    def _set(self, codes, scales, r, n):
+        self.codes, self.scales, self.r, self.n = codes, scales, r, n
+        return self
 
     @property
     def shape(self) -> tuple[int, int]:
@@ -221,15 +248,14 @@ def _matrix(x, dtype, what: str):
     return x.shape
 
 
-def _same_device(x, y, what: str) -> None:
-    if x.get_device() != y.get_device():
-        raise ValueError(f"{what} must be on the same GPU")
-
-
-def _call(on, stream, fn, *args) -> None:
-    """fn(*args, stream) on the device of the tensor `on`."""
-    with _on_device(on):
-        status = fn(*args, _stream_handle(on, stream))
+def _call(index, stream, fn, *args) -> None:
+    """fn(*args, stream) on device `index`."""
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _current_device():
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, s)
     if status:
         raise GemmError(status, fn.__name__)
 
@@ -238,8 +264,6 @@ def _new(on, stream, shape, dtype):
     """Memory on the device of `on` that belongs to the stream it will be used on."""
     if stream is None:
         return on.new_empty(shape, dtype=dtype)
-    import torch
-
     if stream.device != on.device:
         raise ValueError(f"stream is on {stream.device}, the operands on {on.device}")
     with torch.cuda.stream(stream):
@@ -254,36 +278,32 @@ def _record(stream, *tensors) -> None:
 
 
 def _output(out, on, stream, shape):
-    import torch
-
     if out is None:
-        return _new(on, stream, shape, torch.float16)
+        return _new(on, stream, shape, _f16)
     if stream is not None and stream.device != on.device:
         raise ValueError(f"stream is on {stream.device}, the operands on {on.device}")
-    if out.dtype != torch.float16 or tuple(out.shape) != shape or not out.is_contiguous() or \
+    if out.dtype != _f16 or tuple(out.shape) != shape or not out.is_contiguous() or \
             out.device != on.device:
         raise ValueError(f"out must be a contiguous float16 {list(shape)} tensor on {on.device}")
     return out
 
 
 def _new_w4(on, stream, n: int, k: int, group: int) -> W4Matrix:
-    import torch
-
     if group not in W4_GROUPS:
         raise ValueError(f"group must be one of {W4_GROUPS}, not {group!r}")
-    nb, kt = -(-n // 16), -(-k // 128)
-    return W4Matrix(_new(on, stream, (nb, kt, 64, 4), torch.int32),
-                    _new(on, stream, (nb, 128 * kt // group, 16), torch.float16), n, k, group)
+    words, scales = _w4_shapes(n, k, group)
+    return W4Matrix.__new__(W4Matrix)._set(_new(on, stream, words, torch.int32),
+                                           _new(on, stream, scales, _f16), n, k, int(group))
 
 
 def quantize_w4(w, group: int = 128, stream=None) -> W4Matrix:
     """w [N, K] fp16 in 4-bit codes, a scale for each `group` weights of a row."""
-    import torch
-
-    n, k = _matrix(w, torch.float16, "w")
+    if torch is None:
+        _bind_torch()
+    n, k = _matrix(w, _f16, "w")
     q = _new_w4(w, stream, n, k, group)
-    _call(w, stream, load().gemm_f16_w4_quantize, n, k, group, w.data_ptr(), q.words.data_ptr(),
-          q.scales.data_ptr())
+    _call(w.get_device(), stream, load().gemm_f16_w4_quantize, n, k, group, w.data_ptr(),
+          q.words.data_ptr(), q.scales.data_ptr())
     if stream is not None:
         _record(stream, w)
     return q
@@ -294,15 +314,16 @@ def pack_w4(codes, scales, group: int = 128, stream=None) -> W4Matrix:
     [N, ceil(K / group)] fp16, weight = code * scale.  Scales are rounded to 8
     significant bits; a group that cannot be held (a code out of range, a scale
     that is not finite, a weight past 65504) becomes NaN."""
-    import torch
-
+    if torch is None:
+        _bind_torch()
     n, k = _matrix(codes, torch.int8, "codes")
     q = _new_w4(codes, stream, n, k, group)
-    if tuple(_matrix(scales, torch.float16, "scales")) != (n, -(-k // group)):
+    if tuple(_matrix(scales, _f16, "scales")) != (n, -(-k // group)):
         raise ValueError(f"scales{tuple(scales.shape)} do not fit codes{tuple(codes.shape)} in "
                          f"groups of {group}")
-    _same_device(codes, scales, "codes and scales")
-    _call(codes, stream, load().gemm_f16_w4_pack, n, k, group, codes.data_ptr(),
+    if codes.device != scales.device:
+        raise ValueError("codes and scales must be on the same GPU")
+    _call(codes.get_device(), stream, load().gemm_f16_w4_pack, n, k, group, codes.data_ptr(),
           scales.data_ptr(), q.words.data_ptr(), q.scales.data_ptr())
     if stream is not None:
         _record(stream, codes, scales)
@@ -315,8 +336,8 @@ def dequantize_w4(w: W4Matrix, out=None, stream=None):
         raise TypeError("w must be a W4Matrix")
     words = w.words
     out = _output(out, words, stream, (w.n, w.k))
-    _call(words, stream, load().gemm_f16_w4_dequantize, w.n, w.k, w.group, words.data_ptr(),
-          w.scales.data_ptr(), out.data_ptr())
+    _call(words.get_device(), stream, load().gemm_f16_w4_dequantize, w.n, w.k, w.group,
+          words.data_ptr(), w.scales.data_ptr(), out.data_ptr())
     if stream is not None:
         _record(stream, words, w.scales, out)
     return out
@@ -324,17 +345,17 @@ def dequantize_w4(w: W4Matrix, out=None, stream=None):
 
 def quantize_q8(x, stream=None) -> Q8Matrix:
     """x [R, N] fp16 in 8-bit codes, a scale for each 32 values of a row."""
-    import torch
-
-    r, n = _matrix(x, torch.float16, "x")
+    if torch is None:
+        _bind_torch()
+    r, n = _matrix(x, _f16, "x")
     groups = -(-n // Q8_GROUP)
-    q = Q8Matrix(_new(x, stream, (r, groups * Q8_GROUP), torch.int8),
-                 _new(x, stream, (r, groups), torch.float16), n)
-    _call(x, stream, load().gemm_f16_q8_quantize, r, n, x.data_ptr(), q.codes.data_ptr(),
-          q.scales.data_ptr())
+    codes = _new(x, stream, (r, groups * Q8_GROUP), torch.int8)
+    scales = _new(x, stream, (r, groups), _f16)
+    _call(x.get_device(), stream, load().gemm_f16_q8_quantize, r, n, x.data_ptr(),
+          codes.data_ptr(), scales.data_ptr())
     if stream is not None:
         _record(stream, x)
-    return q
+    return Q8Matrix.__new__(Q8Matrix)._set(codes, scales, r, n)
 
 
 def dequantize_q8(x: Q8Matrix, out=None, stream=None):
@@ -343,7 +364,7 @@ def dequantize_q8(x: Q8Matrix, out=None, stream=None):
         raise TypeError("x must be a Q8Matrix")
     codes = x.codes
     out = _output(out, codes, stream, (x.r, x.n))
-    _call(codes, stream, load().gemm_f16_q8_dequantize, x.r, x.n, codes.data_ptr(),
+    _call(codes.get_device(), stream, load().gemm_f16_q8_dequantize, x.r, x.n, codes.data_ptr(),
           x.scales.data_ptr(), out.data_ptr())
     if stream is not None:
         _record(stream, codes, x.scales, out)
@@ -355,21 +376,23 @@ def dequantize_q8(x: Q8Matrix, out=None, stream=None):
 _workspace_bytes: dict = {}
 
 
-def _workspace(key, on, workspace, stream):
-    """(tensor or None, its address, its bytes) for a product planned by
-    key[0](*key[1:-1], compute units)."""
+def _workspace_need(key) -> int:
+    """The bytes that key[0](*key[1:-1], compute units of device key[-1]) plans."""
     need = _workspace_bytes.get(key)
     if need is None:
-        with _on_device(on):
+        with torch.cuda.device(key[-1]):
             need = key[0](*key[1:-1], gemm_f16_device_cus()).workspace_bytes
         if len(_workspace_bytes) >= 1024:
             _workspace_bytes.clear()
         _workspace_bytes[key] = need
+    return need
+
+
+def _workspace(need, on, workspace, stream):
+    """(tensor or None, its address, its bytes)."""
     if workspace is None:
         if not need:
             return None, 0, 0
-        import torch
-
         workspace = _new(on, stream, (need,), torch.uint8)
         return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != on.device or not workspace.is_contiguous():
@@ -381,19 +404,19 @@ def gemm_nt_w4(a, w: W4Matrix, out=None, workspace=None, stream=None):
     """C = a @ W.T for a [M, K] fp16 and W [N, K] in 4 bits, fp16 [M, N]
     (gemm_f16_nt_w4).  The workspace that some sizes need (see
     gemm_f16_nt_w4_plan) is allocated with torch unless `workspace` is given."""
-    import torch
-
     if not isinstance(w, W4Matrix):
         raise TypeError("w must be a W4Matrix")
-    m, k = _matrix(a, torch.float16, "a")
+    m, k = _matrix(a, _f16, "a")
     n, words = w.n, w.words
     if k != w.k:
         raise ValueError(f"shape mismatch: a{tuple(a.shape)} w{w.shape}")
-    _same_device(a, words, "a and w")
+    index = a.get_device()
+    if index != words.get_device():
+        raise ValueError("a and w must be on the same GPU")
     out = _output(out, a, stream, (m, n))
-    ws, ws_ptr, ws_bytes = _workspace((gemm_f16_nt_w4_plan, m, n, k, w.group, a.get_device()), a,
-                                      workspace, stream)
-    _call(a, stream, load().gemm_f16_nt_w4, m, n, k, w.group, a.data_ptr(), words.data_ptr(),
+    ws, ws_ptr, ws_bytes = _workspace(
+        _workspace_need((gemm_f16_nt_w4_plan, m, n, k, w.group, index)), a, workspace, stream)
+    _call(index, stream, load().gemm_f16_nt_w4, m, n, k, w.group, a.data_ptr(), words.data_ptr(),
           w.scales.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes)
     if stream is not None:
         _record(stream, a, words, w.scales, out, ws)
@@ -405,19 +428,19 @@ def gemm_tn_q8(a, x: Q8Matrix, out=None, workspace=None, stream=None):
     (gemm_f16_tn_q8): with a the gradient of a linear layer's output and X its
     kept input, the gradient of its [M, N] weight.  Workspace as for
     gemm_nt_w4."""
-    import torch
-
     if not isinstance(x, Q8Matrix):
         raise TypeError("x must be a Q8Matrix")
-    k, m = _matrix(a, torch.float16, "a")
+    k, m = _matrix(a, _f16, "a")
     n, codes = x.n, x.codes
     if k != x.r:
         raise ValueError(f"shape mismatch: a{tuple(a.shape)} x{x.shape}")
-    _same_device(a, codes, "a and x")
+    index = a.get_device()
+    if index != codes.get_device():
+        raise ValueError("a and x must be on the same GPU")
     out = _output(out, a, stream, (m, n))
-    ws, ws_ptr, ws_bytes = _workspace((gemm_f16_tn_q8_plan, m, n, k, a.get_device()), a, workspace,
-                                      stream)
-    _call(a, stream, load().gemm_f16_tn_q8, m, n, k, a.data_ptr(), codes.data_ptr(),
+    ws, ws_ptr, ws_bytes = _workspace(
+        _workspace_need((gemm_f16_tn_q8_plan, m, n, k, index)), a, workspace, stream)
+    _call(index, stream, load().gemm_f16_tn_q8, m, n, k, a.data_ptr(), codes.data_ptr(),
           x.scales.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes)
     if stream is not None:
         _record(stream, a, codes, x.scales, out, ws)
