@@ -1315,7 +1315,8 @@ static int w4_shape(int64_t N, int64_t K, int32_t group, W4Shape *s)
 {
     if (N < 0 || K < 0) return GEMM_F16_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return GEMM_F16_INVALID_ARG;
-    if (N > INT32_MAX || K > INT32_MAX) return GEMM_F16_UNSUPPORTED;
+    // the kernels count in whole tiles past the end in 32 bits
+    if (N > INT32_MAX - 127 || K > INT32_MAX - 127) return GEMM_F16_UNSUPPORTED;
     s->nb = cdiv(N, 16);
     s->kt = cdiv(K, 128);
     s->tiles = s->nb * s->kt;

@@ -62,7 +62,7 @@ extern "C" {
  *
  * gemm_f16_w4_sizes: pure host function, the bytes of both arrays.
  * GEMM_F16_INVALID_ARG for NULL outputs, negative sizes or a group other than
- * 32, 64 and 128; GEMM_F16_UNSUPPORTED for N or K above 2^31 - 1 or more than
+ * 32, 64 and 128; GEMM_F16_UNSUPPORTED for N or K above 2^31 - 128 or more than
  * 2^31 - 1 tiles.
  *
  * gemm_f16_w4_quantize: W fp16 [N, K] row-major (any 2-byte alignment) to

@@ -268,6 +268,68 @@ def test_tn_q8_large(g, m, n, k):
     check_product(got, a.astype(np.float64).T, x, k, False)
 
 
+def check_on_gpu(got, a, b, k):
+    """check_product for large sizes: the 64-bit product on the GPU."""
+    import torch
+
+    a, b = a.double(), b.double()
+    want = torch.matmul(a, b)
+    fp32 = (k / 4 + k / 32 + 72) * 2.0 ** -24 * torch.matmul(a.abs(), b.abs())   # see product_bound
+    bound = fp32 + (want.abs() + fp32) * 2.0 ** -11 + 2.0 ** -25
+    bad = ~((got.double() - want).abs() <= bound)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}"
+
+
+# a shape for each kernel of the planner's table on 256 compute units, unsplit
+# and split: (kernel, rows, columns, waves), then M, N, K
+W4_KERNELS = [((1, 4, 16, 8), 3, 500, 1000), ((1, 8, 16, 8), 5, 500, 3000),
+              ((1, 8, 32, 8), 7, 6500, 700), ((1, 16, 16, 8), 12, 500, 3000),
+              ((1, 16, 32, 8), 16, 6500, 700), ((1, 16, 64, 8), 9, 12800, 520),
+              ((2, 32, 128, 4), 17, 16, 32), ((2, 32, 128, 4), 30, 1000, 1024),
+              ((2, 32, 256, 4), 17, 16384, 8000), ((2, 48, 256, 4), 333, 6500, 32),
+              ((2, 48, 256, 4), 80, 6500, 2048), ((2, 64, 128, 4), 80, 12800, 32),
+              ((2, 64, 128, 4), 384, 300, 4096), ((2, 64, 256, 4), 160, 12800, 8000),
+              ((2, 96, 256, 8), 333, 12800, 32), ((2, 96, 256, 8), 80, 6500, 8000),
+              ((2, 112, 256, 8), 512, 12800, 32), ((2, 112, 256, 8), 333, 2000, 8000),
+              ((2, 128, 256, 8), 512, 16384, 32), ((2, 128, 256, 8), 120, 12800, 4096),
+              ((0,), 1500, 14336, 4096)]
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("kernel,m,n,k", W4_KERNELS)
+def test_nt_w4_every_kernel(g, kernel, m, n, k, group):
+    import torch
+
+    plan = g.gemm_f16_nt_w4_plan(m, n, k, group, 256)
+    assert (plan.kernel, plan.block_m, plan.block_n, plan.waves)[:len(kernel)] == kernel
+    gen = torch.Generator(device="cuda").manual_seed(m + n + k)
+    codes = torch.randint(-8, 8, (n, k), generator=gen, device="cuda", dtype=torch.int8)
+    # one row's scales past 2720, where the tile kernels unpack otherwise
+    scales = torch.rand(n, -(-k // group), generator=gen, device="cuda") + 0.5
+    scales[n // 2] *= 4000.0
+    q = g.pack_w4(codes, scales.half(), group)
+    a = (torch.randn(m, k, generator=gen, device="cuda") / k).half()
+    check_on_gpu(g.gemm_nt_w4(a, q), a, g.dequantize_w4(q).t(), k)
+
+
+Q8_KERNELS = [((1, 16, 128, 4), 7, 1000, 5), ((1, 16, 128, 4), 16, 300, 500),
+              ((1, 16, 256, 4), 10, 14336, 8192), ((1, 32, 128, 4), 17, 320, 30),
+              ((1, 32, 128, 4), 32, 1000, 1500), ((1, 64, 128, 4), 50, 320, 30),
+              ((1, 64, 128, 4), 130, 1000, 4000), ((0,), 600, 320, 1024)]
+
+
+@pytest.mark.parametrize("kernel,m,n,k", Q8_KERNELS)
+def test_tn_q8_every_kernel(g, kernel, m, n, k):
+    import torch
+
+    plan = g.gemm_f16_tn_q8_plan(m, n, k, 256)
+    assert (plan.kernel, plan.block_m, plan.block_n, plan.waves)[:len(kernel)] == kernel
+    gen = torch.Generator(device="cuda").manual_seed(m + n + k)
+    x = g.quantize_q8(torch.randn(k, n, generator=gen, device="cuda").half())
+    a = (torch.randn(k, m, generator=gen, device="cuda") / k).half()
+    check_on_gpu(g.gemm_tn_q8(a, x), a.t().contiguous(), g.dequantize_q8(x), k)
+
+
 @pytest.mark.parametrize("m", [1, 16, 40, 100, 1200])
 def test_nt_w4_special_values(g, m):
     """Infinities and NaN reach the results that the definition gives them, and

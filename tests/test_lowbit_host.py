@@ -41,7 +41,7 @@ def test_w4_sizes(g, n, k, group, words, scales):
 
 @pytest.mark.parametrize("n,k,group,status", [
     (-1, 1, 32, 1), (1, -1, 32, 1), (1, 1, 16, 1), (1, 1, 0, 1), (1, 1, 256, 1),
-    (2 ** 31, 1, 32, 2), (1, 2 ** 31, 32, 2), (2 ** 31 - 1, 2 ** 31 - 1, 32, 2),
+    (2 ** 31, 1, 32, 2), (1, 2 ** 31, 32, 2), (2 ** 31 - 127, 1, 32, 2), (1, 2 ** 31 - 127, 32, 2), (2 ** 31 - 1, 2 ** 31 - 1, 32, 2),
 ])
 def test_w4_sizes_refused(g, n, k, group, status):
     with pytest.raises(g.GemmError) as e:
