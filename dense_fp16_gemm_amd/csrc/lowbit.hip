@@ -289,7 +289,7 @@ struct W4DecodeParams {
     const u32x4_t *words;
     const uint16_t *scales;
     uint16_t *W;
-    int32_t N, K, kt, tiles;
+    int32_t N, K, ld, kt, tiles;   // W's rows start every ld values; up to ld they are written
     int32_t shift;
 };
 
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_decode_kernel(W4DecodeParams p)
         for (int j = 0; j < 4; ++j) {
             const int64_t c = static_cast<int64_t>(t) * 128 + 32 * j + kq * 8;
             const _Float16 sj = bits_as<_Float16>(s[((32 * j) >> p.shift) * 16]);
-            if (c < p.K) store8(p.W + n * p.K, static_cast<int32_t>(c), p.K, w4_scaled(w[j], sj));
+            if (c < p.K) store8(p.W + n * p.ld, static_cast<int32_t>(c), p.ld, w4_scaled(w[j], sj));
         }
     }
 }
@@ -870,18 +870,26 @@ __global__ __launch_bounds__(256) void w4_join_kernel(W4JoinParams p)
     store4(p.C, p.M, p.N, m, n, sum);
 }
 
-// A with rows of lda columns, lda a multiple of 8: for an A whose rows are not
-// all 16-byte aligned, which the direct-to-LDS loads need.
-__global__ __launch_bounds__(256) void align_rows_kernel(const uint16_t *A, uint16_t *to,
-                                                         int32_t M, int32_t K, int32_t lda)
+// Rows of `cols` values from one pitch to another; those from `cols` up to
+// `limit` become zeros.  For a matrix whose rows are not all 16-byte aligned,
+// which direct-to-LDS loads need, and back.
+struct CopyRowsParams {
+    const uint16_t *from;
+    uint16_t *to;
+    int64_t rows;
+    int32_t ld_from, ld_to, cols, limit;
+};
+
+__global__ __launch_bounds__(256) void copy_rows_kernel(CopyRowsParams p)
 {
-    const int32_t chunks = lda / 8;
-    const int64_t count = static_cast<int64_t>(M) * chunks;
+    const int32_t chunks = (p.limit + 7) / 8;
+    const int64_t count = p.rows * chunks;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count;
          i += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t row = i / chunks;
         const int32_t c = static_cast<int32_t>(i - row * chunks) * 8;
-        *reinterpret_cast<u32x4_t *>(to + row * lda + c) = load8(A + row * K, c, K);
+        store8(p.to + row * p.ld_to, c, p.limit,
+               bits_as<half8_t>(load8(p.from + row * p.ld_from, c, p.cols)));
     }
 }
 
@@ -900,6 +908,7 @@ struct Q8Params {
     u32x2_t *codes;           // 8 codes each, 4 Ng a row
     uint16_t *scales;
     int32_t R, N, chunks;     // chunks of 8 columns a row: 4 Ng
+    int32_t ld;               // out's rows start every ld values; up to ld they are written
     int32_t tx_shift, col_blocks;
 };
 
@@ -1009,7 +1018,7 @@ __global__ __launch_bounds__(64 * WAVES) void q8_decode_kernel(Q8Params p)
         half8_t h;
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = x[e / 2][e % 2];
-        store8(p.out + row * p.N, static_cast<int32_t>(c), p.N, h);
+        store8(p.out + row * p.ld, static_cast<int32_t>(c), p.ld, h);
     }
 }
 
@@ -1024,8 +1033,8 @@ __global__ __launch_bounds__(64 * WAVES) void q8_decode_kernel(Q8Params p)
 // an fp16 number by v_perm_b32, one XOR (its bias and the magic exponent), one
 // subtraction and the product with its scale: exact, two operations a value.
 // A's rows and the scales of a step go through LDS of the wave's own, which
-// turns them round.  The waves' sums meet in LDS, the ranges' in the workspace;
-// q8_join_kernel adds those up in order.
+// turns them round.  The waves' sums meet in LDS, those of several ranges in the
+// workspace, where q8_join_kernel adds them up in order.
 //
 // HBM bounds it, after the launches' 5 us.  CB = 16 reads the most a step
 // (268 MB of codes at 4.8 TB/s, with CB = 8 4.1), CB = 8 makes fewer ranges of
@@ -1038,9 +1047,10 @@ struct Q8TnParams {
     const uint16_t *A;         // [T, M]
     const uint8_t *codes;      // [T, 32 ng]
     const uint16_t *scales;    // [T, ng]
-    float *partial;
+    uint16_t *C;               // [M, N]: written here where there is one range,
+    float *partial;            // which is nullptr then
     int64_t stride;            // values between two ranges' sums
-    int32_t T, M, ng;
+    int32_t T, M, N, ng;
     int32_t blocks, m_tiles;   // blocks of 16 CB columns, tiles of 16 MT rows of C
     int32_t t_split;           // rows of X a range, a multiple of 32
 };
@@ -1204,8 +1214,12 @@ __global__ __launch_bounds__(64 * W, 2) void q8_tn_kernel(Q8TnParams p)
     // sum idx = (mt, e, reg) of lane l: row m0 + 16 mt + r of C, column (block 16 + 4 kq + reg) CB + e
     constexpr int ROUNDS = SUMS / ROUND, PER = ROUND / W;
     static_assert(SUMS % ROUND == 0 && ROUND % W == 0, "rounds");
-    float *to = p.partial + sp * p.stride +
-                (static_cast<int64_t>(block) * p.m_tiles + mtile) * (SUMS * 64) + lane;
+    constexpr int EW = PER / 4;   // e's of a wave and round
+    static_assert(PER % 4 == 0, "a wave takes all four regs of an e");
+    float *to = nullptr;
+    if (p.partial)
+        to = p.partial + sp * p.stride +
+             (static_cast<int64_t>(block) * p.m_tiles + mtile) * (SUMS * 64) + lane;
 #pragma unroll
     for (int rd = 0; rd < ROUNDS; ++rd) {
         __syncthreads();
@@ -1216,11 +1230,25 @@ __global__ __launch_bounds__(64 * W, 2) void q8_tn_kernel(Q8TnParams p)
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            float sum = 0.0f;
+        for (int reg = 0; reg < 4; ++reg) {
+            float sum[EW];
 #pragma unroll
-            for (int w = 0; w < W; ++w) sum += lds.red[w][wave * PER + k][lane];
-            to[(rd * ROUND + wave * PER + k) * 64] = sum;
+            for (int e = 0; e < EW; ++e) {
+                const int k = wave * PER + 4 * e + reg;
+                sum[e] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) sum[e] += lds.red[w][k][lane];
+                if (to) to[(rd * ROUND + k) * 64] = sum[e];
+            }
+            if (to) continue;
+            const int e0 = rd * (ROUND / 4) + wave * EW;   // over all mt
+            const int32_t m = m0 + e0 / CB * 16 + r;
+            const int64_t n = (static_cast<int64_t>(block) * 16 + 4 * kq + reg) * CB + e0 % CB;
+            if (m >= p.M) continue;
+            _Float16 *c = reinterpret_cast<_Float16 *>(p.C) + static_cast<int64_t>(m) * p.N + n;
+#pragma unroll
+            for (int e = 0; e < EW; ++e)
+                if (n + e < p.N) c[e] = static_cast<_Float16>(sum[e]);
         }
     }
 }
@@ -1359,7 +1387,7 @@ static int w4_encode(int64_t N, int64_t K, int32_t group, const void *W, const v
 }
 
 static int w4_decode(int64_t N, int64_t K, const W4Shape &s, const void *words,
-                     const void *scales, void *W, hipStream_t stream)
+                     const void *scales, void *W, int64_t ld, hipStream_t stream)
 {
     W4DecodeParams p;
     p.words = static_cast<const u32x4_t *>(words);
@@ -1367,6 +1395,7 @@ static int w4_decode(int64_t N, int64_t K, const W4Shape &s, const void *words,
     p.W = static_cast<uint16_t *>(W);
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
+    p.ld = static_cast<int32_t>(ld);
     p.kt = static_cast<int32_t>(s.kt);
     p.tiles = static_cast<int32_t>(s.tiles);
     p.shift = s.shift;
@@ -1389,7 +1418,8 @@ static int q8_shape(int64_t R, int64_t N, Q8Shape *s)
 }
 
 static int q8_launch(const void *fn, int64_t R, int64_t N, const Q8Shape &s, const void *X,
-                     void *out, const void *codes, const void *scales, hipStream_t stream)
+                     void *out, int64_t ld, const void *codes, const void *scales,
+                     hipStream_t stream)
 {
     Q8Params p;
     p.X = static_cast<const uint16_t *>(X);
@@ -1399,6 +1429,7 @@ static int q8_launch(const void *fn, int64_t R, int64_t N, const Q8Shape &s, con
     p.R = static_cast<int32_t>(R);
     p.N = static_cast<int32_t>(N);
     p.chunks = static_cast<int32_t>(s.groups * 4);
+    p.ld = static_cast<int32_t>(ld);
     p.tx_shift = 2;
     while (p.tx_shift < 6 && (1 << p.tx_shift) < p.chunks) ++p.tx_shift;
     const int64_t col_blocks = cdiv(p.chunks, int64_t(1) << p.tx_shift);
@@ -1409,25 +1440,86 @@ static int q8_launch(const void *fn, int64_t R, int64_t N, const Q8Shape &s, con
 }
 
 // ---- products ---------------------------------------------------------------
-// Decode: the operand in fp16 at the workspace's start, then what the GEMM's
-// own split over K needs.
+static int copy_rows(const void *from, int64_t ld_from, void *to, int64_t ld_to, int64_t rows,
+                     int64_t cols, int64_t limit, hipStream_t stream)
+{
+    CopyRowsParams p;
+    p.from = static_cast<const uint16_t *>(from);
+    p.to = static_cast<uint16_t *>(to);
+    p.rows = rows;
+    p.ld_from = static_cast<int32_t>(ld_from);
+    p.ld_to = static_cast<int32_t>(ld_to);
+    p.cols = static_cast<int32_t>(cols);
+    p.limit = static_cast<int32_t>(limit);
+    return launch(reinterpret_cast<const void *>(&copy_rows_kernel),
+                  std::min<int64_t>(cdiv(rows * cdiv(limit, 8), 256), 1 << 16), 256, &p, stream);
+}
+
+// Decode: the low-bit operand in fp16, then the library's fp16 GEMM.  The
+// GEMM's fast kernels need rows of a multiple of 8 values, so the fp16 operand
+// gets such rows, A a copy where it has none, and C a padded one where its
+// columns (A^T X: or rows) are not a multiple of 8.  (The GEMM's kernels for
+// other rows run at a fraction of the rate: C = A^T X of 1069 x 463 over 2357
+// rows took 160 us.)  An A whose address is not 16-byte aligned takes those all
+// the same.
+struct Decode {
+    int64_t M, N, K;                  // the GEMM's sizes
+    int64_t b, a, c, split;           // offsets in the workspace: operand, A, C, partial sums
+    int64_t bytes;
+    int32_t splits;
+    gemm_f16_nt_plan_t plan;
+};
+
+static int decode_layout(int64_t M, int64_t N, int64_t K, int32_t num_cus, bool tn, Decode *d)
+{
+    d->M = tn ? round_up(M, 8) : M;
+    d->N = tn ? round_up(N, 8) : N;
+    d->K = tn ? K : round_up(K, 8);
+    int64_t ws = 0;
+    const int v = tn ? gemm_f16_tn_splitk_plan(d->M, d->N, d->K, num_cus, 0, &d->plan, &d->splits, &ws)
+                     : gemm_f16_nt_splitk_plan(d->M, d->N, d->K, num_cus, 0, &d->plan, &d->splits, &ws);
+    if (v != GEMM_F16_OK) return v;
+    d->b = 0;
+    d->a = round_up(d->N * d->K * 2, 256);
+    d->c = d->a + ((tn ? d->M != M : d->K != K) ? round_up(d->M * d->K * 2, 256) : 0);
+    d->split = d->c + (d->M != M || d->N != N ? round_up(d->M * d->N * 2, 256) : 0);
+    d->bytes = d->split + ws;
+    return GEMM_F16_OK;
+}
+
 static int decode_plan(int64_t M, int64_t N, int64_t K, int32_t num_cus, bool tn,
                        gemm_f16_lowbit_plan_t *plan)
 {
-    gemm_f16_nt_plan_t g;
-    int32_t splits = 1;
-    int64_t ws = 0;
-    const int v = tn ? gemm_f16_tn_splitk_plan(M, N, K, num_cus, 0, &g, &splits, &ws)
-                     : gemm_f16_nt_splitk_plan(M, N, K, num_cus, 0, &g, &splits, &ws);
+    Decode d;
+    const int v = decode_layout(M, N, K, num_cus, tn, &d);
     if (v != GEMM_F16_OK) return v;
     plan->kernel = GEMM_F16_LOWBIT_DECODE;
-    plan->block_m = g.block_m;
-    plan->block_n = g.block_n;
-    plan->waves = g.waves;
-    plan->splits = splits;
-    plan->grid = g.grid;
-    plan->workspace_bytes = round_up(N * K * 2, 256) + ws;
+    plan->block_m = d.plan.block_m;
+    plan->block_n = d.plan.block_n;
+    plan->waves = d.plan.waves;
+    plan->splits = d.splits;
+    plan->grid = d.plan.grid;
+    plan->workspace_bytes = d.bytes;
     return GEMM_F16_OK;
+}
+
+// The GEMM, after the operand is written to the workspace's start.
+static int decode_gemm(const Decode &d, int64_t M, int64_t N, int64_t K, bool tn, const void *A,
+                       void *C, char *ws, hipStream_t stream)
+{
+    const int64_t cols = tn ? M : K, ld = tn ? d.M : d.K, rows = tn ? K : M;
+    int v = GEMM_F16_OK;
+    if (ld != cols) {
+        v = copy_rows(A, cols, ws + d.a, ld, rows, cols, ld, stream);
+        A = ws + d.a;
+    }
+    if (v != GEMM_F16_OK) return v;
+    const bool padded = d.M != M || d.N != N;
+    void *out = padded ? ws + d.c : C;
+    v = tn ? gemm_f16_tn_splitk(d.M, d.N, d.K, A, ws, out, 0, ws + d.split, d.bytes - d.split, stream)
+           : gemm_f16_nt_splitk(d.M, d.N, d.K, A, ws, out, 0, ws + d.split, d.bytes - d.split, stream);
+    if (v != GEMM_F16_OK || !padded) return v;
+    return copy_rows(out, d.N, C, N, M, N, N, stream);
 }
 
 // The kernels of the product with 4-bit weights that read the words directly,
@@ -1591,16 +1683,15 @@ static int w4_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t num_c
 
 static int w4_run(const W4Choice &c, const gemm_f16_lowbit_plan_t &plan, int64_t M, int64_t N,
                   int64_t K, const W4Shape &s, const void *A, const void *words,
-                  const void *scales, void *C, void *workspace, int64_t workspace_bytes,
-                  hipStream_t stream)
+                  const void *scales, void *C, void *workspace, int32_t cus, hipStream_t stream)
 {
+    char *ws = static_cast<char *>(workspace);
     if (c.id < 0) {
-        const int v = w4_decode(N, K, s, words, scales, workspace, stream);
-        if (v != GEMM_F16_OK) return v;
-        const int64_t used = round_up(N * K * 2, 256);
-        return gemm_f16_nt_splitk(M, N, K, A, workspace, C, 0,
-                                  static_cast<char *>(workspace) + used, workspace_bytes - used,
-                                  stream);
+        Decode d;
+        int v = decode_layout(M, N, K, cus, false, &d);
+        if (v == GEMM_F16_OK) v = w4_decode(N, K, s, words, scales, ws + d.b, d.K, stream);
+        if (v == GEMM_F16_OK) v = decode_gemm(d, M, N, K, false, A, C, ws, stream);
+        return v;
     }
     const W4Kernel &e = kW4Kernels[c.id];
     if (e.kernel == GEMM_F16_LOWBIT_STREAM) {
@@ -1624,17 +1715,11 @@ static int w4_run(const W4Choice &c, const gemm_f16_lowbit_plan_t &plan, int64_t
     p.lda = static_cast<int32_t>(K);
     p.partial = static_cast<float *>(workspace);
     if (!w4_rows_aligned(K, A)) {
-        uint16_t *to = reinterpret_cast<uint16_t *>(
-            static_cast<char *>(workspace) + (p.splits > 1 ? p.splits * partial : 0));
+        uint16_t *to =
+            reinterpret_cast<uint16_t *>(ws + (p.splits > 1 ? p.splits * partial : 0));
         p.lda = static_cast<int32_t>(round_up(K, 8));
-        const uint16_t *from = p.A;
-        int32_t m = static_cast<int32_t>(M), k = static_cast<int32_t>(K), lda = p.lda;
-        void *args[] = {&from, &to, &m, &k, &lda};
-        const hipError_t err = hipLaunchKernel(
-            reinterpret_cast<const void *>(&align_rows_kernel),
-            dim3(static_cast<uint32_t>(std::min<int64_t>(cdiv(M * (lda / 8), 256), 4096))),
-            dim3(256), args, 0, stream);
-        if (err != hipSuccess) return GEMM_F16_LAUNCH_FAILED;
+        const int v = copy_rows(A, K, to, p.lda, M, K, p.lda, stream);
+        if (v != GEMM_F16_OK) return v;
         p.A = to;
     }
     p.words = static_cast<const u32x4_t *>(words);
@@ -1667,13 +1752,16 @@ static int w4_run(const W4Choice &c, const gemm_f16_lowbit_plan_t &plan, int64_t
 // The kernels of the product with 8-bit activations that read the codes.
 struct Q8Kernel {
     int32_t mt, cb, waves;
+    double step;           // us a step of 32 rows of X for each wave
     const void *fn;
 };
-#define Q8_TN(MT, CB, W) Q8Kernel{MT, CB, W, reinterpret_cast<const void *>(&q8_tn_kernel<MT, CB, W>)}
+#define Q8_TN(MT, CB, W, STEP) \
+    Q8Kernel{MT, CB, W, STEP, reinterpret_cast<const void *>(&q8_tn_kernel<MT, CB, W>)}
 static const Q8Kernel kQ8Kernels[] = {
-    Q8_TN(1, 8, 4), Q8_TN(1, 16, 4), Q8_TN(2, 8, 4), Q8_TN(4, 8, 4),
+    Q8_TN(1, 8, 4, 0.675), Q8_TN(1, 16, 4, 1.04), Q8_TN(2, 8, 4, 0.780), Q8_TN(4, 8, 4, 1.04),
 };
 #undef Q8_TN
+constexpr int kNumQ8Kernels = sizeof(kQ8Kernels) / sizeof(kQ8Kernels[0]);
 
 // What a product runs: an index into kQ8Kernels (-1: decode), tiles and ranges.
 struct Q8Choice {
@@ -1681,7 +1769,8 @@ struct Q8Choice {
     int64_t blocks, m_tiles, t_split, splits;
 };
 
-static Q8Choice q8_layout(int32_t id, int64_t M, int64_t K, const Q8Shape &s, int32_t cus)
+static Q8Choice q8_layout(int32_t id, int64_t M, int64_t K, const Q8Shape &s, int32_t cus,
+                          bool split)
 {
     const Q8Kernel &e = kQ8Kernels[id];
     Q8Choice c;
@@ -1690,33 +1779,46 @@ static Q8Choice q8_layout(int32_t id, int64_t M, int64_t K, const Q8Shape &s, in
     c.m_tiles = cdiv(M, 16 * e.mt);
     // one workgroup a CU, where the rows suffice for a step for each wave
     const int64_t steps = cdiv(K, 32);
-    const int64_t want = std::max<int64_t>(1, cus / (c.blocks * c.m_tiles));
+    const int64_t want = split ? std::max<int64_t>(1, cus / (c.blocks * c.m_tiles)) : 1;
     const int64_t per = cdiv(steps, std::min(want, cdiv(steps, e.waves)));
     c.t_split = per * 32;
     c.splits = cdiv(steps, per);
     return c;
 }
 
-// Up to 64 rows of C the codes are read once, and streaming them won on all 54
-// shapes measured (16 to 64 rows, 256 to 14336 columns, 512 to 8192 rows of X;
-// 1.1 to 3.2 times faster than decoding).  With more rows each tile of 64
-// reads them again.  It still won where the tiles fill whole rounds of the CUs
-// to three quarters, and the sums and their join (rows times columns of C) are
-// small beside the rows of X: 128 x 4096 over 8192 rows 27 us (decoding 44),
-// 256 x 4096 over 8192 43 (49); but 320 x 4096 over 8192 68 (57), 192 x 4096
-// over 512 13 (11).
+// Streaming the codes (in one range, or in as many as fill the CUs), or
+// decoding them for the GEMM, by models of their times in us, fitted to 3,900
+// timings of 661 shapes (8 to 7668 rows of C, 64 to 14336 columns, 54 to 8192
+// rows of X, sizes that are multiples of 8 and not).  Streaming reads the codes
+// again for each tile of rows of C; it wins up to some 64 rows everywhere (1.1
+// to 3.2 times), and with hundreds of rows where the columns are few.  What the
+// models chose took 1.1% longer than the best of each shape in the mean, 34% in
+// the worst.
 static Q8Choice q8_choose(int64_t M, int64_t N, int64_t K, const Q8Shape &s, int32_t cus)
 {
-    const Q8Choice decode = {-1, 0, 0, 0, 0};
+    const double m = static_cast<double>(M), n = static_cast<double>(N), k = static_cast<double>(K);
+    Q8Choice best = {-1, 0, 0, 0, 0};
     // 32-bit counts of tiles and values in the kernels
-    if (M > 512 || s.groups > (1 << 20) || M * s.groups > (1 << 22)) return decode;
-    if (M <= 16) return q8_layout(s.codes > (int64_t(64) << 20) ? 1 : 0, M, K, s, cus);
-    if (M <= 32) return q8_layout(2, M, K, s, cus);
-    const Q8Choice c = q8_layout(3, M, K, s, cus);
-    if (M <= 64) return c;
-    const int64_t tiles = c.blocks * c.m_tiles;
-    const bool fills = tiles <= cus && 4 * (cus / tiles * tiles) >= 3 * static_cast<int64_t>(cus);
-    return fills && M * N <= 512 * K ? c : decode;
+    if (s.groups > (1 << 20) || M > (1 << 20) || M * s.groups > (1 << 26)) return best;
+    // 1 us of each workspace is the caller's, who has to get one
+    double best_us = 9.7 + 6.93e-7 * n * k + 1.68e-9 * std::max(m, 128.0) * std::max(n, 128.0) * k +
+                     1.47e-3 * k + 2.87e-7 * m * n;
+    if (M % 8 != 0) best_us += 2.97 + 7.39e-7 * m * k;                // A's copy
+    if (M % 8 != 0 || N % 8 != 0) best_us += 2.97 + 7.88e-7 * m * n;   // and C's
+    for (int32_t id = 0; id < 2 * kNumQ8Kernels; ++id) {
+        const Q8Kernel &e = kQ8Kernels[id / 2];
+        const Q8Choice c = q8_layout(id / 2, M, K, s, cus, id % 2 != 0);
+        const int64_t wgs = c.blocks * c.m_tiles * c.splits;
+        const double values = static_cast<double>(wgs) * e.mt * e.cb * 256;
+        double us = 4.03 + static_cast<double>(cdiv(wgs, cus) * cdiv(c.t_split / 32, e.waves)) * e.step;
+        us += c.splits > 1 ? 2.8 + 2.81e-6 * values + 0.0663 * static_cast<double>(c.splits)
+                           : 4.31e-6 * values;
+        if (us < best_us) {
+            best_us = us;
+            best = c;
+        }
+    }
+    return best;
 }
 
 static int q8_plan_choice(const Q8Choice &c, int64_t M, int64_t N, int64_t K, int32_t num_cus,
@@ -1730,7 +1832,8 @@ static int q8_plan_choice(const Q8Choice &c, int64_t M, int64_t N, int64_t K, in
     plan->waves = e.waves;
     plan->splits = static_cast<int32_t>(c.splits);
     plan->grid = static_cast<int32_t>(c.blocks * c.m_tiles * c.splits);
-    plan->workspace_bytes = c.blocks * c.m_tiles * c.splits * e.mt * e.cb * 1024;
+    if (c.splits > 1)
+        plan->workspace_bytes = c.blocks * c.m_tiles * c.splits * e.mt * e.cb * 1024;
     return GEMM_F16_OK;
 }
 
@@ -1749,32 +1852,35 @@ static int q8_plan(int64_t M, int64_t N, int64_t K, int32_t num_cus, gemm_f16_lo
 
 static int q8_run(const Q8Choice &c, int64_t M, int64_t N, int64_t K, const Q8Shape &s,
                   const void *A, const void *codes, const void *scales, void *C, void *workspace,
-                  int64_t workspace_bytes, hipStream_t stream)
+                  int32_t cus, hipStream_t stream)
 {
     if (c.id < 0) {
-        const int v = q8_launch(reinterpret_cast<const void *>(&q8_decode_kernel), K, N, s, nullptr,
-                                workspace, codes, scales, stream);
-        if (v != GEMM_F16_OK) return v;
-        const int64_t used = round_up(N * K * 2, 256);
-        return gemm_f16_tn_splitk(M, N, K, A, workspace, C, 0,
-                                  static_cast<char *>(workspace) + used, workspace_bytes - used,
-                                  stream);
+        char *ws = static_cast<char *>(workspace);
+        Decode d;
+        int v = decode_layout(M, N, K, cus, true, &d);
+        if (v == GEMM_F16_OK)
+            v = q8_launch(reinterpret_cast<const void *>(&q8_decode_kernel), K, N, s, nullptr,
+                          ws + d.b, d.N, codes, scales, stream);
+        if (v == GEMM_F16_OK) v = decode_gemm(d, M, N, K, true, A, C, ws, stream);
+        return v;
     }
     const Q8Kernel &e = kQ8Kernels[c.id];
     Q8TnParams p;
     p.A = static_cast<const uint16_t *>(A);
     p.codes = static_cast<const uint8_t *>(codes);
     p.scales = static_cast<const uint16_t *>(scales);
-    p.partial = static_cast<float *>(workspace);
+    p.C = static_cast<uint16_t *>(C);
+    p.partial = c.splits > 1 ? static_cast<float *>(workspace) : nullptr;
     p.stride = c.blocks * c.m_tiles * e.mt * e.cb * 256;
     p.T = static_cast<int32_t>(K);
     p.M = static_cast<int32_t>(M);
+    p.N = static_cast<int32_t>(N);
     p.ng = static_cast<int32_t>(s.groups);
     p.blocks = static_cast<int32_t>(c.blocks);
     p.m_tiles = static_cast<int32_t>(c.m_tiles);
     p.t_split = static_cast<int32_t>(c.t_split);
     const int v = launch(e.fn, c.blocks * c.m_tiles * c.splits, 64 * e.waves, &p, stream);
-    if (v != GEMM_F16_OK) return v;
+    if (v != GEMM_F16_OK || c.splits == 1) return v;
     Q8JoinParams q;
     q.partial = p.partial;
     q.C = static_cast<uint16_t *>(C);
@@ -1832,7 +1938,7 @@ extern "C" int gemm_f16_w4_dequantize(int64_t N, int64_t K, int32_t group, const
         {words, s.words, 16, false}, {scales, s.scales, 8, false}, {W, N * K * 2, 2, true}};
     const int a = check_arrays(arrays, 3);
     if (a != GEMM_F16_OK || s.tiles == 0) return a;
-    return w4_decode(N, K, s, words, scales, W, stream);
+    return w4_decode(N, K, s, words, scales, W, K, stream);
 }
 
 extern "C" int gemm_f16_nt_w4_plan(int64_t M, int64_t N, int64_t K, int32_t group,
@@ -1867,8 +1973,7 @@ extern "C" int gemm_f16_nt_w4(int64_t M, int64_t N, int64_t K, int32_t group, co
     v = w4_plan_choice(choice, M, N, K, s, cus, &plan);
     if (v != GEMM_F16_OK) return v;
     if (plan.workspace_bytes > (workspace ? workspace_bytes : 0)) return GEMM_F16_INVALID_ARG;
-    return w4_run(choice, plan, M, N, K, s, A, words, scales, C, workspace, workspace_bytes,
-                  stream);
+    return w4_run(choice, plan, M, N, K, s, A, words, scales, C, workspace, cus, stream);
 }
 
 extern "C" int gemm_f16_q8_quantize(int64_t R, int64_t N, const void *X, void *codes,
@@ -1881,7 +1986,7 @@ extern "C" int gemm_f16_q8_quantize(int64_t R, int64_t N, const void *X, void *c
         {X, R * N * 2, 2, false}, {codes, s.codes, 16, true}, {scales, s.scales, 2, true}};
     const int a = check_arrays(arrays, 3);
     if (a != GEMM_F16_OK || s.codes == 0) return a;
-    return q8_launch(reinterpret_cast<const void *>(&q8_encode_kernel), R, N, s, X, nullptr, codes,
+    return q8_launch(reinterpret_cast<const void *>(&q8_encode_kernel), R, N, s, X, nullptr, 0, codes,
                      scales, stream);
 }
 
@@ -1895,7 +2000,7 @@ extern "C" int gemm_f16_q8_dequantize(int64_t R, int64_t N, const void *codes, c
         {codes, s.codes, 16, false}, {scales, s.scales, 2, false}, {X, R * N * 2, 2, true}};
     const int a = check_arrays(arrays, 3);
     if (a != GEMM_F16_OK || s.codes == 0) return a;
-    return q8_launch(reinterpret_cast<const void *>(&q8_decode_kernel), R, N, s, nullptr, X, codes,
+    return q8_launch(reinterpret_cast<const void *>(&q8_decode_kernel), R, N, s, nullptr, X, N, codes,
                      scales, stream);
 }
 
@@ -1930,5 +2035,5 @@ extern "C" int gemm_f16_tn_q8(int64_t M, int64_t N, int64_t K, const void *A, co
     v = q8_plan_choice(choice, M, N, K, cus, &plan);
     if (v != GEMM_F16_OK) return v;
     if (plan.workspace_bytes > (workspace ? workspace_bytes : 0)) return GEMM_F16_INVALID_ARG;
-    return q8_run(choice, M, N, K, s, A, codes, scales, C, workspace, workspace_bytes, stream);
+    return q8_run(choice, M, N, K, s, A, codes, scales, C, workspace, cus, stream);
 }

@@ -292,7 +292,7 @@ W4_KERNELS = [((1, 4, 16, 8), 3, 500, 1000), ((1, 8, 16, 8), 5, 500, 3000),
               ((2, 96, 256, 8), 333, 12800, 32), ((2, 96, 256, 8), 80, 6500, 8000),
               ((2, 112, 256, 8), 512, 12800, 32), ((2, 112, 256, 8), 333, 2000, 8000),
               ((2, 128, 256, 8), 512, 16384, 32), ((2, 128, 256, 8), 120, 12800, 4096),
-              ((0,), 1500, 14336, 4096)]
+              ((0,), 1500, 14336, 4096), ((0,), 2200, 7001, 4001)]
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
@@ -312,17 +312,23 @@ def test_nt_w4_every_kernel(g, kernel, m, n, k, group):
     check_on_gpu(g.gemm_nt_w4(a, q), a, g.dequantize_w4(q).t(), k)
 
 
-Q8_KERNELS = [((1, 16, 128, 4), 7, 1000, 5), ((1, 16, 128, 4), 16, 300, 500),
-              ((1, 16, 256, 4), 10, 14336, 8192), ((1, 32, 128, 4), 17, 320, 30),
-              ((1, 32, 128, 4), 32, 1000, 1500), ((1, 64, 128, 4), 50, 320, 30),
-              ((1, 64, 128, 4), 130, 1000, 4000), ((0,), 600, 320, 1024)]
+# the same for the 8-bit product, and the ranges that its rows are split into
+Q8_KERNELS = [((1, 16, 128, 4), 1, 7, 1000, 5), ((1, 16, 128, 4), 1, 16, 300, 500),
+              ((1, 16, 128, 4), 28, 40, 300, 8000), ((1, 16, 256, 4), 4, 10, 14336, 8192),
+              ((1, 16, 256, 4), 1, 7, 60000, 33), ((1, 32, 128, 4), 16, 30, 2000, 8000),
+              ((1, 32, 128, 4), 1, 1500, 333, 40), ((1, 64, 128, 4), 2, 130, 4096, 4000),
+              ((1, 64, 128, 4), 3, 1069, 463, 2357), ((1, 64, 128, 4), 2, 1001, 999, 8001),
+              ((1, 64, 128, 4), 1, 100, 14337, 33), ((0,), 1, 1600, 1608, 3000),
+              ((0,), 1, 1601, 1608, 1500), ((0,), 1, 1600, 1603, 1500), ((0,), 1, 1601, 1601, 1500),
+              ((0,), 4, 3000, 64, 2048)]
 
 
-@pytest.mark.parametrize("kernel,m,n,k", Q8_KERNELS)
-def test_tn_q8_every_kernel(g, kernel, m, n, k):
+@pytest.mark.parametrize("kernel,splits,m,n,k", Q8_KERNELS)
+def test_tn_q8_every_kernel(g, kernel, splits, m, n, k):
     import torch
 
     plan = g.gemm_f16_tn_q8_plan(m, n, k, 256)
+    assert plan.splits == splits
     assert (plan.kernel, plan.block_m, plan.block_n, plan.waves)[:len(kernel)] == kernel
     gen = torch.Generator(device="cuda").manual_seed(m + n + k)
     x = g.quantize_q8(torch.randn(k, n, generator=gen, device="cuda").half())
