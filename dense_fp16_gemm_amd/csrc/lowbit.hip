@@ -1638,12 +1638,6 @@ static int64_t w4_partial_bytes(const W4Kernel &e, int64_t M, const W4Shape &s)
     return cdiv(M, e.rows) * cdiv(s.nb, e.blocks) * (e.rows / 16) * e.blocks * 1024;
 }
 
-// Whether the rows of A can be read by 16-byte direct-to-LDS loads as they are.
-static bool w4_rows_aligned(int64_t K, const void *A)
-{
-    return K % 8 == 0 && reinterpret_cast<uintptr_t>(A) % 16 == 0;
-}
-
 static int w4_plan_choice(const W4Choice &c, int64_t M, int64_t N, int64_t K, const W4Shape &s,
                           int32_t num_cus, gemm_f16_lowbit_plan_t *plan)
 {
@@ -1659,9 +1653,7 @@ static int w4_plan_choice(const W4Choice &c, int64_t M, int64_t N, int64_t K, co
         w4_ranges(s.kt, c.splits, &per_range, &plan->splits);
         grid *= cdiv(M, e.rows) * plan->splits;
         if (plan->splits > 1) plan->workspace_bytes = plan->splits * w4_partial_bytes(e, M, s);
-        // and the aligned copy of A, also where this call's A needs none: its
-        // address is not known here
-        plan->workspace_bytes += round_up(M * round_up(K, 8) * 2, 256);
+        if (K % 8 != 0) plan->workspace_bytes += round_up(M * round_up(K, 8) * 2, 256);   // A's copy
     }
     plan->grid = static_cast<int32_t>(grid);
     return GEMM_F16_OK;
@@ -1681,6 +1673,23 @@ static int w4_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t num_c
     return w4_plan_choice(w4_choose(M, K, s, num_cus), M, N, K, s, num_cus, plan);
 }
 
+static int w4_stream(int32_t id, int64_t M, int64_t N, int64_t K, const W4Shape &s, const void *A,
+                     const void *words, const void *scales, void *C, hipStream_t stream)
+{
+    const W4Kernel &e = kW4Kernels[id];
+    W4Params p;
+    p.A = static_cast<const uint16_t *>(A);
+    p.words = static_cast<const u32x4_t *>(words);
+    p.scales = static_cast<const uint16_t *>(scales);
+    p.C = static_cast<uint16_t *>(C);
+    p.M = static_cast<int32_t>(M);
+    p.N = static_cast<int32_t>(N);
+    p.K = static_cast<int32_t>(K);
+    p.kt = static_cast<int32_t>(s.kt);
+    p.nb = static_cast<int32_t>(s.nb);
+    return launch(e.fn[s.shift - 5], cdiv(s.nb, e.blocks), 64 * e.waves, &p, stream);
+}
+
 static int w4_run(const W4Choice &c, const gemm_f16_lowbit_plan_t &plan, int64_t M, int64_t N,
                   int64_t K, const W4Shape &s, const void *A, const void *words,
                   const void *scales, void *C, void *workspace, int32_t cus, hipStream_t stream)
@@ -1694,18 +1703,20 @@ static int w4_run(const W4Choice &c, const gemm_f16_lowbit_plan_t &plan, int64_t
         return v;
     }
     const W4Kernel &e = kW4Kernels[c.id];
-    if (e.kernel == GEMM_F16_LOWBIT_STREAM) {
-        W4Params p;
-        p.A = static_cast<const uint16_t *>(A);
-        p.words = static_cast<const u32x4_t *>(words);
-        p.scales = static_cast<const uint16_t *>(scales);
-        p.C = static_cast<uint16_t *>(C);
-        p.M = static_cast<int32_t>(M);
-        p.N = static_cast<int32_t>(N);
-        p.K = static_cast<int32_t>(K);
-        p.kt = static_cast<int32_t>(s.kt);
-        p.nb = static_cast<int32_t>(s.nb);
-        return launch(e.fn[s.shift - 5], plan.grid, 64 * e.waves, &p, stream);
+    if (e.kernel == GEMM_F16_LOWBIT_STREAM)
+        return w4_stream(c.id, M, N, K, s, A, words, scales, C, stream);
+    if (K % 8 == 0 && reinterpret_cast<uintptr_t>(A) % 16 != 0) {
+        // the tile kernels' loads need 16-byte aligned rows, and the workspace
+        // is planned by sizes alone: 16 rows at a time by the kernels that
+        // take any alignment
+        for (int64_t m = 0; m < M; m += 16) {
+            const int64_t rows = std::min<int64_t>(16, M - m);
+            const int v = w4_stream(w4_choose(rows, K, s, cus).id, rows, N, K, s,
+                                    static_cast<const uint16_t *>(A) + m * K, words, scales,
+                                    static_cast<uint16_t *>(C) + m * N, stream);
+            if (v != GEMM_F16_OK) return v;
+        }
+        return GEMM_F16_OK;
     }
     W4TileParams p;
     int64_t per_range;
@@ -1714,7 +1725,7 @@ static int w4_run(const W4Choice &c, const gemm_f16_lowbit_plan_t &plan, int64_t
     p.A = static_cast<const uint16_t *>(A);
     p.lda = static_cast<int32_t>(K);
     p.partial = static_cast<float *>(workspace);
-    if (!w4_rows_aligned(K, A)) {
+    if (K % 8 != 0) {
         uint16_t *to =
             reinterpret_cast<uint16_t *>(ws + (p.splits > 1 ? p.splits * partial : 0));
         p.lda = static_cast<int32_t>(round_up(K, 8));

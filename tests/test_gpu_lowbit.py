@@ -404,14 +404,15 @@ def test_empty(g):
     assert tuple(g.gemm_tn_q8(torch.zeros(32, 0, **f16), c).shape) == (0, 64)
 
 
+@pytest.mark.parametrize("k", [333, 336])
 @pytest.mark.parametrize("m", [1, 5, 17, 64, 100, 600])
-def test_nt_w4_unaligned_and_in_bounds(g, m):
+def test_nt_w4_unaligned_and_in_bounds(g, m, k):
     """Operands at 2-byte offsets; nothing around C is written, and what lies
     around A (NaN here) does not enter."""
     import torch
 
     rng = np.random.default_rng(m)
-    n, k = 71, 333
+    n = 71
     codes, scales, w = w4_case(rng, n, k, 64, False)
     a = rng.standard_normal((m, k)).astype(np.float16)
     q = g.pack_w4(dev(codes), dev(scales), 64)
@@ -579,11 +580,16 @@ def test_refusals(g):
             g.gemm_nt_w4(a, q, out=out)
     with pytest.raises(g.GemmError):            # C on top of A
         g.gemm_nt_w4(a, q, out=a.view(-1)[:128].view(4, 32))
-    big = torch.ones(2000, 64, **f16)
-    with pytest.raises(g.GemmError):            # too small a workspace
-        g.gemm_nt_w4(big, q, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
-    with pytest.raises(ValueError):
-        g.gemm_nt_w4(big, q, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    big, qb = torch.ones(64, 4096, **f16), g.quantize_w4(torch.ones(32, 4096, **f16), 32)
+    need = g.gemm_f16_nt_w4_plan(64, 32, 4096, 32, cus).workspace_bytes
+    assert need > 0
+    for ws in (torch.empty(need - 1, dtype=torch.uint8, device="cuda"),
+               torch.empty(need + 64, dtype=torch.uint8, device="cuda")[64:]):
+        with pytest.raises(g.GemmError):        # too small, and not 256-byte aligned
+            g.gemm_nt_w4(big, qb, workspace=ws)
+    with pytest.raises(ValueError):             # not on the GPU
+        g.gemm_nt_w4(big, qb, workspace=torch.empty(need, dtype=torch.uint8))
     with pytest.raises(ValueError):
         g.gemm_tn_q8(torch.ones(31, 4, **f16), c)
     with pytest.raises(ValueError):
