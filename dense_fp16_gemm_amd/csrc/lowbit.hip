@@ -34,6 +34,10 @@ __device__ __forceinline__ T bits_as(S s)
     return __builtin_bit_cast(T, s);
 }
 
+// The wave's index in its workgroup, in a scalar register: what is computed from
+// it alone (which tile, its addresses) then takes no vector operations.
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // Eight halves of a row at column c, as dwords; columns at or past `cols` are 0.
 __device__ __forceinline__ u32x4_t load8(const uint16_t *row, int32_t c, int32_t cols)
 {
@@ -143,7 +147,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_encode_kernel(W4EncodeParams p)
     const int r = lane & 15, kq = lane >> 4;
     const int per_tile = 128 >> p.shift;
     const int64_t step = static_cast<int64_t>(gridDim.x) * WAVES;
-    for (int64_t tile = static_cast<int64_t>(blockIdx.x) * WAVES + (threadIdx.x >> 6); tile < p.tiles;
+    for (int64_t tile = static_cast<int64_t>(blockIdx.x) * WAVES + wave_index(); tile < p.tiles;
          tile += step) {
         const int32_t b = static_cast<int32_t>(tile) / p.kt;
         const int32_t t = static_cast<int32_t>(tile) - b * p.kt;
@@ -262,23 +266,33 @@ __global__ __launch_bounds__(64 * WAVES) void w4_encode_kernel(W4EncodeParams p)
     }
 }
 
-// Elements 2 p and 2 p + 1 of a word, as the halves q: the four bits become
-// the low bits of 1024 + (q + 8), which is exact in fp16.
-__device__ __forceinline__ half2_t w4_pair(uint32_t word, int p)
+// A word's mask and exponent, held in registers: as literals they cannot share
+// the one instruction that does both (a third of the unpacking's operations).
+struct W4Bits {
+    uint32_t mask, exponent;
+};
+
+__device__ __forceinline__ W4Bits w4_bits(uint32_t mask, uint32_t exponent)
 {
-    const uint32_t u = ((word >> (4 * p)) & 0x000f000fu) | 0x64006400u;
-    const half2_t off = {_Float16(1032.0f), _Float16(1032.0f)};
-    return bits_as<half2_t>(u) - off;
+    asm("" : "+v"(mask));
+    asm("" : "+s"(exponent));
+    return W4Bits{mask, exponent};
 }
 
-// A word's eight weights times their scale.
-__device__ __forceinline__ half8_t w4_scaled(uint32_t word, _Float16 s)
+// For w4_scaled: the low four bits of each half, under fp16's 1024.
+__device__ __forceinline__ W4Bits w4_low_bits() { return w4_bits(0x000f000fu, 0x64006400u); }
+
+// A word's eight weights times their scale: four bits u become the low bits of
+// 1024 + u, less 1032 the code u - 8, times the scale, each exact in fp16.
+__device__ __forceinline__ half8_t w4_scaled(uint32_t word, _Float16 s, W4Bits bits)
 {
     const half2_t s2 = {s, s};
+    const half2_t off = {_Float16(1032.0f), _Float16(1032.0f)};
     half8_t h;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        const half2_t x = w4_pair(word, p) * s2;
+        const half2_t x =
+            (bits_as<half2_t>(((word >> (4 * p)) & bits.mask) | bits.exponent) - off) * s2;
         h[2 * p] = x[0];
         h[2 * p + 1] = x[1];
     }
@@ -298,9 +312,10 @@ __global__ __launch_bounds__(64 * WAVES) void w4_decode_kernel(W4DecodeParams p)
 {
     const int lane = threadIdx.x & 63;
     const int r = lane & 15, kq = lane >> 4;
+    const W4Bits bits = w4_low_bits();
     const int per_tile = 128 >> p.shift;
     const int64_t step = static_cast<int64_t>(gridDim.x) * WAVES;
-    for (int64_t tile = static_cast<int64_t>(blockIdx.x) * WAVES + (threadIdx.x >> 6); tile < p.tiles;
+    for (int64_t tile = static_cast<int64_t>(blockIdx.x) * WAVES + wave_index(); tile < p.tiles;
          tile += step) {
         const int32_t b = static_cast<int32_t>(tile) / p.kt;
         const int32_t t = static_cast<int32_t>(tile) - b * p.kt;
@@ -312,7 +327,8 @@ __global__ __launch_bounds__(64 * WAVES) void w4_decode_kernel(W4DecodeParams p)
         for (int j = 0; j < 4; ++j) {
             const int64_t c = static_cast<int64_t>(t) * 128 + 32 * j + kq * 8;
             const _Float16 sj = bits_as<_Float16>(s[((32 * j) >> p.shift) * 16]);
-            if (c < p.K) store8(p.W + n * p.ld, static_cast<int32_t>(c), p.ld, w4_scaled(w[j], sj));
+            if (c < p.K) store8(p.W + n * p.ld, static_cast<int32_t>(c), p.ld,
+                               w4_scaled(w[j], sj, bits));
         }
     }
 }
@@ -416,7 +432,7 @@ __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
     constexpr int NS = 128 >> SH;    // scales a tile and row
     __shared__ float red[W][NB][16][20];   // 20: rows of 16 sums apart in the banks
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    const int wave = wave_index();
     const int r = lane & 15, kq = lane >> 4;
     const int m = r & (MC - 1), jj = r / MC;
     const int32_t b0 = blockIdx.x * NB;
@@ -430,6 +446,7 @@ __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
         words[nb] = p.words + b * p.kt * 64 + lane;
         scales[nb] = p.scales + b * p.kt * NS * 16 + r;
     }
+    const W4Bits bits = w4_low_bits();
     f32x4_t acc[NB][JC] = {};
     u32x4_t wv[2][D][NB];
     half8_t af[2][D][AL];
@@ -455,7 +472,7 @@ __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc[nb][j % JC] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    w4_scaled(wv[buf][d][nb][j], sc[buf][d][nb][(32 * j) >> SH]),
+                    w4_scaled(wv[buf][d][nb][j], sc[buf][d][nb][(32 * j) >> SH], bits),
                     af[buf][d][j / JC], acc[nb][j % JC], 0, 0, 0);
     };
     const int32_t full = p.K / 128;
@@ -499,7 +516,7 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
     __shared__ float red[W][NB][16][20];
     __shared__ half8_t abuf[W][RL * 4][16];
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    const int wave = wave_index();
     const int r = lane & 15, kq = lane >> 4;
     const int32_t b0 = blockIdx.x * NB;
     const uint16_t *arow[RL];
@@ -515,6 +532,7 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
         words[nb] = p.words + b * p.kt * 64 + lane;
         scales[nb] = p.scales + b * p.kt * NS * 16 + r;
     }
+    const W4Bits bits = w4_low_bits();
     f32x4_t acc[NB] = {};
     u32x4_t wv[2][NB];
     half8_t af[2][RL];
@@ -549,7 +567,8 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc[nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    w4_scaled(wv[buf][nb][j], sc[buf][nb][(32 * j) >> SH]), a[j], acc[nb], 0, 0, 0);
+                    w4_scaled(wv[buf][nb][j], sc[buf][nb][(32 * j) >> SH], bits), a[j], acc[nb], 0, 0,
+                    0);
     };
     const int32_t full = p.K / 128;
     w4_run_tiles<W, 1>(full, wave, load, mma);
@@ -634,7 +653,7 @@ __device__ __forceinline__ void dma4(i32x4_t rsrc, uint32_t voff, uint32_t lds)
 // the four bits u at the top of the significand of 16 + u, which times s less
 // 24 s is s (u - 8).  24 s is exact (3 times a number of 8 significant bits)
 // and the fused operation rounds once, a number that fp16 holds: no rounding.
-__device__ __forceinline__ half8_t w4_tile_word(uint32_t w, _Float16 s)
+__device__ __forceinline__ half8_t w4_tile_word(uint32_t w, _Float16 s, W4Bits bits)
 {
     const half2_t s2 = {s, s};
     const half2_t c2 = s2 * _Float16(-24.0f);
@@ -643,12 +662,13 @@ __device__ __forceinline__ half8_t w4_tile_word(uint32_t w, _Float16 s)
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const half2_t x = __builtin_elementwise_fma(
-            bits_as<half2_t>((t[p] & 0x03c003c0u) | 0x4c004c00u), s2, c2);
+            bits_as<half2_t>((t[p] & bits.mask) | bits.exponent), s2, c2);
         h[2 * p] = x[0];
         h[2 * p + 1] = x[1];
     }
     return h;
 }
+__device__ __forceinline__ W4Bits w4_high_bits() { return w4_bits(0x03c003c0u, 0x4c004c00u); }
 constexpr float W4_TILE_WORD_MOST = 2720.0f;   // 24 * 2720 < 65504
 
 // Four neighbouring columns of a row of C.
@@ -680,7 +700,7 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
     static_assert(S * STAGE <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = wave_index();
     const int r = lane & 15, kq = lane >> 4;
     // Units run over the rows of A first, so that a word's users are
     // neighbours, and each XCD (workgroups u mod 8) takes a contiguous range.
@@ -802,6 +822,7 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
     // second one then goes on from there.  (Both in one loop cost registers:
     // 48 x 16384 x 16384 took 45.3 us.)  The waves of a workgroup may be in
     // different loops, with the same barriers.
+    const W4Bits bits = w4_high_bits();
     int32_t i = 0;
     bool large = false;
     for (; i < T; ++i) {
@@ -814,11 +835,12 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
                 most = fmaxf(most, __builtin_fabsf(static_cast<float>(sc[nb][s])));
         large = __any(most > W4_TILE_WORD_MOST);
         if (large) break;
-        compute([](uint32_t w, _Float16 s) { return w4_tile_word(w, s); });
+        compute([&](uint32_t w, _Float16 s) { return w4_tile_word(w, s, bits); });
     }
     if (large) {
+        const W4Bits low = w4_low_bits();
         for (;;) {
-            compute([](uint32_t w, _Float16 s) { return w4_scaled(w, s); });
+            compute([&](uint32_t w, _Float16 s) { return w4_scaled(w, s, low); });
             if (++i == T) break;
             begin(i);
         }
@@ -1083,7 +1105,7 @@ __global__ __launch_bounds__(64 * W, 2) void q8_tn_kernel(Q8TnParams p)
     };
     __shared__ __attribute__((aligned(16))) Lds lds;
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    const int wave = wave_index();
     const int r = lane & 15, kq = lane >> 4;
     int32_t u = blockIdx.x;
     {
