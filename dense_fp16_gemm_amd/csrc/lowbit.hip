@@ -1436,6 +1436,9 @@ static int q8_shape(int64_t R, int64_t N, Q8Shape *s)
     s->groups = cdiv(N, GEMM_F16_Q8_GROUP);
     s->codes = R * s->groups * GEMM_F16_Q8_GROUP;
     s->scales = R * s->groups * 2;
+    // A workgroup of 256 takes 8192 values, in matrices a little wider than its
+    // 512 columns 4352: 2^36 keep a launch's threads within 32 bits.
+    if (s->codes > (int64_t(1) << 36)) return GEMM_F16_UNSUPPORTED;
     return GEMM_F16_OK;
 }
 
@@ -1457,7 +1460,6 @@ static int q8_launch(const void *fn, int64_t R, int64_t N, const Q8Shape &s, con
     const int64_t col_blocks = cdiv(p.chunks, int64_t(1) << p.tx_shift);
     p.col_blocks = static_cast<int32_t>(col_blocks);
     const int64_t grid = col_blocks * cdiv(R, int64_t((64 * WAVES) >> p.tx_shift) * Q8_ROWS);
-    if (grid > INT32_MAX) return GEMM_F16_UNSUPPORTED;
     return launch(fn, grid, 64 * WAVES, &p, stream);
 }
 
@@ -1583,6 +1585,11 @@ struct W4Choice {
     int32_t id, splits;
 };
 
+// A launch counts its threads in 32 bits: of workgroups of 512, fewer than 2^23.
+// Matrices of more blocks (67 million rows of W) are decoded for the GEMM, whose
+// grid does not grow with them.
+constexpr int64_t W4_MOST_WORKGROUPS = 1 << 22;
+
 // The tile kernels and splits, and the decoding path, by a model of their
 // times in us, fitted to 1,900 timings of 110 shapes (17 to 2048 rows, N and K
 // of 1024 to 16384, words from HBM): rounds of workgroups over the CUs times
@@ -1595,12 +1602,13 @@ static W4Choice w4_choose_tile(int64_t M, int64_t K, const W4Shape &s, int32_t c
     // words to fp16 and back from memory, and the GEMM at its rate for large M
     W4Choice best = {-1, 1};
     double best_us = 12.2 + (7.1e-7 + 1.18e-9 * std::max<double>(M, 423)) * std::max(nk, 8.4e6);
-    // 32-bit offsets of the tile kernel's resources and columns
-    if (M > 8192 || K > (1 << 21) || s.nb > (1 << 24)) return best;
+    // 32-bit offsets of the tile kernel's resources
+    if (M > 8192 || K > (1 << 21)) return best;
     for (int32_t id = 0; id < kNumW4Kernels; ++id) {
         const W4Kernel &e = kW4Kernels[id];
         if (e.kernel != GEMM_F16_LOWBIT_TILE) continue;
         const int64_t tiles = cdiv(M, e.rows) * cdiv(s.nb, e.blocks);
+        if (tiles > W4_MOST_WORKGROUPS) continue;
         const bool two = e.step2 > 0;
         const int64_t slots = static_cast<int64_t>(cus) * (two ? 2 : 1);
         int64_t last = 0;
@@ -1626,6 +1634,7 @@ static W4Choice w4_choose_tile(int64_t M, int64_t K, const W4Shape &s, int32_t c
 
 static W4Choice w4_choose(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
 {
+    if (s.nb > W4_MOST_WORKGROUPS) return {-1, 1};
     if (M <= 4) return {0, 1};
     // the most blocks a workgroup that still give three CUs in four one
     const int64_t most = s.nb / std::max<int64_t>(1, 3 * static_cast<int64_t>(cus) / 4);

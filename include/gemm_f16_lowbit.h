@@ -127,6 +127,8 @@ typedef struct {
  * device with num_cus compute units.
  *
  * M = 0 or N = 0: nothing to compute.  K = 0: C is filled with +0.
+ * GEMM_F16_UNSUPPORTED for M above 2^31 - 1, for N and K as above, and for
+ * sizes that decoding and the fp16 GEMM would run, where that refuses them.
  */
 int gemm_f16_nt_w4_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t num_cus,
                         gemm_f16_lowbit_plan_t *plan);
@@ -146,7 +148,7 @@ int gemm_f16_nt_w4(int64_t M, int64_t N, int64_t K, int32_t group, const void *A
  * gemm_f16_q8_quantize: X fp16 [R, N] row-major (any 2-byte alignment) to
  * codes and scales.  gemm_f16_q8_dequantize: the other way.  Overlap,
  * alignment and empty sizes as for W4; GEMM_F16_UNSUPPORTED for R or N above
- * 2^31 - 32.
+ * 2^31 - 32 or more than 2^36 codes.
  */
 int gemm_f16_q8_quantize(int64_t R, int64_t N, const void *X, void *codes, void *scales,
                          hipStream_t stream);

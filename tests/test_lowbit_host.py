@@ -137,6 +137,37 @@ def test_q8_plans(g, m, n, k):
             g.gemm_f16_tn_q8_plan(*bad)
 
 
+@pytest.mark.parametrize("m", [1, 4, 5, 16, 17, 333, 8192])
+@pytest.mark.parametrize("n", [2 ** 26, 2 ** 27 - 16, 2 ** 27, 2 ** 31 - 128])
+def test_w4_launches_count_threads_in_32_bits(g, m, n):
+    for k in (1, 128):
+        try:
+            p = g.gemm_f16_nt_w4_plan(m, n, k, 32, 256)
+        except g.GemmError as e:   # as the fp16 product of such sizes is
+            assert e.status == 2 and 2 * m * n >= 2 ** 40
+            continue
+        if p.kernel != g.LOWBIT_DECODE:
+            assert p.grid * p.waves * 64 < 2 ** 32
+        if n > 2 ** 26:
+            assert p.kernel == g.LOWBIT_DECODE and p.workspace_bytes >= 2 * n * k
+
+
+@pytest.mark.parametrize("r,n,status", [
+    (2 ** 27, 544, 2), (2 ** 31 - 32, 33, 2), (2 ** 31 - 32, 32, 1), (2 ** 26, 1024, 1),
+    (2 ** 26 + 1, 1024, 2), (33, 2 ** 31 - 32, 2), (32, 2 ** 31 - 32, 1),
+])
+def test_q8_launches_count_threads_in_32_bits(g, r, n, status):
+    # what is not refused for its size is refused for its NULL arrays
+    lib = g.load()
+    assert lib.gemm_f16_q8_quantize(r, n, 0, 0, 0, 0) == status
+    assert lib.gemm_f16_q8_dequantize(r, n, 0, 0, 0, 0) == status
+    assert lib.gemm_f16_tn_q8(16, n, r, 0, 0, 0, 0, 0, 0, 0) == status
+    if status == 1:   # the kernels' rows and columns a workgroup
+        chunks = -(-n // 32) * 4
+        wide = min(64, 1 << (chunks - 1).bit_length())
+        assert -(-chunks // wide) * -(-r // (1024 // wide)) * 256 < 2 ** 32
+
+
 def test_empty_products_plan_nothing(g):
     for p in (g.gemm_f16_nt_w4_plan(0, 5, 5, 32, 256), g.gemm_f16_nt_w4_plan(5, 5, 0, 32, 256),
               g.gemm_f16_tn_q8_plan(5, 0, 5, 256), g.gemm_f16_tn_q8_plan(5, 5, 0, 256)):
