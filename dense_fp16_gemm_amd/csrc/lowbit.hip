@@ -1499,6 +1499,9 @@ static int decode_layout(int64_t M, int64_t N, int64_t K, int32_t num_cus, bool 
     d->M = tn ? round_up(M, 8) : M;
     d->N = tn ? round_up(N, 8) : N;
     d->K = tn ? K : round_up(K, 8);
+    // the workspace's offsets in 64 bits
+    const int64_t most = int64_t(1) << 60;
+    if (d->M * d->K > most || d->N * d->K > most || d->M * d->N > most) return GEMM_F16_UNSUPPORTED;
     int64_t ws = 0;
     const int v = tn ? gemm_f16_tn_splitk_plan(d->M, d->N, d->K, num_cus, 0, &d->plan, &d->splits, &ws)
                      : gemm_f16_nt_splitk_plan(d->M, d->N, d->K, num_cus, 0, &d->plan, &d->splits, &ws);

@@ -128,7 +128,8 @@ typedef struct {
  *
  * M = 0 or N = 0: nothing to compute.  K = 0: C is filled with +0.
  * GEMM_F16_UNSUPPORTED for M above 2^31 - 1, for N and K as above, and for
- * sizes that decoding and the fp16 GEMM would run, where that refuses them.
+ * sizes that decoding and the fp16 GEMM would run, where that refuses them or
+ * a matrix has more than 2^60 values.
  */
 int gemm_f16_nt_w4_plan(int64_t M, int64_t N, int64_t K, int32_t group, int32_t num_cus,
                         gemm_f16_lowbit_plan_t *plan);

@@ -168,6 +168,23 @@ def test_q8_launches_count_threads_in_32_bits(g, r, n, status):
         assert -(-chunks // wide) * -(-r // (1024 // wide)) * 256 < 2 ** 32
 
 
+@pytest.mark.parametrize("m,n,k", [(2 ** 31 - 9, 31, 2 ** 31 - 32), (2 ** 31 - 9, 2 ** 20, 2 ** 16),
+                                   (2 ** 31 - 9, 2 ** 31 - 33, 31), (2 ** 30, 2 ** 10, 2 ** 26)])
+def test_no_workspace_past_64_bits(g, m, n, k):
+    """Refused, or the workspace holds the operand that is decoded."""
+    for call in (lambda: g.gemm_f16_tn_q8_plan(m, n, k, 256),
+                 lambda: g.gemm_f16_nt_w4_plan(m, n, k, 128, 256)):
+        try:
+            p = call()
+        except g.GemmError as e:
+            assert e.status == 2
+            continue
+        assert p.kernel == g.LOWBIT_DECODE and p.workspace_bytes >= 2 * n * k
+    if m * k > 2 ** 60 or m * n > 2 ** 60:
+        with pytest.raises(g.GemmError):
+            g.gemm_f16_tn_q8_plan(m, n, k, 256)
+
+
 def test_empty_products_plan_nothing(g):
     for p in (g.gemm_f16_nt_w4_plan(0, 5, 5, 32, 256), g.gemm_f16_nt_w4_plan(5, 5, 0, 32, 256),
               g.gemm_f16_tn_q8_plan(5, 0, 5, 256), g.gemm_f16_tn_q8_plan(5, 5, 0, 256)):
