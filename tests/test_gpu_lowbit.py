@@ -690,3 +690,101 @@ def test_gradient_against_differences(g):
         # the loss is linear in w: differences are exact but for float64's rounding
         diff = (loss(w + d) - loss(w - d)) / 2
         assert abs(diff - (grad * d).sum()) <= (bound * np.abs(d)).sum() + 1e-9 * abs(loss(w))
+
+
+# ---- beyond 32 bits -------------------------------------------------------------
+def test_w4_beyond_32_bits(g):
+    """Words past 2^32 bytes, the fp16 matrix past 2^34: the last rows of every
+    kernel's result, which are those of the last rows alone, and the first."""
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    n, k, group = 2 ** 20 + 37, 8320, 128
+    nb, kt = -(-n // 16), -(-k // 128)
+    words = torch.randint(-2 ** 31, 2 ** 31, (nb, kt, 64, 4), dtype=torch.int32, device="cuda",
+                          generator=gen)
+    assert words.numel() * 4 > 2 ** 32
+    scales = torch.randint(1, 256, (nb, kt, 16), device="cuda", generator=gen).half() / 2 ** 14
+    w = g.W4Matrix(words, scales, n, k, group)
+    # the first and the last rows, as matrices of their own
+    head, rest = 32, n - 16 * (nb - 2)
+    lo = g.W4Matrix(words[:2], scales[:2], head, k, group)
+    hi = g.W4Matrix(words[-2:], scales[-2:], rest, k, group)
+    lo64, hi64 = (host(g.dequantize_w4(x)).astype(np.float64) for x in (lo, hi))
+    for m in (1, 3, 16, 48, 1500):
+        a = torch.randn((m, k), device="cuda", generator=gen).half()
+        c = g.gemm_nt_w4(a, w)
+        a64 = host(a).astype(np.float64)
+        check_product(host(c[:, :head]), a64, lo64.T, k, False)
+        check_product(host(c[:, -rest:]), a64, hi64.T, k, False)
+        del c
+    full = g.dequantize_w4(w)
+    assert (host(full[:head]).astype(np.float64) == lo64).all()
+    assert (host(full[-rest:]).astype(np.float64) == hi64).all()
+    again = g.quantize_w4(full, group)
+    tail = g.quantize_w4(full[-rest:].contiguous(), group)
+    assert torch.equal(again.words[-2:], tail.words)
+    assert torch.equal(again.scales[-2:], tail.scales)
+
+
+def test_q8_beyond_32_bits(g):
+    """Codes past 2^32 bytes.  Rows of A are zeros but for the first and the last
+    1000, so the product is that of those rows of X."""
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(32)
+    r, n, rows = 2 ** 20 + 40037, 4160, 1000
+    x = torch.empty((r, n), dtype=torch.float16, device="cuda")
+    for i in range(0, r, 2 ** 17):
+        x[i:i + 2 ** 17] = torch.randn(x[i:i + 2 ** 17].shape, device="cuda", generator=gen)
+    q = g.quantize_q8(x)
+    assert q.codes.numel() > 2 ** 32
+    ends = []
+    for part in (slice(0, rows), slice(r - rows, r)):
+        alone = g.quantize_q8(x[part])
+        assert torch.equal(q.codes[part], alone.codes) and torch.equal(q.scales[part], alone.scales)
+        ends.append(host(g.dequantize_q8(alone)))
+    back = g.dequantize_q8(q, out=x)
+    assert (host(back[:rows]) == ends[0]).all() and (host(back[-rows:]) == ends[1]).all()
+    del back, x
+    x64 = np.concatenate(ends).astype(np.float64)
+    for m in (16, 40, 512):
+        a = torch.zeros((r, m), dtype=torch.float16, device="cuda")
+        a[:rows] = torch.randn((rows, m), device="cuda", generator=gen)
+        a[-rows:] = torch.randn((rows, m), device="cuda", generator=gen)
+        a64 = np.concatenate([host(a[:rows]), host(a[-rows:])]).astype(np.float64)
+        # zeros add nothing and round nothing, so the bound is that of 2000 rows
+        # with a step more for each range that K may be split into, 256 at most
+        c = host(g.gemm_tn_q8(a, q))
+        check_product(c, a64.T, x64, 2 * rows, False)
+
+
+def test_threads_on_their_own_streams(g):
+    """Calls of several host threads at once, each with sizes of its own that
+    change from call to call: the same bits as alone."""
+    import threading
+
+    import torch
+
+    calls = [(call, host(call())) for call, _, _ in products(g, np.random.default_rng(41))]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(first):
+        try:
+            s = torch.cuda.Stream()
+            for i in range(20):
+                call, want = calls[(first + i) % len(calls)]
+                out = call(stream=s)
+                s.synchronize()
+                if not (host(out) == want).all():
+                    wrong.append((first, i))
+        except BaseException as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=run, args=(t,)) for t in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
