@@ -282,19 +282,23 @@ __device__ __forceinline__ W4Bits w4_bits(uint32_t mask, uint32_t exponent)
 // For w4_scaled: the low four bits of each half, under fp16's 1024.
 __device__ __forceinline__ W4Bits w4_low_bits() { return w4_bits(0x000f000fu, 0x64006400u); }
 
-// A word's eight weights times their scale: four bits u become the low bits of
-// 1024 + u, less 1032 the code u - 8, times the scale, each exact in fp16.
-__device__ __forceinline__ half8_t w4_scaled(uint32_t word, _Float16 s, W4Bits bits)
+// Weights 2 i and 2 i + 1 of a word times their scale: four bits u become the low
+// bits of 1024 + u, less 1032 the code u - 8, times the scale, each exact in fp16.
+__device__ __forceinline__ half2_t w4_pair(uint32_t word, int i, _Float16 s, W4Bits bits)
 {
     const half2_t s2 = {s, s};
     const half2_t off = {_Float16(1032.0f), _Float16(1032.0f)};
+    return (bits_as<half2_t>(((word >> (4 * i)) & bits.mask) | bits.exponent) - off) * s2;
+}
+
+__device__ __forceinline__ half8_t w4_scaled(uint32_t word, _Float16 s, W4Bits bits)
+{
     half8_t h;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const half2_t x =
-            (bits_as<half2_t>(((word >> (4 * p)) & bits.mask) | bits.exponent) - off) * s2;
-        h[2 * p] = x[0];
-        h[2 * p + 1] = x[1];
+    for (int i = 0; i < 4; ++i) {
+        const half2_t x = w4_pair(word, i, s, bits);
+        h[2 * i] = x[0];
+        h[2 * i + 1] = x[1];
     }
     return h;
 }
@@ -599,9 +603,10 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
 // weight is unpacked twice in a workgroup.
 //
 // What bounds it is the vector ALU beside the matrix units: unpacking a word
-// of eight weights takes 12 operations, while its MFMAs take 16 MT cycles.
-// w4_tile_word scales and centres in one fused operation to save three of 15
-// (333 x 4096 x 14336: 51.7 to 48.1 us, 48 x 16384 x 16384: 47.1 to 43.0).
+// of eight weights takes 12 operations of 4 cycles, while its MFMAs take 16 MT
+// cycles.  w4_tile_pair scales and centres in one fused operation to save three
+// of 15 (333 x 4096 x 14336: 51.7 to 48.1 us, 48 x 16384 x 16384: 47.1 to 43.0),
+// and a word is unpacked between the MFMAs of the word before it.
 //
 // Few tiles leave CUs idle: K is then split, each range's fp32 sums go to the
 // workspace in the order in which lanes hold them (every store and load a
@@ -649,24 +654,16 @@ __device__ __forceinline__ void dma4(i32x4_t rsrc, uint32_t voff, uint32_t lds)
                  : "v"(voff), "s"(rsrc), "{m0}"(lds));
 }
 
-// A word's eight weights times their scale, as w4_scaled, for s up to 2720:
+// Weights 2 i and 2 i + 1 of a word times their scale, as w4_pair, for s up to 2720:
 // the four bits u at the top of the significand of 16 + u, which times s less
 // 24 s is s (u - 8).  24 s is exact (3 times a number of 8 significant bits)
 // and the fused operation rounds once, a number that fp16 holds: no rounding.
-__device__ __forceinline__ half8_t w4_tile_word(uint32_t w, _Float16 s, W4Bits bits)
+__device__ __forceinline__ half2_t w4_tile_pair(uint32_t w, int i, _Float16 s, W4Bits bits)
 {
     const half2_t s2 = {s, s};
     const half2_t c2 = s2 * _Float16(-24.0f);
-    const uint32_t t[4] = {w << 6, w << 2, w >> 2, w >> 6};
-    half8_t h;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const half2_t x = __builtin_elementwise_fma(
-            bits_as<half2_t>((t[p] & bits.mask) | bits.exponent), s2, c2);
-        h[2 * p] = x[0];
-        h[2 * p + 1] = x[1];
-    }
-    return h;
+    const uint32_t t = i < 2 ? w << (6 - 4 * i) : w >> (4 * i - 6);
+    return __builtin_elementwise_fma(bits_as<half2_t>((t & bits.mask) | bits.exponent), s2, c2);
 }
 __device__ __forceinline__ W4Bits w4_high_bits() { return w4_bits(0x03c003c0u, 0x4c004c00u); }
 constexpr float W4_TILE_WORD_MOST = 2720.0f;   // 24 * 2720 < 65504
@@ -795,7 +792,7 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
                 sc[nb][s] = *reinterpret_cast<const _Float16 *>(ss + (nb * NS + s) * 32);
         }
     };
-    auto compute = [&](auto word) {
+    auto compute = [&](auto pair) {
         const uint8_t *st = smem + stage * STAGE;
         half8_t a[2][MT];
         auto read_a = [&](int j) {
@@ -803,22 +800,39 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
             for (int mt = 0; mt < MT; ++mt)
                 a[j & 1][mt] = *reinterpret_cast<const half8_t *>(st + mt * 4096 + aoff[j]);
         };
+        // The order is fixed by hand: after each MFMA a share of the next
+        // word's unpacking and of the next fragments' reads.  The compiler puts
+        // the two kinds of work one after the other (333 x 4096 x 14336: 50.3
+        // us, so 48.1, and 46.2 with a third buffer, S = 3).
         read_a(0);
+        half8_t w[2];
+        auto unpack = [&](int v, int i) {
+            const half2_t x = pair(wv[v % NB][v / NB], i, sc[v % NB][(32 * (v / NB)) >> SH]);
+            w[v & 1][2 * i] = x[0];
+            w[v & 1][2 * i + 1] = x[1];
+        };
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j < 3) read_a(j + 1);
+        for (int i = 0; i < 4; ++i) unpack(0, i);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const half8_t w = word(wv[nb][j], sc[nb][(32 * j) >> SH]);
+        for (int u = 0; u < 4 * NB; ++u) {
+            const int j = u / NB, nb = u % NB;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    acc[mt][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, a[j & 1][mt],
-                                                                         acc[mt][nb], 0, 0, 0);
+            for (int mt = 0; mt < MT; ++mt) {
+                acc[mt][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[u & 1], a[j & 1][mt],
+                                                                     acc[mt][nb], 0, 0, 0);
+                if (nb == 0 && j < 3)
+                    a[(j + 1) & 1][mt] =
+                        *reinterpret_cast<const half8_t *>(st + mt * 4096 + aoff[j + 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i * MT / 4 == mt && u + 1 < 4 * NB) unpack(u + 1, i);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         stage = stage == S - 1 ? 0 : stage + 1;
     };
-    // The loop stops at a step with a scale too large for w4_tile_word; a
+    // The loop stops at a step with a scale too large for w4_tile_pair; a
     // second one then goes on from there.  (Both in one loop cost registers:
     // 48 x 16384 x 16384 took 45.3 us.)  The waves of a workgroup may be in
     // different loops, with the same barriers.
@@ -835,12 +849,12 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
                 most = fmaxf(most, __builtin_fabsf(static_cast<float>(sc[nb][s])));
         large = __any(most > W4_TILE_WORD_MOST);
         if (large) break;
-        compute([&](uint32_t w, _Float16 s) { return w4_tile_word(w, s, bits); });
+        compute([&](uint32_t w, int i, _Float16 s) { return w4_tile_pair(w, i, s, bits); });
     }
     if (large) {
         const W4Bits low = w4_low_bits();
         for (;;) {
-            compute([&](uint32_t w, _Float16 s) { return w4_scaled(w, s, low); });
+            compute([&](uint32_t w, int i, _Float16 s) { return w4_pair(w, i, s, low); });
             if (++i == T) break;
             begin(i);
         }
@@ -887,6 +901,7 @@ __global__ __launch_bounds__(256) void w4_join_kernel(W4JoinParams p)
     if (m >= p.M || n >= p.N) return;
     const float *from = p.partial + idx * 4;
     f32x4_t sum = *reinterpret_cast<const f32x4_t *>(from);
+#pragma unroll 4
     for (int32_t s = 1; s < p.splits; ++s)
         sum += *reinterpret_cast<const f32x4_t *>(from + s * p.stride);
     store4(p.C, p.M, p.N, m, n, sum);
@@ -1575,10 +1590,10 @@ static const W4Kernel kW4Kernels[] = {
     W4_STREAM(4, 1, 8, 2),
     W4_ROWS(2, 1, 8), W4_ROWS(2, 2, 8),
     W4_ROWS(4, 1, 8), W4_ROWS(4, 2, 8), W4_ROWS(4, 4, 8),
-    W4_TILE(2, 2, 4, 4, 0.719, 0.957), W4_TILE(2, 4, 4, 2, 1.011, 1.461),
-    W4_TILE(3, 4, 4, 2, 1.164, 1.712), W4_TILE(4, 2, 4, 3, 0.783, 1.210),
-    W4_TILE(4, 4, 4, 2, 1.330, 2.033), W4_TILE(6, 2, 8, 2, 1.449, 0),
-    W4_TILE(7, 2, 8, 2, 1.610, 0),     W4_TILE(8, 2, 8, 2, 1.753, 0),
+    W4_TILE(2, 2, 4, 4, 0.518, 0.813), W4_TILE(3, 2, 8, 2, 0.911, 1.474),
+    W4_TILE(4, 2, 4, 3, 0.689, 1.061), W4_TILE(4, 2, 8, 3, 0.989, 0),
+    W4_TILE(6, 2, 8, 3, 1.209, 0),     W4_TILE(7, 2, 8, 3, 1.366, 0),
+    W4_TILE(8, 2, 8, 3, 1.505, 0),
 };
 constexpr int kNumW4Kernels = sizeof(kW4Kernels) / sizeof(kW4Kernels[0]);
 
@@ -1594,17 +1609,18 @@ struct W4Choice {
 constexpr int64_t W4_MOST_WORKGROUPS = 1 << 22;
 
 // The tile kernels and splits, and the decoding path, by a model of their
-// times in us, fitted to 1,900 timings of 110 shapes (17 to 2048 rows, N and K
+// times in us, fitted to 4,000 timings of 117 shapes (24 to 2048 rows, N and K
 // of 1024 to 16384, words from HBM): rounds of workgroups over the CUs times
-// the steps of a range, and for a split the partial sums' way through memory
-// and the join.  Its error is 6%; what it chose took 0.7% longer than the best
-// tile kernel and split of each shape in the mean, 13% in the worst.
+// the steps of a range, the clock that long products lose to the power limit,
+// and for a split the partial sums' way through memory and the join.  Its error
+// is 6%; what it chose took 1.1% longer than the best of each shape in the mean,
+// 16% in the worst.
 static W4Choice w4_choose_tile(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
 {
     const double nk = static_cast<double>(s.nb) * 16 * K;
     // words to fp16 and back from memory, and the GEMM at its rate for large M
     W4Choice best = {-1, 1};
-    double best_us = 12.2 + (7.1e-7 + 1.18e-9 * std::max<double>(M, 423)) * std::max(nk, 8.4e6);
+    double best_us = 12.2 + (7.0e-7 + 1.13e-9 * std::max<double>(M, 423)) * std::max(nk, 8.4e6);
     // 32-bit offsets of the tile kernel's resources
     if (M > 8192 || K > (1 << 21)) return best;
     for (int32_t id = 0; id < kNumW4Kernels; ++id) {
@@ -1621,11 +1637,12 @@ static W4Choice w4_choose_tile(int64_t M, int64_t K, const W4Shape &s, int32_t c
             last = per;
             const int64_t ranges = cdiv(s.kt, per), wgs = tiles * ranges;
             const int64_t full = wgs / slots, rest = wgs % slots;
-            double us = 3.9 + full * (two ? e.step2 : e.step1) * per;
+            double us = 3.7 + full * (two ? e.step2 : e.step1) * per;
             if (rest > 0) us += (rest <= cus || !two ? e.step1 : e.step2) * per;
             if (ranges > 1)
-                us += 1.5 + 0.23 * ranges +
-                      2.75e-7 * static_cast<double>(wgs) * (e.rows / 16) * e.blocks * 1024;
+                us += 1.5 + 0.114 * ranges +
+                      3.41e-7 * static_cast<double>(wgs) * (e.rows / 16) * e.blocks * 1024;
+            us += 2.26e-10 * std::max(0.0, nk * static_cast<double>(M) - 1.22e10);
             if (us < best_us) {
                 best_us = us;
                 best = {id, static_cast<int32_t>(ranges)};

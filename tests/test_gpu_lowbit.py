@@ -286,12 +286,12 @@ W4_KERNELS = [((1, 4, 16, 8), 3, 500, 1000), ((1, 8, 16, 8), 5, 500, 3000),
               ((1, 8, 32, 8), 7, 6500, 700), ((1, 16, 16, 8), 12, 500, 3000),
               ((1, 16, 32, 8), 16, 6500, 700), ((1, 16, 64, 8), 9, 12800, 520),
               ((2, 32, 128, 4), 17, 16, 32), ((2, 32, 128, 4), 30, 1000, 1024),
-              ((2, 32, 256, 4), 17, 16384, 8000), ((2, 48, 256, 4), 333, 6500, 32),
-              ((2, 48, 256, 4), 80, 6500, 2048), ((2, 64, 128, 4), 80, 12800, 32),
-              ((2, 64, 128, 4), 384, 300, 4096), ((2, 64, 256, 4), 160, 12800, 8000),
+              ((2, 48, 256, 8), 333, 6500, 32), ((2, 48, 256, 8), 40, 6500, 8000),
+              ((2, 64, 128, 4), 80, 12800, 32), ((2, 64, 128, 4), 60, 6500, 2048),
+              ((2, 64, 256, 8), 200, 16384, 32), ((2, 64, 256, 8), 112, 6500, 4096),
               ((2, 96, 256, 8), 333, 12800, 32), ((2, 96, 256, 8), 80, 6500, 8000),
-              ((2, 112, 256, 8), 512, 12800, 32), ((2, 112, 256, 8), 333, 2000, 8000),
-              ((2, 128, 256, 8), 512, 16384, 32), ((2, 128, 256, 8), 120, 12800, 4096),
+              ((2, 112, 256, 8), 512, 12800, 32), ((2, 112, 256, 8), 200, 6500, 4096),
+              ((2, 128, 256, 8), 512, 16384, 32), ((2, 128, 256, 8), 120, 12800, 8000),
               ((0,), 1500, 14336, 4096), ((0,), 2200, 7001, 4001)]
 
 
