@@ -338,7 +338,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_decode_kernel(W4DecodeParams p)
 }
 
 // ---------------------------------------------------------------------------
-// C = A W^T for at most 16 rows of A: the words streamed through registers
+// C = A W^T for at most 48 rows of A: the words streamed through registers
 // ---------------------------------------------------------------------------
 // One workgroup computes NB blocks of 16 columns of C (rows of W).  Its waves
 // take the blocks' tiles in turn (wave w the tiles w, w + W, ..: together they
@@ -358,7 +358,7 @@ struct W4Params {
 
 // Sums of the waves (W x JC sets of them) in order, rounded once.
 template <int NB, int W, int JC>
-__device__ __forceinline__ void w4_join_waves(const W4Params &p, int32_t b0,
+__device__ __forceinline__ void w4_join_waves(const W4Params &p, int32_t b0, int32_t m0,
                                               const float (*red)[NB][16][20])
 {
     constexpr int MC = 16 / JC;
@@ -371,8 +371,8 @@ __device__ __forceinline__ void w4_join_waves(const W4Params &p, int32_t b0,
 #pragma unroll
             for (int j = 0; j < JC; ++j) sum += red[w][nb][j * MC + m][n];
         const int64_t col = static_cast<int64_t>(b0 + nb) * 16 + n;
-        if (m < p.M && col < p.N)
-            reinterpret_cast<_Float16 *>(p.C)[static_cast<int64_t>(m) * p.N + col] =
+        if (m0 + m < p.M && col < p.N)
+            reinterpret_cast<_Float16 *>(p.C)[static_cast<int64_t>(m0 + m) * p.N + col] =
                 static_cast<_Float16>(sum);
     }
 }
@@ -501,7 +501,7 @@ __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
             if (jj == j) v = acc[nb][j];
         *reinterpret_cast<f32x4_t *>(&red[wave][nb][r][kq * 4]) = v;
     }
-    w4_join_waves<NB, W, JC>(p, b0, red);
+    w4_join_waves<NB, W, JC>(p, b0, 0, red);
 }
 
 // At most 4 RL rows of A.  Loads of A in the MFMA's own layout touch 64 bytes
@@ -512,13 +512,19 @@ __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
 // against 6.9 at K = 4096.  Several blocks a workgroup use the rows of A more
 // than once, where N still gives nearly every CU a workgroup (16 x 16384 x
 // 16384: 45 us with one, 33 with two, 29.2 with four; 16 x 4096 x 14336: 12.5,
-// 14.9, 22.5).
+// 14.9, 22.5).  For 17 to 48 rows, two or three tiles of 16 share a word's
+// unpacking, and no sum goes through memory as it does where tiles split K (32 x
+// 4096 x 4096: 7.5 us, 9.8 in tiles; 48 x 4096 x 4096 9.5 and 11.8).
 template <int SH, int RL, int NB, int W>
 __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
 {
     constexpr int NS = 128 >> SH;
-    __shared__ float red[W][NB][16][20];
-    __shared__ half8_t abuf[W][RL * 4][16];
+    constexpr int MT = (RL + 3) / 4;   // tiles of 16 rows of A
+    union Lds {
+        float red[W][NB][16][20];
+        half8_t abuf[W][RL * 4][16];
+    };
+    __shared__ Lds lds;
     const int lane = threadIdx.x & 63;
     const int wave = wave_index();
     const int r = lane & 15, kq = lane >> 4;
@@ -527,7 +533,7 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
 #pragma unroll
     for (int i = 0; i < RL; ++i)
         arow[i] = p.A + static_cast<int64_t>(min(4 * i + kq, p.M - 1)) * p.K;
-    half8_t *ab = abuf[wave][0];
+    half8_t *ab = lds.abuf[wave][0];
     const u32x4_t *words[NB];
     const uint16_t *scales[NB];
 #pragma unroll
@@ -537,7 +543,7 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
         scales[nb] = p.scales + b * p.kt * NS * 16 + r;
     }
     const W4Bits bits = w4_low_bits();
-    f32x4_t acc[NB] = {};
+    f32x4_t acc[NB][MT] = {};
     u32x4_t wv[2][NB];
     half8_t af[2][RL];
     _Float16 sc[2][NB][NS];
@@ -559,20 +565,27 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
     // columns past 4 RL repeat the last row, like rows past M: not stored
     const int rr = r < RL * 4 ? r : RL * 4 - 1;
     auto mma = [&](int buf, int) {
-        half8_t a[4];
+        half8_t a[4][MT];
         // the wave alone uses these 4 RL rows, and its LDS operations keep
         // their order
 #pragma unroll
-        for (int i = 0; i < RL; ++i) ab[(4 * i + kq) * 16 + (r ^ (4 * i + kq))] = af[buf][i];
+        for (int i = 0; i < RL; ++i)
+            ab[(4 * i + kq) * 16 + (r ^ ((4 * i + kq) & 15))] = af[buf][i];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = ab[rr * 16 + ((4 * j + kq) ^ rr)];
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                a[j][mt] = ab[(16 * mt + rr) * 16 + ((4 * j + kq) ^ rr)];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    w4_scaled(wv[buf][nb][j], sc[buf][nb][(32 * j) >> SH], bits), a[j], acc[nb], 0, 0,
-                    0);
+            for (int j = 0; j < 4; ++j) {
+                const half8_t w = w4_scaled(wv[buf][nb][j], sc[buf][nb][(32 * j) >> SH], bits);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    acc[nb][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, a[j][mt], acc[nb][mt], 0,
+                                                                         0, 0);
+            }
     };
     const int32_t full = p.K / 128;
     w4_run_tiles<W, 1>(full, wave, load, mma);
@@ -587,9 +600,13 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
         mma(0, 0);
     }
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-        *reinterpret_cast<f32x4_t *>(&red[wave][nb][r][kq * 4]) = acc[nb];
-    w4_join_waves<NB, W, 1>(p, b0, red);
+    for (int mt = 0; mt < MT; ++mt) {
+        __syncthreads();   // the sums' LDS is that of the rows, or of the last sums
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+            *reinterpret_cast<f32x4_t *>(&lds.red[wave][nb][r][kq * 4]) = acc[nb][mt];
+        w4_join_waves<NB, W, 1>(p, b0, mt * 16, lds.red);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1568,28 +1585,32 @@ static int decode_gemm(const Decode &d, int64_t M, int64_t N, int64_t K, bool tn
 // for each group size.
 struct W4Kernel {
     int32_t kernel, rows, blocks, waves;   // rows of A, blocks of 16 rows of W a workgroup
-    // tile kernels: us a step of 128 columns with one workgroup on a CU, and
-    // with two (0: they do not fit)
-    double step1, step2;
+    // Where a model of times chooses: us before the first step and a step of 128
+    // columns (for each wave of a stream kernel) with one workgroup on a CU, and
+    // with two (0: they do not fit).
+    double start, step1, step2;
     const void *fn[3];                     // group 32, 64, 128
 };
-#define W4_KERNEL(KIND, ROWS, BLOCKS, W, T1, T2, K5, K6, K7)                          \
-    W4Kernel{KIND, ROWS, BLOCKS, W, T1, T2,                                           \
+#define W4_KERNEL(KIND, ROWS, BLOCKS, W, T0, T1, T2, K5, K6, K7)                      \
+    W4Kernel{KIND, ROWS, BLOCKS, W, T0, T1, T2,                                       \
              {reinterpret_cast<const void *>(&K5), reinterpret_cast<const void *>(&K6), \
               reinterpret_cast<const void *>(&K7)}}
 #define W4_STREAM(JC, NB, W, D)                                                       \
-    W4_KERNEL(GEMM_F16_LOWBIT_STREAM, 16 / JC, NB, W, 0, 0, (w4_stream_kernel<5, JC, NB, W, D>), \
+    W4_KERNEL(GEMM_F16_LOWBIT_STREAM, 16 / JC, NB, W, 0, 0, 0, (w4_stream_kernel<5, JC, NB, W, D>), \
               (w4_stream_kernel<6, JC, NB, W, D>), (w4_stream_kernel<7, JC, NB, W, D>))
-#define W4_ROWS(RL, NB, W)                                                            \
-    W4_KERNEL(GEMM_F16_LOWBIT_STREAM, 4 * RL, NB, W, 0, 0, (w4_rows_kernel<5, RL, NB, W>),  \
+#define W4_ROWS(RL, NB, W, T0, T1, T2)                                                \
+    W4_KERNEL(GEMM_F16_LOWBIT_STREAM, 4 * RL, NB, W, T0, T1, T2, (w4_rows_kernel<5, RL, NB, W>),  \
               (w4_rows_kernel<6, RL, NB, W>), (w4_rows_kernel<7, RL, NB, W>))
 #define W4_TILE(MT, NB, W, S, T1, T2)                                                 \
-    W4_KERNEL(GEMM_F16_LOWBIT_TILE, 16 * MT, NB * W, W, T1, T2, (w4_tile_kernel<5, MT, NB, W, S>), \
+    W4_KERNEL(GEMM_F16_LOWBIT_TILE, 16 * MT, NB * W, W, 3.7, T1, T2, (w4_tile_kernel<5, MT, NB, W, S>), \
               (w4_tile_kernel<6, MT, NB, W, S>), (w4_tile_kernel<7, MT, NB, W, S>))
 static const W4Kernel kW4Kernels[] = {
     W4_STREAM(4, 1, 8, 2),
-    W4_ROWS(2, 1, 8), W4_ROWS(2, 2, 8),
-    W4_ROWS(4, 1, 8), W4_ROWS(4, 2, 8), W4_ROWS(4, 4, 8),
+    W4_ROWS(2, 1, 8, 0, 0, 0), W4_ROWS(2, 2, 8, 0, 0, 0),
+    W4_ROWS(4, 1, 8, 0, 0, 0), W4_ROWS(4, 2, 8, 0, 0, 0), W4_ROWS(4, 4, 8, 0, 0, 0),
+    W4_ROWS(8, 1, 8, 2.63, 1.043, 0),      W4_ROWS(8, 2, 4, 3.33, 0.625, 1.290),
+    W4_ROWS(8, 4, 8, 3.44, 2.101, 0),      W4_ROWS(12, 1, 8, 2.83, 1.452, 0),
+    W4_ROWS(12, 2, 4, 3.96, 0.806, 1.629), W4_ROWS(12, 4, 4, 4.45, 1.382, 0),
     W4_TILE(2, 2, 4, 4, 0.518, 0.813), W4_TILE(3, 2, 8, 2, 0.911, 1.474),
     W4_TILE(4, 2, 4, 3, 0.689, 1.061), W4_TILE(4, 2, 8, 3, 0.989, 0),
     W4_TILE(6, 2, 8, 3, 1.209, 0),     W4_TILE(7, 2, 8, 3, 1.366, 0),
@@ -1608,19 +1629,65 @@ struct W4Choice {
 // grid does not grow with them.
 constexpr int64_t W4_MOST_WORKGROUPS = 1 << 22;
 
-// The tile kernels and splits, and the decoding path, by a model of their
-// times in us, fitted to 4,000 timings of 117 shapes (24 to 2048 rows, N and K
-// of 1024 to 16384, words from HBM): rounds of workgroups over the CUs times
-// the steps of a range, the clock that long products lose to the power limit,
-// and for a split the partial sums' way through memory and the join.  Its error
-// is 6%; what it chose took 1.1% longer than the best of each shape in the mean,
-// 16% in the worst.
-static W4Choice w4_choose_tile(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
+// Kernel `e`'s time in us by the model, its K in `ranges` ranges of `steps` steps.
+static double w4_model(const W4Kernel &e, int64_t workgroups, int64_t steps, int64_t ranges,
+                       int32_t cus)
+{
+    const bool two = e.step2 > 0;
+    const int64_t slots = static_cast<int64_t>(cus) * (two ? 2 : 1);
+    const int64_t full = workgroups / slots, rest = workgroups % slots;
+    double us = e.start + full * (two ? e.step2 : e.step1) * steps;
+    if (rest > 0) us += (rest <= cus || !two ? e.step1 : e.step2) * steps;
+    if (ranges > 1)
+        us += 1.5 + 0.114 * ranges +
+              3.41e-7 * static_cast<double>(workgroups) * (e.rows / 16) * e.blocks * 1024;
+    return us;
+}
+
+// The stream kernel for at most 48 rows, and its time (16 rows and fewer: none).
+static int32_t w4_choose_stream(int64_t M, const W4Shape &s, int32_t cus, double *best_us)
+{
+    if (M <= 4) return 0;
+    // the most blocks a workgroup that still give three CUs in four one
+    const int64_t most = s.nb / std::max<int64_t>(1, 3 * static_cast<int64_t>(cus) / 4);
+    if (M <= 8) return most >= 2 ? 2 : 1;
+    if (M <= 16) return most >= 4 ? 5 : most >= 2 ? 4 : 3;
+    int32_t best = -1;
+    for (int32_t id = 0; id < kNumW4Kernels; ++id) {
+        const W4Kernel &e = kW4Kernels[id];
+        if (e.kernel != GEMM_F16_LOWBIT_STREAM || e.start == 0 || e.rows < M) continue;
+        const double us = w4_model(e, cdiv(s.nb, e.blocks), cdiv(s.kt, e.waves), 1, cus);
+        if (best < 0 || us < *best_us) {
+            *best_us = us;
+            best = id;
+        }
+    }
+    return best;
+}
+constexpr int64_t W4_STREAM_ROWS = 48;
+
+// The stream kernels up to 48 rows, the tile kernels and splits, and the
+// decoding path, by a model of their times in us, fitted to 8,000 timings of
+// 160 shapes (20 to 2048 rows, N and K of 512 to 32768, words from HBM): rounds
+// of workgroups over the CUs times the steps of a range, the clock that long
+// products lose to the power limit, and for a split the partial sums' way
+// through memory and the join.  Its error is 6%; what it chose took 1.1% longer
+// than the best of each shape in the mean, 16% in the worst.  (Of 17 to 48 rows,
+// the tile kernels alone took 25% longer: 32 x 4096 x 4096 9.8 us, streamed 7.5.)
+static W4Choice w4_search(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
 {
     const double nk = static_cast<double>(s.nb) * 16 * K;
     // words to fp16 and back from memory, and the GEMM at its rate for large M
     W4Choice best = {-1, 1};
     double best_us = 12.2 + (7.0e-7 + 1.13e-9 * std::max<double>(M, 423)) * std::max(nk, 8.4e6);
+    if (M <= W4_STREAM_ROWS) {
+        double us = 0;
+        const int32_t id = w4_choose_stream(M, s, cus, &us);
+        if (us < best_us) {
+            best_us = us;
+            best.id = id;
+        }
+    }
     // 32-bit offsets of the tile kernel's resources
     if (M > 8192 || K > (1 << 21)) return best;
     for (int32_t id = 0; id < kNumW4Kernels; ++id) {
@@ -1628,21 +1695,15 @@ static W4Choice w4_choose_tile(int64_t M, int64_t K, const W4Shape &s, int32_t c
         if (e.kernel != GEMM_F16_LOWBIT_TILE) continue;
         const int64_t tiles = cdiv(M, e.rows) * cdiv(s.nb, e.blocks);
         if (tiles > W4_MOST_WORKGROUPS) continue;
-        const bool two = e.step2 > 0;
-        const int64_t slots = static_cast<int64_t>(cus) * (two ? 2 : 1);
+        const int64_t slots = static_cast<int64_t>(cus) * (e.step2 > 0 ? 2 : 1);
         int64_t last = 0;
         for (int64_t sp = 1; sp <= 64 && sp <= s.kt && (sp == 1 || tiles * sp <= 4 * slots); ++sp) {
             const int64_t per = cdiv(s.kt, sp);
             if (per == last) continue;   // the same ranges
             last = per;
-            const int64_t ranges = cdiv(s.kt, per), wgs = tiles * ranges;
-            const int64_t full = wgs / slots, rest = wgs % slots;
-            double us = 3.7 + full * (two ? e.step2 : e.step1) * per;
-            if (rest > 0) us += (rest <= cus || !two ? e.step1 : e.step2) * per;
-            if (ranges > 1)
-                us += 1.5 + 0.114 * ranges +
-                      3.41e-7 * static_cast<double>(wgs) * (e.rows / 16) * e.blocks * 1024;
-            us += 2.26e-10 * std::max(0.0, nk * static_cast<double>(M) - 1.22e10);
+            const int64_t ranges = cdiv(s.kt, per);
+            const double us = w4_model(e, tiles * ranges, per, ranges, cus) +
+                              2.26e-10 * std::max(0.0, nk * static_cast<double>(M) - 1.22e10);
             if (us < best_us) {
                 best_us = us;
                 best = {id, static_cast<int32_t>(ranges)};
@@ -1655,11 +1716,7 @@ static W4Choice w4_choose_tile(int64_t M, int64_t K, const W4Shape &s, int32_t c
 static W4Choice w4_choose(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
 {
     if (s.nb > W4_MOST_WORKGROUPS) return {-1, 1};
-    if (M <= 4) return {0, 1};
-    // the most blocks a workgroup that still give three CUs in four one
-    const int64_t most = s.nb / std::max<int64_t>(1, 3 * static_cast<int64_t>(cus) / 4);
-    if (M <= 8) return {most >= 2 ? 2 : 1, 1};
-    if (M <= 16) return {most >= 4 ? 5 : most >= 2 ? 4 : 3, 1};
+    if (M <= 16) return {w4_choose_stream(M, s, cus, nullptr), 1};
     // the search takes microseconds: each thread keeps its last few choices
     struct Entry {
         int64_t M, K, nb;
@@ -1670,7 +1727,7 @@ static W4Choice w4_choose(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
     static thread_local int next = 0;
     for (const Entry &c : cache)
         if (c.cus == cus && c.M == M && c.K == K && c.nb == s.nb) return c.choice;
-    const W4Choice choice = w4_choose_tile(M, K, s, cus);
+    const W4Choice choice = w4_search(M, K, s, cus);
     cache[next] = Entry{M, K, s.nb, cus, choice};
     next = (next + 1) % 8;
     return choice;
@@ -1758,11 +1815,12 @@ static int w4_run(const W4Choice &c, const gemm_f16_lowbit_plan_t &plan, int64_t
         return w4_stream(c.id, M, N, K, s, A, words, scales, C, stream);
     if (K % 8 == 0 && reinterpret_cast<uintptr_t>(A) % 16 != 0) {
         // the tile kernels' loads need 16-byte aligned rows, and the workspace
-        // is planned by sizes alone: 16 rows at a time by the kernels that
-        // take any alignment
-        for (int64_t m = 0; m < M; m += 16) {
-            const int64_t rows = std::min<int64_t>(16, M - m);
-            const int v = w4_stream(w4_choose(rows, K, s, cus).id, rows, N, K, s,
+        // is planned by sizes alone: 48 rows at a time by the kernels that take
+        // any alignment
+        for (int64_t m = 0; m < M; m += W4_STREAM_ROWS) {
+            const int64_t rows = std::min(W4_STREAM_ROWS, M - m);
+            double us = 0;
+            const int v = w4_stream(w4_choose_stream(rows, s, cus, &us), rows, N, K, s,
                                     static_cast<const uint16_t *>(A) + m * K, words, scales,
                                     static_cast<uint16_t *>(C) + m * N, stream);
             if (v != GEMM_F16_OK) return v;
