@@ -38,6 +38,14 @@ __device__ __forceinline__ T bits_as(S s)
 // it alone (which tile, its addresses) then takes no vector operations.
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
+// This workgroup's unit of work, where each XCD (workgroups mod 8) takes a
+// contiguous range of them: neighbours share cache lines in its L2.
+__device__ __forceinline__ int32_t xcd_unit()
+{
+    const int32_t q = gridDim.x >> 3, rem = gridDim.x & 7, x = blockIdx.x & 7;
+    return x * q + (x < rem ? x : rem) + (blockIdx.x >> 3);
+}
+
 // Eight halves of a row at column c, as dwords; columns at or past `cols` are 0.
 __device__ __forceinline__ u32x4_t load8(const uint16_t *row, int32_t c, int32_t cols)
 {
@@ -147,7 +155,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_encode_kernel(W4EncodeParams p)
     const int r = lane & 15, kq = lane >> 4;
     const int per_tile = 128 >> p.shift;
     const int64_t step = static_cast<int64_t>(gridDim.x) * WAVES;
-    for (int64_t tile = static_cast<int64_t>(blockIdx.x) * WAVES + wave_index(); tile < p.tiles;
+    for (int64_t tile = static_cast<int64_t>(xcd_unit()) * WAVES + wave_index(); tile < p.tiles;
          tile += step) {
         const int32_t b = static_cast<int32_t>(tile) / p.kt;
         const int32_t t = static_cast<int32_t>(tile) - b * p.kt;
@@ -319,7 +327,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_decode_kernel(W4DecodeParams p)
     const W4Bits bits = w4_low_bits();
     const int per_tile = 128 >> p.shift;
     const int64_t step = static_cast<int64_t>(gridDim.x) * WAVES;
-    for (int64_t tile = static_cast<int64_t>(blockIdx.x) * WAVES + wave_index(); tile < p.tiles;
+    for (int64_t tile = static_cast<int64_t>(xcd_unit()) * WAVES + wave_index(); tile < p.tiles;
          tile += step) {
         const int32_t b = static_cast<int32_t>(tile) / p.kt;
         const int32_t t = static_cast<int32_t>(tile) - b * p.kt;
@@ -716,13 +724,8 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
     const int lane = threadIdx.x & 63;
     const int wave = wave_index();
     const int r = lane & 15, kq = lane >> 4;
-    // Units run over the rows of A first, so that a word's users are
-    // neighbours, and each XCD (workgroups u mod 8) takes a contiguous range.
-    int32_t u = blockIdx.x;
-    {
-        const int32_t q = gridDim.x >> 3, rem = gridDim.x & 7, x = u & 7;
-        u = x * q + (x < rem ? x : rem) + (u >> 3);
-    }
+    // units run over the rows of A first, so that a word's users are neighbours
+    int32_t u = xcd_unit();
     const int32_t tm = u % p.tiles_m;
     const int32_t un = u / p.tiles_m;
     const int32_t tn = un % p.tiles_n;
@@ -976,7 +979,7 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v)
 
 __global__ __launch_bounds__(64 * WAVES) void q8_encode_kernel(Q8Params p)
 {
-    const int32_t rb = blockIdx.x / p.col_blocks, cb = blockIdx.x - rb * p.col_blocks;
+    const int32_t u = xcd_unit(), rb = u / p.col_blocks, cb = u - rb * p.col_blocks;
     const int32_t chunk = (cb << p.tx_shift) + (threadIdx.x & ((1 << p.tx_shift) - 1));
     const int32_t ty = (64 * WAVES) >> p.tx_shift;
     const int64_t row0 = static_cast<int64_t>(rb) * ty * Q8_ROWS + (threadIdx.x >> p.tx_shift);
@@ -1047,7 +1050,7 @@ __device__ __forceinline__ void q8_scaled(uint32_t codes, half2_t s2, half2_t *l
 
 __global__ __launch_bounds__(64 * WAVES) void q8_decode_kernel(Q8Params p)
 {
-    const int32_t rb = blockIdx.x / p.col_blocks, cb = blockIdx.x - rb * p.col_blocks;
+    const int32_t u = xcd_unit(), rb = u / p.col_blocks, cb = u - rb * p.col_blocks;
     const int32_t chunk = (cb << p.tx_shift) + (threadIdx.x & ((1 << p.tx_shift) - 1));
     const int32_t ty = (64 * WAVES) >> p.tx_shift;
     const int64_t row0 = static_cast<int64_t>(rb) * ty * Q8_ROWS + (threadIdx.x >> p.tx_shift);
@@ -1139,11 +1142,7 @@ __global__ __launch_bounds__(64 * W, 2) void q8_tn_kernel(Q8TnParams p)
     const int lane = threadIdx.x & 63;
     const int wave = wave_index();
     const int r = lane & 15, kq = lane >> 4;
-    int32_t u = blockIdx.x;
-    {
-        const int32_t q = gridDim.x >> 3, rem = gridDim.x & 7, x = u & 7;
-        u = x * q + (x < rem ? x : rem) + (u >> 3);
-    }
+    int32_t u = xcd_unit();
     const int32_t mtile = u % p.m_tiles;
     u /= p.m_tiles;
     const int32_t block = u % p.blocks, sp = u / p.blocks;
