@@ -1136,7 +1136,7 @@ __global__ __launch_bounds__(64 * W, 2) void q8_tn_kernel(Q8TnParams p)
     };
     union Lds {
         Wave wave[W];
-        float red[W][ROUND][64];
+        float red[W][ROUND][64 + 4];   // 4: the sums of a row apart in the banks
     };
     __shared__ __attribute__((aligned(16))) Lds lds;
     const int lane = threadIdx.x & 63;
@@ -1265,14 +1265,9 @@ __global__ __launch_bounds__(64 * W, 2) void q8_tn_kernel(Q8TnParams p)
             mma(0);
         }
     // sum idx = (mt, e, reg) of lane l: row m0 + 16 mt + r of C, column (block 16 + 4 kq + reg) CB + e
-    constexpr int ROUNDS = SUMS / ROUND, PER = ROUND / W;
-    static_assert(SUMS % ROUND == 0 && ROUND % W == 0, "rounds");
-    constexpr int EW = PER / 4;   // e's of a wave and round
-    static_assert(PER % 4 == 0, "a wave takes all four regs of an e");
-    float *to = nullptr;
-    if (p.partial)
-        to = p.partial + sp * p.stride +
-             (static_cast<int64_t>(block) * p.m_tiles + mtile) * (SUMS * 64) + lane;
+    constexpr int ROUNDS = SUMS / ROUND, PER = ROUND / W, RM = ROUND / (4 * CB);
+    static_assert(SUMS % ROUND == 0 && ROUND % W == 0 && ROUND % (4 * CB) == 0, "rounds");
+    const int64_t unit = static_cast<int64_t>(block) * p.m_tiles + mtile;
 #pragma unroll
     for (int rd = 0; rd < ROUNDS; ++rd) {
         __syncthreads();
@@ -1282,26 +1277,36 @@ __global__ __launch_bounds__(64 * W, 2) void q8_tn_kernel(Q8TnParams p)
             lds.red[wave][k][lane] = acc[idx / (4 * CB)][idx / 4 % CB][idx % 4];
         }
         __syncthreads();
+        if (p.partial) {   // a range's sums, in the order in which lanes hold them
+            float *to = p.partial + sp * p.stride + (unit * SUMS + rd * ROUND) * 64 + lane;
 #pragma unroll
-        for (int reg = 0; reg < 4; ++reg) {
-            float sum[EW];
+            for (int i = 0; i < PER; ++i) {
+                const int k = wave * PER + i;
+                float sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < EW; ++e) {
-                const int k = wave * PER + 4 * e + reg;
-                sum[e] = 0.0f;
-#pragma unroll
-                for (int w = 0; w < W; ++w) sum[e] += lds.red[w][k][lane];
-                if (to) to[(rd * ROUND + k) * 64] = sum[e];
+                for (int w = 0; w < W; ++w) sum += lds.red[w][k][lane];
+                to[k * 64] = sum;
             }
-            if (to) continue;
-            const int e0 = rd * (ROUND / 4) + wave * EW;   // over all mt
-            const int32_t m = m0 + e0 / CB * 16 + r;
-            const int64_t n = (static_cast<int64_t>(block) * 16 + 4 * kq + reg) * CB + e0 % CB;
-            if (m >= p.M) continue;
-            _Float16 *c = reinterpret_cast<_Float16 *>(p.C) + static_cast<int64_t>(m) * p.N + n;
+            continue;
+        }
+        // the whole sum, eight neighbouring columns a thread
 #pragma unroll
-            for (int e = 0; e < EW; ++e)
-                if (n + e < p.N) c[e] = static_cast<_Float16>(sum[e]);
+        for (int o = threadIdx.x; o < RM * 16 * 2 * CB; o += 64 * W) {
+            const int row = o / (2 * CB), c = o % (2 * CB) * 8;
+            const int l = c / (4 * CB) * 16 + row % 16;
+            const int32_t m = m0 + (rd * RM + row / 16) * 16 + row % 16;
+            const int64_t n = static_cast<int64_t>(block) * 16 * CB + c;
+            if (m >= p.M || n >= p.N) continue;
+            half8_t h;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int k = (row / 16 * CB + c % CB + i) * 4 + c / CB % 4;
+                float sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) sum += lds.red[w][k][l];
+                h[i] = static_cast<_Float16>(sum);
+            }
+            store8(p.C + static_cast<int64_t>(m) * p.N, static_cast<int32_t>(n), p.N, h);
         }
     }
 }
@@ -1877,7 +1882,7 @@ struct Q8Kernel {
 #define Q8_TN(MT, CB, W, STEP) \
     Q8Kernel{MT, CB, W, STEP, reinterpret_cast<const void *>(&q8_tn_kernel<MT, CB, W>)}
 static const Q8Kernel kQ8Kernels[] = {
-    Q8_TN(1, 8, 4, 0.675), Q8_TN(1, 16, 4, 1.04), Q8_TN(2, 8, 4, 0.780), Q8_TN(4, 8, 4, 1.04),
+    Q8_TN(1, 8, 4, 0.651), Q8_TN(1, 16, 4, 1.11), Q8_TN(2, 8, 4, 0.810), Q8_TN(4, 8, 4, 1.06),
 };
 #undef Q8_TN
 constexpr int kNumQ8Kernels = sizeof(kQ8Kernels) / sizeof(kQ8Kernels[0]);
@@ -1906,13 +1911,14 @@ static Q8Choice q8_layout(int32_t id, int64_t M, int64_t K, const Q8Shape &s, in
 }
 
 // Streaming the codes (in one range, or in as many as fill the CUs), or
-// decoding them for the GEMM, by models of their times in us, fitted to 3,900
-// timings of 661 shapes (8 to 7668 rows of C, 64 to 14336 columns, 54 to 8192
+// decoding them for the GEMM, by models of their times in us, fitted to 2,900
+// timings of 870 shapes (8 to 7668 rows of C, 64 to 14336 columns, 3 to 8192
 // rows of X, sizes that are multiples of 8 and not).  Streaming reads the codes
 // again for each tile of rows of C; it wins up to some 64 rows everywhere (1.1
-// to 3.2 times), and with hundreds of rows where the columns are few.  What the
-// models chose took 1.1% longer than the best of each shape in the mean, 34% in
-// the worst.
+// to 3.2 times), with hundreds of rows where the columns are few, and with
+// thousands where the rows of X are (3300 x 3613 over 54 rows: 31.4 us decoded,
+// 19.8 streamed).  What the models chose took 1.6% longer than the best of each
+// shape in the mean, 37% in the worst.
 static Q8Choice q8_choose(int64_t M, int64_t N, int64_t K, const Q8Shape &s, int32_t cus)
 {
     const double m = static_cast<double>(M), n = static_cast<double>(N), k = static_cast<double>(K);
@@ -1920,18 +1926,18 @@ static Q8Choice q8_choose(int64_t M, int64_t N, int64_t K, const Q8Shape &s, int
     // 32-bit counts of tiles and values in the kernels
     if (s.groups > (1 << 20) || M > (1 << 20) || M * s.groups > (1 << 26)) return best;
     // 1 us of each workspace is the caller's, who has to get one
-    double best_us = 9.7 + 6.93e-7 * n * k + 1.68e-9 * std::max(m, 128.0) * std::max(n, 128.0) * k +
-                     1.47e-3 * k + 2.87e-7 * m * n;
-    if (M % 8 != 0) best_us += 2.97 + 7.39e-7 * m * k;                // A's copy
-    if (M % 8 != 0 || N % 8 != 0) best_us += 2.97 + 7.88e-7 * m * n;   // and C's
+    double best_us = 12.0 + 6.56e-7 * n * k + 1.62e-9 * std::max(m, 128.0) * std::max(n, 128.0) * k +
+                     7.8e-4 * k + 2.07e-7 * m * n;
+    if (M % 8 != 0) best_us += 3.02 + 7.49e-7 * m * k;                // A's copy
+    if (M % 8 != 0 || N % 8 != 0) best_us += 3.02 + 7.93e-7 * m * n;   // and C's
     for (int32_t id = 0; id < 2 * kNumQ8Kernels; ++id) {
         const Q8Kernel &e = kQ8Kernels[id / 2];
         const Q8Choice c = q8_layout(id / 2, M, K, s, cus, id % 2 != 0);
         const int64_t wgs = c.blocks * c.m_tiles * c.splits;
         const double values = static_cast<double>(wgs) * e.mt * e.cb * 256;
-        double us = 4.03 + static_cast<double>(cdiv(wgs, cus) * cdiv(c.t_split / 32, e.waves)) * e.step;
-        us += c.splits > 1 ? 2.8 + 2.81e-6 * values + 0.0663 * static_cast<double>(c.splits)
-                           : 4.31e-6 * values;
+        double us = 3.95 + static_cast<double>(cdiv(wgs, cus) * cdiv(c.t_split / 32, e.waves)) * e.step;
+        us += c.splits > 1 ? 2.55 + 2.47e-6 * values + 0.0623 * static_cast<double>(c.splits)
+                           : 6.53e-7 * values;
         if (us < best_us) {
             best_us = us;
             best = c;

@@ -325,8 +325,10 @@ Q8_KERNELS = [((1, 16, 128, 4), 1, 7, 1000, 5), ((1, 16, 128, 4), 1, 16, 300, 50
               ((1, 32, 128, 4), 1, 1500, 333, 40), ((1, 64, 128, 4), 2, 130, 4096, 4000),
               ((1, 64, 128, 4), 3, 1069, 463, 2357), ((1, 64, 128, 4), 2, 1001, 999, 8001),
               ((1, 64, 128, 4), 1, 100, 14337, 33), ((0,), 1, 1600, 1608, 3000),
-              ((0,), 1, 1601, 1608, 1500), ((0,), 1, 1600, 1603, 1500), ((0,), 1, 1601, 1601, 1500),
-              ((0,), 4, 3000, 64, 2048)]
+              ((0,), 1, 1601, 1608, 2357), ((0,), 1, 1600, 1603, 1500), ((0,), 1, 1601, 1603, 2357),
+              ((0,), 3, 3000, 300, 2357), ((0,), 4, 333, 4096, 8000), ((0,), 5, 1500, 999, 8000),
+              ((1, 64, 128, 4), 1, 3001, 1999, 70), ((1, 32, 128, 4), 1, 1500, 300, 3),
+              ((1, 16, 256, 4), 1, 130, 7001, 45)]
 
 
 @pytest.mark.parametrize("kernel,splits,m,n,k", Q8_KERNELS)
@@ -467,7 +469,7 @@ def test_rows_of_a_checkpoint(g):
 
 # ---- how they are called --------------------------------------------------------
 W4_CALLS = [(1, 512, 1024), (24, 512, 1024), (80, 512, 1024), (1200, 512, 256)]
-Q8_CALLS = [(16, 512, 2000), (50, 512, 2000), (512, 1024, 2000)]
+Q8_CALLS = [(16, 512, 2000), (50, 512, 2000), (512, 1024, 2000), (1200, 1024, 2000)]
 
 
 def products(g, rng):
