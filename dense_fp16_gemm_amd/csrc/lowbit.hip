@@ -891,11 +891,26 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
                 *reinterpret_cast<f32x4_t *>(to + (nb * MT + mt) * 256) = acc[mt][nb];
         return;
     }
+    // C through LDS, so that a row's columns leave in one run (stored as lanes
+    // hold them, 32 bytes of a row at a time, 3936 x 15296 x 64 took 56.3 us; 42.8)
+    constexpr int COLS = 16 * NB * W, PITCH = COLS + 8;
+    static_assert(16 * MT * PITCH * 2 <= S * STAGE, "LDS");
+    _Float16 *rows_c = reinterpret_cast<_Float16 *>(smem);
+    __syncthreads();
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-            store4(p.C, p.M, p.N, m0 + mt * 16 + r, (b0 + nb) * 16 + kq * 4, acc[mt][nb]);
+            *reinterpret_cast<half4_t *>(&rows_c[(mt * 16 + r) * PITCH + (wave * NB + nb) * 16 + kq * 4]) =
+                __builtin_convertvector(acc[mt][nb], half4_t);
+    __syncthreads();
+    for (int o = threadIdx.x; o < 2 * MT * COLS; o += 64 * W) {
+        const int row = o / (COLS / 8), c = o % (COLS / 8) * 8;
+        const int32_t n = tn * COLS + c;
+        if (row >= rows || n >= p.N) continue;
+        store8(p.C + static_cast<int64_t>(m0 + row) * p.N, n, p.N,
+               *reinterpret_cast<const half8_t *>(&rows_c[row * PITCH + c]));
+    }
 }
 
 // C from the ranges' sums, in order; one lane's four values a thread.
