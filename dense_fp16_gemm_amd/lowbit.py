@@ -25,12 +25,14 @@ torch = None
 
 
 def _bind_torch() -> None:
-    global torch, _f16, _current_device, _raw_stream
+    global torch, _f16, _int8, _empty, _current_device, _raw_stream, _lib
     import torch as t
 
-    _f16 = t.float16
-    _current_device = t.cuda.current_device
-    # the raw handle without building a Stream object, where torch has the query
+    _f16, _int8, _empty = t.float16, t.int8, t.empty_strided
+    _lib = load()
+    # without torch's check that CUDA is initialised (the operands are on a GPU),
+    # and the raw handle without building a Stream object, where torch has these
+    _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
     _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: t.cuda.current_stream(index).cuda_stream)
     torch = t
@@ -234,18 +236,21 @@ class Q8Matrix:
 
 # ---- torch convenience -------------------------------------------------------
 # A call for one token is a few microseconds on the GPU, so the path to it is
-# kept short: one call into the library, no wrapper objects, no device switch
-# where the device is current.
-def _matrix(x, dtype, what: str):
+# kept short: few Python calls, one into the library, no wrapper objects, no
+# device switch where the device is current.
+def _is_matrix(x, dtype) -> bool:
+    return x.dtype is dtype and x.dim() == 2 and x.is_cuda and x.is_contiguous()
+
+
+def _refuse(x, dtype, what: str):
+    """Raises what is wrong with an x that is not _is_matrix(x, dtype)."""
     if x.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}")
     if x.dim() != 2:
         raise ValueError(f"{what} must be a matrix")
     if not x.is_cuda:
         raise ValueError(f"{what} must be on a GPU")
-    if not x.is_contiguous():
-        raise ValueError(f"{what} must be contiguous (row-major)")
-    return x.shape
+    raise ValueError(f"{what} must be contiguous (row-major)")
 
 
 def _call(index, stream, fn, *args) -> None:
@@ -270,6 +275,13 @@ def _new(on, stream, shape, dtype):
         return on.new_empty(shape, dtype=dtype)
 
 
+def _new_rows(on, stream, rows, cols, dtype):
+    """_new() of a matrix, by torch's quickest way."""
+    if stream is None:
+        return _empty((rows, cols), (cols, 1), dtype=dtype, device=on.device)
+    return _new(on, stream, (rows, cols), dtype)
+
+
 def _record(stream, *tensors) -> None:
     """Tensors of other streams, used on `stream`: not to be reused before it is done."""
     for t in tensors:
@@ -279,7 +291,7 @@ def _record(stream, *tensors) -> None:
 
 def _output(out, on, stream, shape):
     if out is None:
-        return _new(on, stream, shape, _f16)
+        return _new_rows(on, stream, *shape, _f16)
     if stream is not None and stream.device != on.device:
         raise ValueError(f"stream is on {stream.device}, the operands on {on.device}")
     if out.dtype != _f16 or tuple(out.shape) != shape or not out.is_contiguous() or \
@@ -300,9 +312,11 @@ def quantize_w4(w, group: int = 128, stream=None) -> W4Matrix:
     """w [N, K] fp16 in 4-bit codes, a scale for each `group` weights of a row."""
     if torch is None:
         _bind_torch()
-    n, k = _matrix(w, _f16, "w")
+    if not _is_matrix(w, _f16):
+        _refuse(w, _f16, "w")
+    n, k = w.shape
     q = _new_w4(w, stream, n, k, group)
-    _call(w.get_device(), stream, load().gemm_f16_w4_quantize, n, k, group, w.data_ptr(),
+    _call(w.get_device(), stream, _lib.gemm_f16_w4_quantize, n, k, group, w.data_ptr(),
           q.words.data_ptr(), q.scales.data_ptr())
     if stream is not None:
         _record(stream, w)
@@ -316,14 +330,18 @@ def pack_w4(codes, scales, group: int = 128, stream=None) -> W4Matrix:
     that is not finite, a weight past 65504) becomes NaN."""
     if torch is None:
         _bind_torch()
-    n, k = _matrix(codes, torch.int8, "codes")
+    if not _is_matrix(codes, _int8):
+        _refuse(codes, _int8, "codes")
+    if not _is_matrix(scales, _f16):
+        _refuse(scales, _f16, "scales")
+    n, k = codes.shape
     q = _new_w4(codes, stream, n, k, group)
-    if tuple(_matrix(scales, _f16, "scales")) != (n, -(-k // group)):
+    if tuple(scales.shape) != (n, -(-k // group)):
         raise ValueError(f"scales{tuple(scales.shape)} do not fit codes{tuple(codes.shape)} in "
                          f"groups of {group}")
     if codes.device != scales.device:
         raise ValueError("codes and scales must be on the same GPU")
-    _call(codes.get_device(), stream, load().gemm_f16_w4_pack, n, k, group, codes.data_ptr(),
+    _call(codes.get_device(), stream, _lib.gemm_f16_w4_pack, n, k, group, codes.data_ptr(),
           scales.data_ptr(), q.words.data_ptr(), q.scales.data_ptr())
     if stream is not None:
         _record(stream, codes, scales)
@@ -336,7 +354,7 @@ def dequantize_w4(w: W4Matrix, out=None, stream=None):
         raise TypeError("w must be a W4Matrix")
     words = w.words
     out = _output(out, words, stream, (w.n, w.k))
-    _call(words.get_device(), stream, load().gemm_f16_w4_dequantize, w.n, w.k, w.group,
+    _call(words.get_device(), stream, _lib.gemm_f16_w4_dequantize, w.n, w.k, w.group,
           words.data_ptr(), w.scales.data_ptr(), out.data_ptr())
     if stream is not None:
         _record(stream, words, w.scales, out)
@@ -347,11 +365,13 @@ def quantize_q8(x, stream=None) -> Q8Matrix:
     """x [R, N] fp16 in 8-bit codes, a scale for each 32 values of a row."""
     if torch is None:
         _bind_torch()
-    r, n = _matrix(x, _f16, "x")
+    if not _is_matrix(x, _f16):
+        _refuse(x, _f16, "x")
+    r, n = x.shape
     groups = -(-n // Q8_GROUP)
-    codes = _new(x, stream, (r, groups * Q8_GROUP), torch.int8)
-    scales = _new(x, stream, (r, groups), _f16)
-    _call(x.get_device(), stream, load().gemm_f16_q8_quantize, r, n, x.data_ptr(),
+    codes = _new_rows(x, stream, r, groups * Q8_GROUP, _int8)
+    scales = _new_rows(x, stream, r, groups, _f16)
+    _call(x.get_device(), stream, _lib.gemm_f16_q8_quantize, r, n, x.data_ptr(),
           codes.data_ptr(), scales.data_ptr())
     if stream is not None:
         _record(stream, x)
@@ -364,7 +384,7 @@ def dequantize_q8(x: Q8Matrix, out=None, stream=None):
         raise TypeError("x must be a Q8Matrix")
     codes = x.codes
     out = _output(out, codes, stream, (x.r, x.n))
-    _call(codes.get_device(), stream, load().gemm_f16_q8_dequantize, x.r, x.n, codes.data_ptr(),
+    _call(codes.get_device(), stream, _lib.gemm_f16_q8_dequantize, x.r, x.n, codes.data_ptr(),
           x.scales.data_ptr(), out.data_ptr())
     if stream is not None:
         _record(stream, codes, x.scales, out)
@@ -376,23 +396,19 @@ def dequantize_q8(x: Q8Matrix, out=None, stream=None):
 _workspace_bytes: dict = {}
 
 
-def _workspace_need(key) -> int:
+def _plan_workspace(key) -> int:
     """The bytes that key[0](*key[1:-1], compute units of device key[-1]) plans."""
-    need = _workspace_bytes.get(key)
-    if need is None:
-        with torch.cuda.device(key[-1]):
-            need = key[0](*key[1:-1], gemm_f16_device_cus()).workspace_bytes
-        if len(_workspace_bytes) >= 1024:
-            _workspace_bytes.clear()
-        _workspace_bytes[key] = need
+    with torch.cuda.device(key[-1]):
+        need = key[0](*key[1:-1], gemm_f16_device_cus()).workspace_bytes
+    if len(_workspace_bytes) >= 1024:
+        _workspace_bytes.clear()
+    _workspace_bytes[key] = need
     return need
 
 
 def _workspace(need, on, workspace, stream):
-    """(tensor or None, its address, its bytes)."""
+    """(tensor, its address, its bytes)."""
     if workspace is None:
-        if not need:
-            return None, 0, 0
         workspace = _new(on, stream, (need,), torch.uint8)
         return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != on.device or not workspace.is_contiguous():
@@ -406,7 +422,9 @@ def gemm_nt_w4(a, w: W4Matrix, out=None, workspace=None, stream=None):
     gemm_f16_nt_w4_plan) is allocated with torch unless `workspace` is given."""
     if not isinstance(w, W4Matrix):
         raise TypeError("w must be a W4Matrix")
-    m, k = _matrix(a, _f16, "a")
+    if not _is_matrix(a, _f16):
+        _refuse(a, _f16, "a")
+    m, k = a.shape
     n, words = w.n, w.words
     if k != w.k:
         raise ValueError(f"shape mismatch: a{tuple(a.shape)} w{w.shape}")
@@ -414,9 +432,14 @@ def gemm_nt_w4(a, w: W4Matrix, out=None, workspace=None, stream=None):
     if index != words.get_device():
         raise ValueError("a and w must be on the same GPU")
     out = _output(out, a, stream, (m, n))
-    ws, ws_ptr, ws_bytes = _workspace(
-        _workspace_need((gemm_f16_nt_w4_plan, m, n, k, w.group, index)), a, workspace, stream)
-    _call(index, stream, load().gemm_f16_nt_w4, m, n, k, w.group, a.data_ptr(), words.data_ptr(),
+    key = (gemm_f16_nt_w4_plan, m, n, k, w.group, index)
+    need = _workspace_bytes.get(key)
+    if need is None:
+        need = _plan_workspace(key)
+    ws, ws_ptr, ws_bytes = None, 0, 0
+    if need or workspace is not None:
+        ws, ws_ptr, ws_bytes = _workspace(need, a, workspace, stream)
+    _call(index, stream, _lib.gemm_f16_nt_w4, m, n, k, w.group, a.data_ptr(), words.data_ptr(),
           w.scales.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes)
     if stream is not None:
         _record(stream, a, words, w.scales, out, ws)
@@ -430,7 +453,9 @@ def gemm_tn_q8(a, x: Q8Matrix, out=None, workspace=None, stream=None):
     gemm_nt_w4."""
     if not isinstance(x, Q8Matrix):
         raise TypeError("x must be a Q8Matrix")
-    k, m = _matrix(a, _f16, "a")
+    if not _is_matrix(a, _f16):
+        _refuse(a, _f16, "a")
+    k, m = a.shape
     n, codes = x.n, x.codes
     if k != x.r:
         raise ValueError(f"shape mismatch: a{tuple(a.shape)} x{x.shape}")
@@ -438,9 +463,14 @@ def gemm_tn_q8(a, x: Q8Matrix, out=None, workspace=None, stream=None):
     if index != codes.get_device():
         raise ValueError("a and x must be on the same GPU")
     out = _output(out, a, stream, (m, n))
-    ws, ws_ptr, ws_bytes = _workspace(
-        _workspace_need((gemm_f16_tn_q8_plan, m, n, k, index)), a, workspace, stream)
-    _call(index, stream, load().gemm_f16_tn_q8, m, n, k, a.data_ptr(), codes.data_ptr(),
+    key = (gemm_f16_tn_q8_plan, m, n, k, index)
+    need = _workspace_bytes.get(key)
+    if need is None:
+        need = _plan_workspace(key)
+    ws, ws_ptr, ws_bytes = None, 0, 0
+    if need or workspace is not None:
+        ws, ws_ptr, ws_bytes = _workspace(need, a, workspace, stream)
+    _call(index, stream, _lib.gemm_f16_tn_q8, m, n, k, a.data_ptr(), codes.data_ptr(),
           x.scales.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes)
     if stream is not None:
         _record(stream, a, codes, x.scales, out, ws)
