@@ -316,7 +316,7 @@ def quantize_w4(w, group: int = 128, stream=None) -> W4Matrix:
         _refuse(w, _f16, "w")
     n, k = w.shape
     q = _new_w4(w, stream, n, k, group)
-    _call(w.get_device(), stream, _lib.gemm_f16_w4_quantize, n, k, group, w.data_ptr(),
+    _call(w.get_device(), stream, _lib.gemm_f16_w4_quantize, n, k, q.group, w.data_ptr(),
           q.words.data_ptr(), q.scales.data_ptr())
     if stream is not None:
         _record(stream, w)
@@ -341,7 +341,7 @@ def pack_w4(codes, scales, group: int = 128, stream=None) -> W4Matrix:
                          f"groups of {group}")
     if codes.device != scales.device:
         raise ValueError("codes and scales must be on the same GPU")
-    _call(codes.get_device(), stream, _lib.gemm_f16_w4_pack, n, k, group, codes.data_ptr(),
+    _call(codes.get_device(), stream, _lib.gemm_f16_w4_pack, n, k, q.group, codes.data_ptr(),
           scales.data_ptr(), q.words.data_ptr(), q.scales.data_ptr())
     if stream is not None:
         _record(stream, codes, scales)

@@ -136,6 +136,14 @@ def test_w4_pack(g, n, k, group):
     assert (host(g.dequantize_w4(q)).astype(np.float64) == ref.values(full, r, group, k)).all()
 
 
+def test_group_from_numpy(g):
+    """A group size out of an array or a configuration is as good as an int."""
+    q = g.quantize_w4(dev(np.full((5, 70), 7, np.float16)), np.int64(64))
+    p = g.pack_w4(dev(np.full((5, 70), 7, np.int8)), dev(np.ones((5, 2), np.float16)), np.int32(64))
+    assert q.group == p.group == 64
+    assert (host(g.dequantize_w4(q)) == 7).all() and (host(g.dequantize_w4(p)) == 7).all()
+
+
 def test_w4_pack_refuses_groups(g):
     """What four bits or fp16 do not hold makes its group NaN, and no other."""
     codes = np.ones((16, 256), np.int8)
