@@ -130,7 +130,9 @@ __device__ __forceinline__ float half_of(u32x4_t v, int i)
 // One wave per tile of 16 rows by 128 columns, each lane the 32 weights whose
 // words it writes: four loads of 16 bytes (8 for int8 codes), the group's
 // largest magnitude over the four lanes of a row, one 16-byte store.  Memory
-// bounds it.
+// bounds it (4096 x 14336: 33.3 us, 4.4 TB/s).  Loads of 256 bytes of four rows,
+// turned round in LDS, took 22 us for 28 where rows are not 16-byte aligned, and
+// 1 to 2 us more where they are, as weights' rows mostly are.
 struct W4EncodeParams {
     const uint16_t *W;       // fp16 [N, K], or
     const int8_t *codes;     // int8 [N, K] and
@@ -319,7 +321,8 @@ struct W4DecodeParams {
     int32_t shift;
 };
 
-// W4 back to fp16, one wave per tile; memory bounds it.
+// W4 back to fp16, one wave per tile; memory bounds it (8192 x 8192: 25.5 us, 6.6
+// TB/s; 28.3 with neighbouring tiles on different XCDs).
 __global__ __launch_bounds__(64 * WAVES) void w4_decode_kernel(W4DecodeParams p)
 {
     const int lane = threadIdx.x & 63;
@@ -433,9 +436,10 @@ __device__ __forceinline__ void w4_run_tiles(int32_t full, int wave, Load load, 
 // accumulators multiplies the words of its own step with the whole register,
 // and of its results only the columns of that step are used.
 //
-// JC = 4, eight waves with two tiles a buffer: 1 x 4096 x 14336 takes 8.0 us
-// from HBM (2.3 us of it an empty kernel's), 1 x 16384 x 16384 25.2 us (5.3
-// TB/s); one tile a buffer 9.1 and 27.1, four 9.8 and 35.6.
+// JC = 4, eight waves with two tiles a buffer: 1 x 4096 x 14336 takes 7.0 us at
+// best from HBM (2.3 us of it an empty kernel's), 1 x 16384 x 16384 25.2 us (5.3
+// TB/s).  When that first one took 8.0 us, one tile a buffer took 9.1 (and 27.1),
+// four 9.8 (35.6).
 template <int SH, int JC, int NB, int W, int D>
 __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
 {
@@ -631,7 +635,9 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
 // of eight weights takes 12 operations of 4 cycles, while its MFMAs take 16 MT
 // cycles.  w4_tile_pair scales and centres in one fused operation to save three
 // of 15 (333 x 4096 x 14336: 51.7 to 48.1 us, 48 x 16384 x 16384: 47.1 to 43.0),
-// and a word is unpacked between the MFMAs of the word before it.
+// and a word is unpacked between the MFMAs of the word before it.  333 x 4096 x
+// 14336 now keeps the matrix units busy for 51% of the cycles, at a clock that
+// the power limit holds near 1.75 GHz; 512 x 16384 x 16384 runs at 1.2 PFLOP/s.
 //
 // Few tiles leave CUs idle: K is then split, each range's fp32 sums go to the
 // workspace in the order in which lanes hold them (every store and load a
@@ -971,7 +977,10 @@ __global__ __launch_bounds__(256) void copy_rows_kernel(CopyRowsParams p)
 // A thread handles eight neighbouring columns, four neighbouring threads the
 // 32 of a group, 2^tx_shift threads (at most a wave: 512 columns) a row, and
 // each thread ROWS rows, so that several loads are in flight.  Memory bounds
-// both kernels.
+// both kernels: 4999 x 7001 takes 18.5 us to codes and 16.6 back (5.8 and 6.4
+// TB/s, part of it from the last cache).  Rows of codes and scales end inside
+// cache lines, so neighbouring workgroups belong on one XCD: in launch order
+// they read up to 1.4 times as much and took 21.7 and 20.3 us.
 constexpr int Q8_ROWS = 4;
 
 struct Q8Params {

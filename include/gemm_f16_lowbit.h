@@ -96,8 +96,9 @@ enum {
     /* the operand is written out in fp16 into the workspace and the library's
      * fp16 GEMM (with its own split over K) runs on it */
     GEMM_F16_LOWBIT_DECODE = 0,
-    /* the codes go from memory to the matrix units through registers, one
-     * pass, no workspace */
+    /* the codes go from memory to the matrix units through registers; 4 bits:
+     * one pass, no workspace; 8 bits: where the rows of X are split, the
+     * ranges' fp32 sums through the workspace */
     GEMM_F16_LOWBIT_STREAM = 1,
     /* tiles of the codes and of A through LDS; where K is split, the ranges'
      * fp32 sums through the workspace */
