@@ -25,10 +25,10 @@ torch = None
 
 
 def _bind_torch() -> None:
-    global torch, _f16, _int8, _empty, _current_device, _raw_stream, _lib
+    global torch, _f16, _int8, _int32, _empty, _current_device, _raw_stream, _lib
     import torch as t
 
-    _f16, _int8, _empty = t.float16, t.int8, t.empty_strided
+    _f16, _int8, _int32, _empty = t.float16, t.int8, t.int32, t.empty_strided
     _lib = load()
     # without torch's check that CUDA is initialised (the operands are on a GPU),
     # and the raw handle without building a Stream object, where torch has these
@@ -282,6 +282,19 @@ def _new_rows(on, stream, rows, cols, dtype):
     return _new(on, stream, (rows, cols), dtype)
 
 
+def _new_w4(on, stream, n: int, k: int, group: int) -> W4Matrix:
+    if group not in W4_GROUPS:
+        raise ValueError(f"group must be one of {W4_GROUPS}, not {group!r}")
+    group = int(group)
+    words, scales = _w4_shapes(n, k, group)
+    q = W4Matrix.__new__(W4Matrix)
+    if stream is not None:
+        return q._set(_new(on, stream, words, torch.int32), _new(on, stream, scales, _f16), n, k, group)
+    device, kt, groups = on.device, words[1], scales[1]
+    return q._set(_empty(words, (256 * kt, 256, 4, 1), dtype=_int32, device=device),
+                  _empty(scales, (16 * groups, 16, 1), dtype=_f16, device=device), n, k, group)
+
+
 def _record(stream, *tensors) -> None:
     """Tensors of other streams, used on `stream`: not to be reused before it is done."""
     for t in tensors:
@@ -298,14 +311,6 @@ def _output(out, on, stream, shape):
             out.device != on.device:
         raise ValueError(f"out must be a contiguous float16 {list(shape)} tensor on {on.device}")
     return out
-
-
-def _new_w4(on, stream, n: int, k: int, group: int) -> W4Matrix:
-    if group not in W4_GROUPS:
-        raise ValueError(f"group must be one of {W4_GROUPS}, not {group!r}")
-    words, scales = _w4_shapes(n, k, group)
-    return W4Matrix.__new__(W4Matrix)._set(_new(on, stream, words, torch.int32),
-                                           _new(on, stream, scales, _f16), n, k, int(group))
 
 
 def quantize_w4(w, group: int = 128, stream=None) -> W4Matrix:
