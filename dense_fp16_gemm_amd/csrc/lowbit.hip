@@ -624,12 +624,13 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
 // ---------------------------------------------------------------------------
 // C = A W^T for more rows of A: tiles through LDS
 // ---------------------------------------------------------------------------
-// A workgroup computes 16 MT rows of A by W NB blocks of 16 rows of W over a
-// range of K.  Each step is one tile of 128 columns: direct-to-LDS loads keep
-// S - 1 steps in flight (A's rows, which all waves share; each wave's own
-// words and scales), one barrier a step says that a step's data is there and
-// that the stage before it is free.  Every wave unpacks its own words, so no
-// weight is unpacked twice in a workgroup.
+// A workgroup computes 16 MT rows of A by WC NB blocks of 16 rows of W over a
+// range of K.  Each step is one tile of 128 columns, or with KH = 2 sets of WC
+// waves two, whose sums meet in LDS at the end: direct-to-LDS loads keep S - 1
+// steps in flight (A's rows, which a set's waves share; each wave's own words
+// and scales), one barrier a step says that a step's data is there and that the
+// stage before it is free.  Every wave unpacks its own words, so no weight is
+// unpacked twice in a workgroup.
 //
 // What bounds it is the vector ALU beside the matrix units: unpacking a word
 // of eight weights takes 12 operations of 4 cycles, while its MFMAs take 16 MT
@@ -641,13 +642,16 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
 //
 // Few tiles leave CUs idle: K is then split, each range's fp32 sums go to the
 // workspace in the order in which lanes hold them (every store and load a
-// whole KB), and w4_join_kernel adds them up in order.
+// whole KB), and w4_join_kernel adds them up in order.  Two sets of waves make a
+// tile half as wide for the same work a step, so twice as many tiles and half
+// the ranges (512 x 4096 x 4096: 26.0 to 22.1 us, unsplit in both; 64 x 8192 x
+// 8192: 20.4 to 18.9, four ranges of half the tile's sums).
 struct W4TileParams {
     const uint16_t *A;
     const u32x4_t *words;
     const uint16_t *scales;
     uint16_t *C;
-    float *partial;            // [splits][tiles][waves][NB][MT][64] of 4 values
+    float *partial;            // [splits][tiles][WC][NB][MT][64] of 4 values
     int32_t M, N, K, lda;      // lda a multiple of 8, A 16-byte aligned
     int32_t kt, nb;            // tiles of 128 columns, blocks of 16 rows of W
     int32_t tiles_m, tiles_n, splits;
@@ -715,20 +719,23 @@ __device__ __forceinline__ void store4(uint16_t *C, int32_t M, int32_t N, int32_
         if (n + e < N) reinterpret_cast<_Float16 *>(c)[e] = h[e];
 }
 
-template <int SH, int MT, int NB, int W, int S>
+template <int SH, int MT, int NB, int W, int S, int KH>
 __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
 {
+    static_assert((KH == 1 || KH == 2) && W % KH == 0, "sets of waves");
+    constexpr int WC = W / KH;                     // waves of a set, side by side
     constexpr int NS = 128 >> SH;                  // scales a tile and row of W
-    constexpr int AF = (4 * MT + W - 1) / W;       // loads of A a wave and step: 4 rows each
+    constexpr int AF = (4 * MT + WC - 1) / WC;     // loads of A a wave and step: 4 rows each
     constexpr int SC = (NB * NS * 8 + 63) / 64;    // loads of scales
     constexpr int LOADS = AF + NB + SC;
-    constexpr int A_BYTES = AF * W * 1024, W_BYTES = W * NB * 1024, S_BYTES = W * SC * 256;
+    constexpr int SET_BYTES = AF * WC * 1024;      // of A, for a set's tile
+    constexpr int A_BYTES = KH * SET_BYTES, W_BYTES = W * NB * 1024, S_BYTES = W * SC * 256;
     constexpr int STAGE = A_BYTES + W_BYTES + S_BYTES;
     static_assert(S >= 2 && (S - 2) * LOADS <= 63, "vmcnt counts at most 63 loads");
     static_assert(S * STAGE <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
     const int lane = threadIdx.x & 63;
-    const int wave = wave_index();
+    const int wave = wave_index(), set = wave / WC, wc = wave % WC;
     const int r = lane & 15, kq = lane >> 4;
     // units run over the rows of A first, so that a word's users are neighbours
     int32_t u = xcd_unit();
@@ -736,9 +743,9 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
     const int32_t un = u / p.tiles_m;
     const int32_t tn = un % p.tiles_n;
     const int32_t t0 = un / p.tiles_n * p.kt_split;
-    const int32_t T = min(p.kt_split, p.kt - t0);
+    const int32_t T = min(p.kt_split, p.kt - t0), steps = (T + KH - 1) / KH;
     const int32_t m0 = tm * 16 * MT;
-    const int32_t b0 = (tn * W + wave) * NB;
+    const int32_t b0 = (tn * WC + wc) * NB;
     const uint32_t klen = static_cast<uint32_t>(p.K - t0 * 128);
     const int32_t rows = min(16 * MT, p.M - m0);
     // rows past M and blocks past N start past their resources: zeros
@@ -759,7 +766,7 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
     uint32_t va[AF], ka[AF], vs[SC];
 #pragma unroll
     for (int i = 0; i < AF; ++i) {
-        const int row = (i * W + wave) * 4 + kq;
+        const int row = (i * WC + wc) * 4 + kq;
         ka[i] = 8 * (r ^ (row & 15));
         va[i] = row < 16 * MT
                     ? (static_cast<uint32_t>(row) * static_cast<uint32_t>(p.lda) + ka[i]) * 2u
@@ -778,21 +785,22 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
     // step waits for the same count
     auto fetch = [&](int stage, int32_t i) {
         const uint32_t base = lds0 + stage * STAGE;
-        const bool in = i < T;
-        const uint32_t ui = static_cast<uint32_t>(i);
+        const int32_t t = i * KH + set;
+        const bool in = t < T;
+        const uint32_t ut = static_cast<uint32_t>(t);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-            dma16(rw[nb], in ? lane * 16u + ui * 1024u : OOB_OFFSET,
+            dma16(rw[nb], in ? lane * 16u + ut * 1024u : OOB_OFFSET,
                   base + A_BYTES + (wave * NB + nb) * 1024);
 #pragma unroll
         for (int s = 0; s < SC; ++s)
-            dma4(rs, in && vs[s] != OOB_OFFSET ? vs[s] + ui * (NS * 32u) : OOB_OFFSET,
+            dma4(rs, in && vs[s] != OOB_OFFSET ? vs[s] + ut * (NS * 32u) : OOB_OFFSET,
                  base + A_BYTES + W_BYTES + (wave * SC + s) * 256);
 #pragma unroll
         for (int f = 0; f < AF; ++f)
-            dma16(ra, in && va[f] != OOB_OFFSET && ka[f] + ui * 128u < klen ? va[f] + ui * 256u
+            dma16(ra, in && va[f] != OOB_OFFSET && ka[f] + ut * 128u < klen ? va[f] + ut * 256u
                                                                          : OOB_OFFSET,
-                  base + (f * W + wave) * 1024);
+                  base + set * SET_BYTES + (f * WC + wc) * 1024);
     };
     f32x4_t acc[MT][NB] = {};
 #pragma unroll
@@ -819,7 +827,7 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
         }
     };
     auto compute = [&](auto pair) {
-        const uint8_t *st = smem + stage * STAGE;
+        const uint8_t *st = smem + stage * STAGE + set * SET_BYTES;
         half8_t a[2][MT];
         auto read_a = [&](int j) {
 #pragma unroll
@@ -865,7 +873,7 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
     const W4Bits bits = w4_high_bits();
     int32_t i = 0;
     bool large = false;
-    for (; i < T; ++i) {
+    for (; i < steps; ++i) {
         begin(i);
         float most = 0.0f;
 #pragma unroll
@@ -881,15 +889,34 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
         const W4Bits low = w4_low_bits();
         for (;;) {
             compute([&](uint32_t w, int i, _Float16 s) { return w4_pair(w, i, s, low); });
-            if (++i == T) break;
+            if (++i == steps) break;
             begin(i);
         }
     }
     // no load may still be on its way to this LDS when the workgroup ends
     asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    if constexpr (KH == 2) {
+        static_assert(WC * NB * MT * 1024 <= S * STAGE, "LDS");
+        f32x4_t *other = reinterpret_cast<f32x4_t *>(smem) + wc * (NB * MT * 64) + lane;
+        __syncthreads();
+        if (set == 1) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) other[(nb * MT + mt) * 64] = acc[mt][nb];
+        }
+        __syncthreads();
+        if (set == 0) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) acc[mt][nb] += other[(nb * MT + mt) * 64];
+        }
+    }
     // lane l holds columns 4 (l / 16) .. + 3 of the block, row l % 16 of A
     if (p.splits > 1) {
-        float *to = p.partial + (static_cast<int64_t>(u) * W + wave) * (NB * MT * 256) + lane * 4;
+        if (set > 0) return;
+        float *to = p.partial + (static_cast<int64_t>(u) * WC + wc) * (NB * MT * 256) + lane * 4;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -899,16 +926,19 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
     }
     // C through LDS, so that a row's columns leave in one run (stored as lanes
     // hold them, 32 bytes of a row at a time, 3936 x 15296 x 64 took 56.3 us; 42.8)
-    constexpr int COLS = 16 * NB * W, PITCH = COLS + 8;
+    constexpr int COLS = 16 * NB * WC, PITCH = COLS + 8;
     static_assert(16 * MT * PITCH * 2 <= S * STAGE, "LDS");
     _Float16 *rows_c = reinterpret_cast<_Float16 *>(smem);
     __syncthreads();
+    if (set == 0) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            *reinterpret_cast<half4_t *>(&rows_c[(mt * 16 + r) * PITCH + (wave * NB + nb) * 16 + kq * 4]) =
-                __builtin_convertvector(acc[mt][nb], half4_t);
+            for (int mt = 0; mt < MT; ++mt)
+                *reinterpret_cast<half4_t *>(
+                    &rows_c[(mt * 16 + r) * PITCH + (wc * NB + nb) * 16 + kq * 4]) =
+                    __builtin_convertvector(acc[mt][nb], half4_t);
+    }
     __syncthreads();
     for (int o = threadIdx.x; o < 2 * MT * COLS; o += 64 * W) {
         const int row = o / (COLS / 8), c = o % (COLS / 8) * 8;
@@ -1613,25 +1643,26 @@ static int decode_gemm(const Decode &d, int64_t M, int64_t N, int64_t K, bool tn
 // for each group size.
 struct W4Kernel {
     int32_t kernel, rows, blocks, waves;   // rows of A, blocks of 16 rows of W a workgroup
-    // Where a model of times chooses: us before the first step and a step of 128
-    // columns (for each wave of a stream kernel) with one workgroup on a CU, and
-    // with two (0: they do not fit).
+    int32_t tiles_step;                    // tiles of 128 columns that its waves take at once
+    // Where a model of times chooses: us before the first step, and a step with
+    // one workgroup on a CU and with two (0: they do not fit).
     double start, step1, step2;
     const void *fn[3];                     // group 32, 64, 128
 };
-#define W4_KERNEL(KIND, ROWS, BLOCKS, W, T0, T1, T2, K5, K6, K7)                      \
-    W4Kernel{KIND, ROWS, BLOCKS, W, T0, T1, T2,                                       \
+#define W4_KERNEL(KIND, ROWS, BLOCKS, W, STEP, T0, T1, T2, K5, K6, K7)                \
+    W4Kernel{KIND, ROWS, BLOCKS, W, STEP, T0, T1, T2,                                 \
              {reinterpret_cast<const void *>(&K5), reinterpret_cast<const void *>(&K6), \
               reinterpret_cast<const void *>(&K7)}}
 #define W4_STREAM(JC, NB, W, D)                                                       \
-    W4_KERNEL(GEMM_F16_LOWBIT_STREAM, 16 / JC, NB, W, 0, 0, 0, (w4_stream_kernel<5, JC, NB, W, D>), \
+    W4_KERNEL(GEMM_F16_LOWBIT_STREAM, 16 / JC, NB, W, W, 0, 0, 0, (w4_stream_kernel<5, JC, NB, W, D>), \
               (w4_stream_kernel<6, JC, NB, W, D>), (w4_stream_kernel<7, JC, NB, W, D>))
 #define W4_ROWS(RL, NB, W, T0, T1, T2)                                                \
-    W4_KERNEL(GEMM_F16_LOWBIT_STREAM, 4 * RL, NB, W, T0, T1, T2, (w4_rows_kernel<5, RL, NB, W>),  \
+    W4_KERNEL(GEMM_F16_LOWBIT_STREAM, 4 * RL, NB, W, W, T0, T1, T2, (w4_rows_kernel<5, RL, NB, W>), \
               (w4_rows_kernel<6, RL, NB, W>), (w4_rows_kernel<7, RL, NB, W>))
-#define W4_TILE(MT, NB, W, S, T1, T2)                                                 \
-    W4_KERNEL(GEMM_F16_LOWBIT_TILE, 16 * MT, NB * W, W, 3.7, T1, T2, (w4_tile_kernel<5, MT, NB, W, S>), \
-              (w4_tile_kernel<6, MT, NB, W, S>), (w4_tile_kernel<7, MT, NB, W, S>))
+#define W4_TILE(MT, NB, W, S, KH, T1, T2)                                             \
+    W4_KERNEL(GEMM_F16_LOWBIT_TILE, 16 * MT, NB * W / KH, W, KH, 3.35, T1, T2,        \
+              (w4_tile_kernel<5, MT, NB, W, S, KH>), (w4_tile_kernel<6, MT, NB, W, S, KH>), \
+              (w4_tile_kernel<7, MT, NB, W, S, KH>))
 static const W4Kernel kW4Kernels[] = {
     W4_STREAM(4, 1, 8, 2),
     W4_ROWS(2, 1, 8, 0, 0, 0), W4_ROWS(2, 2, 8, 0, 0, 0),
@@ -1639,10 +1670,10 @@ static const W4Kernel kW4Kernels[] = {
     W4_ROWS(8, 1, 8, 2.63, 1.043, 0),      W4_ROWS(8, 2, 4, 3.33, 0.625, 1.290),
     W4_ROWS(8, 4, 8, 3.44, 2.101, 0),      W4_ROWS(12, 1, 8, 2.83, 1.452, 0),
     W4_ROWS(12, 2, 4, 3.96, 0.806, 1.629), W4_ROWS(12, 4, 4, 4.45, 1.382, 0),
-    W4_TILE(2, 2, 4, 4, 0.518, 0.813), W4_TILE(3, 2, 8, 2, 0.911, 1.474),
-    W4_TILE(4, 2, 4, 3, 0.689, 1.061), W4_TILE(4, 2, 8, 3, 0.989, 0),
-    W4_TILE(6, 2, 8, 3, 1.209, 0),     W4_TILE(7, 2, 8, 3, 1.366, 0),
-    W4_TILE(8, 2, 8, 3, 1.505, 0),
+    W4_TILE(2, 2, 4, 4, 1, 0.500, 0.790), W4_TILE(3, 2, 8, 2, 1, 0.869, 1.417),
+    W4_TILE(4, 2, 8, 2, 2, 1.170, 0),     W4_TILE(4, 2, 8, 3, 1, 0.962, 0),
+    W4_TILE(6, 2, 8, 2, 2, 1.446, 0),     W4_TILE(6, 2, 8, 3, 1, 1.173, 0),
+    W4_TILE(7, 2, 8, 3, 1, 1.312, 0),     W4_TILE(8, 2, 8, 3, 1, 1.452, 0),
 };
 constexpr int kNumW4Kernels = sizeof(kW4Kernels) / sizeof(kW4Kernels[0]);
 
@@ -1657,18 +1688,18 @@ struct W4Choice {
 // grid does not grow with them.
 constexpr int64_t W4_MOST_WORKGROUPS = 1 << 22;
 
-// Kernel `e`'s time in us by the model, its K in `ranges` ranges of `steps` steps.
-static double w4_model(const W4Kernel &e, int64_t workgroups, int64_t steps, int64_t ranges,
-                       int32_t cus)
+// Kernel `e`'s time in us by the model, its K in `ranges` ranges of `kt` tiles.
+static double w4_model(const W4Kernel &e, int64_t workgroups, int64_t kt, int64_t ranges, int32_t cus)
 {
+    const int64_t steps = cdiv(kt, e.tiles_step);
     const bool two = e.step2 > 0;
     const int64_t slots = static_cast<int64_t>(cus) * (two ? 2 : 1);
     const int64_t full = workgroups / slots, rest = workgroups % slots;
     double us = e.start + full * (two ? e.step2 : e.step1) * steps;
     if (rest > 0) us += (rest <= cus || !two ? e.step1 : e.step2) * steps;
     if (ranges > 1)
-        us += 1.5 + 0.114 * ranges +
-              3.41e-7 * static_cast<double>(workgroups) * (e.rows / 16) * e.blocks * 1024;
+        us += 2.27 + 0.111 * ranges +
+              3.55e-7 * static_cast<double>(workgroups) * (e.rows / 16) * e.blocks * 1024;
     return us;
 }
 
@@ -1684,7 +1715,7 @@ static int32_t w4_choose_stream(int64_t M, const W4Shape &s, int32_t cus, double
     for (int32_t id = 0; id < kNumW4Kernels; ++id) {
         const W4Kernel &e = kW4Kernels[id];
         if (e.kernel != GEMM_F16_LOWBIT_STREAM || e.start == 0 || e.rows < M) continue;
-        const double us = w4_model(e, cdiv(s.nb, e.blocks), cdiv(s.kt, e.waves), 1, cus);
+        const double us = w4_model(e, cdiv(s.nb, e.blocks), s.kt, 1, cus);
         if (best < 0 || us < *best_us) {
             *best_us = us;
             best = id;
@@ -1699,7 +1730,7 @@ constexpr int64_t W4_STREAM_ROWS = 48;
 // 160 shapes (20 to 2048 rows, N and K of 512 to 32768, words from HBM): rounds
 // of workgroups over the CUs times the steps of a range, the clock that long
 // products lose to the power limit, and for a split the partial sums' way
-// through memory and the join.  Its error is 6%; what it chose took 1.1% longer
+// through memory and the join.  Its error is 6%; what it chose took 1 to 2% longer
 // than the best of each shape in the mean, 16% in the worst.  (Of 17 to 48 rows,
 // the tile kernels alone took 25% longer: 32 x 4096 x 4096 9.8 us, streamed 7.5.)
 static W4Choice w4_search(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
@@ -1707,7 +1738,7 @@ static W4Choice w4_search(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
     const double nk = static_cast<double>(s.nb) * 16 * K;
     // words to fp16 and back from memory, and the GEMM at its rate for large M
     W4Choice best = {-1, 1};
-    double best_us = 12.2 + (7.0e-7 + 1.13e-9 * std::max<double>(M, 423)) * std::max(nk, 8.4e6);
+    double best_us = 12.2 + (7.0e-7 + 1.10e-9 * std::max<double>(M, 423)) * std::max(nk, 8.4e6);
     if (M <= W4_STREAM_ROWS) {
         double us = 0;
         const int32_t id = w4_choose_stream(M, s, cus, &us);
@@ -1731,7 +1762,7 @@ static W4Choice w4_search(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
             last = per;
             const int64_t ranges = cdiv(s.kt, per);
             const double us = w4_model(e, tiles * ranges, per, ranges, cus) +
-                              2.26e-10 * std::max(0.0, nk * static_cast<double>(M) - 1.22e10);
+                              2.81e-10 * std::max(0.0, nk * static_cast<double>(M) - 1.05e10);
             if (us < best_us) {
                 best_us = us;
                 best = {id, static_cast<int32_t>(ranges)};

@@ -294,17 +294,19 @@ W4_KERNELS = [((1, 4, 16, 8), 3, 500, 1000), ((1, 8, 16, 8), 5, 500, 3000),
               ((1, 8, 32, 8), 7, 6500, 700), ((1, 16, 16, 8), 12, 500, 3000),
               ((1, 16, 32, 8), 16, 6500, 700), ((1, 16, 64, 8), 9, 12800, 520),
               ((1, 32, 16, 8), 17, 70, 32), ((1, 32, 16, 8), 30, 1000, 3000),
-              ((1, 32, 32, 4), 24, 6500, 32), ((1, 32, 32, 4), 32, 6500, 2001),
+              ((1, 32, 32, 4), 24, 6500, 700), ((1, 32, 32, 4), 32, 6500, 2001),
               ((1, 32, 64, 8), 17, 12800, 700), ((1, 32, 64, 8), 29, 12801, 4001),
               ((1, 48, 16, 8), 40, 70, 700), ((1, 48, 16, 8), 48, 1000, 2100),
               ((1, 48, 32, 4), 33, 6500, 700), ((1, 48, 32, 4), 45, 6500, 2048),
               ((1, 48, 64, 4), 40, 12800, 2048), ((1, 48, 64, 4), 47, 12801, 3000),
               ((2, 32, 128, 4), 40, 70, 32), ((2, 32, 128, 4), 60, 1000, 700),
               ((2, 48, 256, 8), 333, 6500, 32), ((2, 48, 256, 8), 40, 6500, 8000),
-              ((2, 64, 128, 4), 80, 12800, 32), ((2, 64, 128, 4), 60, 6500, 2048),
-              ((2, 64, 256, 8), 200, 16384, 32), ((2, 64, 256, 8), 112, 6500, 4096),
-              ((2, 96, 256, 8), 333, 12800, 32), ((2, 96, 256, 8), 80, 6500, 8000),
-              ((2, 112, 256, 8), 512, 12800, 32), ((2, 112, 256, 8), 200, 6500, 4096),
+              ((2, 64, 128, 8), 80, 12800, 700), ((2, 64, 128, 8), 60, 6500, 2048),
+              ((2, 64, 128, 8), 333, 1000, 2000), ((2, 64, 128, 8), 500, 4001, 4100),
+              ((2, 64, 256, 8), 200, 16384, 32), ((2, 64, 256, 8), 60, 12800, 8000),
+              ((2, 96, 128, 8), 160, 12800, 700), ((2, 96, 128, 8), 80, 6500, 4096),
+              ((2, 96, 256, 8), 333, 12800, 32), ((2, 96, 256, 8), 80, 12800, 8000),
+              ((2, 112, 256, 8), 512, 12800, 32), ((2, 112, 256, 8), 112, 6500, 8000),
               ((2, 128, 256, 8), 512, 16384, 32), ((2, 128, 256, 8), 120, 12800, 8000),
               ((0,), 1500, 14336, 4096), ((0,), 2200, 7001, 4001)]
 
