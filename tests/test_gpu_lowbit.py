@@ -806,3 +806,57 @@ def test_threads_on_their_own_streams(g):
     for t in threads:
         t.join()
     assert not wrong
+
+
+# ---- nothing around C and the workspace is written, by any kernel ----------------
+def guarded(shape):
+    """(tensor of `shape` at a 2-byte offset in a buffer of sentinels, check())."""
+    import torch
+
+    count = shape[0] * shape[1]
+    buf = torch.full((count + 4096,), 7.0, dtype=torch.float16, device="cuda")
+    out = buf[2049:2049 + count].view(shape)
+
+    def check():
+        assert (buf[:2049] == 7).all() and (buf[2049 + count:] == 7).all()
+
+    return out, check
+
+
+def guarded_workspace(need):
+    import torch
+
+    buf = torch.full((need + 8192,), 0x5A, dtype=torch.uint8, device="cuda")
+
+    def check():
+        assert (buf[:4096] == 0x5A).all() and (buf[4096 + need:] == 0x5A).all()
+
+    return buf[4096:4096 + need], check
+
+
+@pytest.mark.parametrize("kernel,m,n,k", W4_KERNELS)
+def test_nt_w4_every_kernel_in_bounds(g, kernel, m, n, k):
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(m * n + k)
+    q = g.quantize_w4(torch.randn(n, k, generator=gen, device="cuda").half(), 64)
+    a = torch.randn(m, k, generator=gen, device="cuda").half()
+    out, out_kept = guarded((m, n))
+    ws, ws_kept = guarded_workspace(g.gemm_f16_nt_w4_plan(m, n, k, 64, 256).workspace_bytes)
+    g.gemm_nt_w4(a, q, out=out, workspace=ws)
+    out_kept(), ws_kept()
+    assert torch.equal(out, g.gemm_nt_w4(a, q))
+
+
+@pytest.mark.parametrize("kernel,splits,m,n,k", Q8_KERNELS)
+def test_tn_q8_every_kernel_in_bounds(g, kernel, splits, m, n, k):
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(m * n + k)
+    x = g.quantize_q8(torch.randn(k, n, generator=gen, device="cuda").half())
+    a = torch.randn(k, m, generator=gen, device="cuda").half()
+    out, out_kept = guarded((m, n))
+    ws, ws_kept = guarded_workspace(g.gemm_f16_tn_q8_plan(m, n, k, 256).workspace_bytes)
+    g.gemm_tn_q8(a, x, out=out, workspace=ws)
+    out_kept(), ws_kept()
+    assert torch.equal(out, g.gemm_tn_q8(a, x))
