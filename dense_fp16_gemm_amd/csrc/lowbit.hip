@@ -143,10 +143,12 @@ struct W4EncodeParams {
     int32_t shift;           // log2 of the group
 };
 
-// Most significant 8 bits of a scale, to nearest with ties to even.
+// Most significant 8 bits of a scale, to nearest with ties to even.  Infinities
+// and NaN stay as they are: the carry out of a NaN's payload would make it zero.
 __device__ __forceinline__ float round_scale(float s)
 {
     const uint32_t u = bits_as<uint32_t>(s);
+    if ((u & 0x7f800000u) == 0x7f800000u) return s;
     return bits_as<float>((u + 0x7fffu + ((u >> 16) & 1)) & 0xffff0000u);
 }
 

@@ -332,7 +332,7 @@ def pack_w4(codes, scales, group: int = 128, stream=None) -> W4Matrix:
     """A W4Matrix from another quantiser's codes [N, K] int8 in -8..7 and scales
     [N, ceil(K / group)] fp16, weight = code * scale.  Scales are rounded to 8
     significant bits; a group that cannot be held (a code out of range, a scale
-    that is not finite, a weight past 65504) becomes NaN."""
+    that is not finite or is rounded to 65536, a weight past 65504) becomes NaN."""
     if torch is None:
         _bind_torch()
     if not _is_matrix(codes, _int8):

@@ -71,8 +71,8 @@ extern "C" {
  * gemm_f16_w4_pack: the same storage from codes int8 [N, K] row-major and
  * in_scales fp16 [N, ceil(K / group)] row-major that another quantiser made.
  * Scales are rounded to 8 significant bits (to nearest, ties to even).  A
- * group with a code outside -8 .. 7, a scale that is not finite, or a product
- * past 65504 gets s = NaN and codes 0.
+ * group with a code outside -8 .. 7, a scale that is not finite (as given or,
+ * from 65408, as rounded), or a product past 65504 gets s = NaN and codes 0.
  *
  * gemm_f16_w4_dequantize: words and scales to W fp16 [N, K] row-major.
  *
