@@ -390,6 +390,18 @@ __device__ __forceinline__ void w4_join_waves(const W4Params &p, int32_t b0, int
     }
 }
 
+// Zeros for the scales of groups past K, in the tile `t` that K ends in: they belong
+// to no weight and may hold anything, and a NaN times a zero of A would be one.
+template <int SH, int NB, int NS>
+__device__ __forceinline__ void w4_clear_pads(_Float16 (&sc)[NB][NS], int32_t t, int32_t K)
+{
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int s = 1; s < NS; ++s)
+            if (t * 128 + (s << SH) >= K) sc[nb][s] = _Float16(0.0f);
+}
+
 // Runs a wave's whole tiles in two buffers of D: one's loads fly while the
 // other's are multiplied.  Loads are unconditional (past the end the last tile
 // again), so that the waits on one buffer leave the other's in flight.
@@ -498,6 +510,7 @@ __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
     // the tile that K ends in: columns past K are zeros
     if (full < p.kt && full % W == wave) {
         load_w(0, 0, full);
+        w4_clear_pads<SH>(sc[0][0], full, p.K);
 #pragma unroll
         for (int i = 0; i < AL; ++i) {
             const int64_t c = static_cast<int64_t>(full) * 128 + 32 * (jj + JC * i) + 8 * kq;
@@ -605,6 +618,7 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
     w4_run_tiles<W, 1>(full, wave, load, mma);
     if (full < p.kt && full % W == wave) {
         load_w(0, full);
+        w4_clear_pads<SH>(sc[0], full, p.K);
 #pragma unroll
         for (int i = 0; i < RL; ++i) {
             const int64_t c = static_cast<int64_t>(full) * 128 + 8 * r;
@@ -766,6 +780,7 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
     // A in LDS: rows of 256 bytes, the 16-byte chunks of row i XORed with i to
     // spread the fragments' reads over the banks; applied where they are fetched
     uint32_t va[AF], ka[AF], vs[SC];
+    int32_t ts[SC];
 #pragma unroll
     for (int i = 0; i < AF; ++i) {
         const int row = (i * WC + wc) * 4 + kq;
@@ -777,7 +792,11 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
 #pragma unroll
     for (int i = 0; i < SC; ++i) {
         const int d = i * 64 + lane, blk = d / (NS * 8), rem = d % (NS * 8);
-        vs[i] = blk < NB ? static_cast<uint32_t>(blk) * p.kt * (NS * 32u) + rem * 4u : OOB_OFFSET;
+        vs[i] = static_cast<uint32_t>(blk) * p.kt * (NS * 32u) + rem * 4u;
+        // tiles of the range in which the group (first column (rem / 8) << SH) starts
+        // before K: scales of groups past K may hold anything
+        const uint32_t before = (klen + 127u - static_cast<uint32_t>((rem / 8) << SH)) / 128u;
+        ts[i] = blk < NB ? min(T, static_cast<int32_t>(before)) : 0;
     }
     int aoff[4];
 #pragma unroll
@@ -796,7 +815,7 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
                   base + A_BYTES + (wave * NB + nb) * 1024);
 #pragma unroll
         for (int s = 0; s < SC; ++s)
-            dma4(rs, in && vs[s] != OOB_OFFSET ? vs[s] + ut * (NS * 32u) : OOB_OFFSET,
+            dma4(rs, t < ts[s] ? vs[s] + ut * (NS * 32u) : OOB_OFFSET,
                  base + A_BYTES + W_BYTES + (wave * SC + s) * 256);
 #pragma unroll
         for (int f = 0; f < AF; ++f)

@@ -59,6 +59,7 @@ extern "C" {
  *           group g ..; 8-byte aligned; finite or NaN, at most 8 significant
  *           bits, and |s * q| at most 65504 (what the two functions below
  *           write; other scales give products rounded in more than one way).
+ *           Scales of groups past K and of rows past N do not matter.
  *
  * gemm_f16_w4_sizes: pure host function, the bytes of both arrays.
  * GEMM_F16_INVALID_ARG for NULL outputs, negative sizes or a group other than

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 import lowbit_ref as ref
-from test_gpu_lowbit import dev, g, host  # noqa: F401  (g: the fixture)
+from test_gpu_lowbit import W4_KERNELS, dev, g, host  # noqa: F401  (g: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +30,32 @@ def test_w4_pack_every_scale(g):  # noqa: F811
     np.testing.assert_array_equal(stored, ref.w4_scales(r, 1 << 16, 64, 32, 0.0))
     np.testing.assert_array_equal(host(g.dequantize_w4(q)).astype(np.float64),
                                   ref.values(want, r, 32, 64))
+
+
+# ---- storage that another program laid out ---------------------------------------
+def padded(k, group):
+    """Whether the last tile of K has groups that lie past K."""
+    return -(-k // group) * group < -(-k // 128) * 128
+
+
+@pytest.mark.parametrize("kernel,m,n,k,group",
+                         [(*case, group) for case in W4_KERNELS for group in (32, 64)
+                          if padded(case[3], group)])
+def test_nt_w4_scales_past_the_matrix(g, kernel, m, n, k, group):  # noqa: F811
+    """Scales of groups past K and of rows past N belong to no weight: NaN and
+    infinities in them (memory that a program did not fill) reach no result."""
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(m + n + k)
+    q = g.quantize_w4(torch.randn(n, k, generator=gen, device="cuda").half(), group)
+    a = torch.randn(m, k, generator=gen, device="cuda").half()
+    want = g.gemm_nt_w4(a, q)
+    assert want.isfinite().all()
+    groups = -(-k // group)
+    assert q.scales[:, groups:].numel() > 0
+    for value in (float("nan"), float("inf"), -65504.0):
+        q.scales[:, groups:] = value
+        if n % 16:
+            q.scales[-1, :, n % 16:] = value
+        assert torch.equal(g.gemm_nt_w4(a, q), want)
+        assert g.dequantize_w4(q).isfinite().all()
