@@ -141,7 +141,9 @@ def gemm_f16_tn_q8(M: int, N: int, K: int, A: int, codes: int, scales: int, C: i
 class W4Matrix:
     """An [n, k] matrix in W4 storage: words int32 [ceil(n / 16), ceil(k / 128),
     64, 4] and scales fp16 [ceil(n / 16), 128 ceil(k / 128) / group, 16], as
-    quantize_w4() and pack_w4() make them.  The tensors are kept, not copied."""
+    quantize_w4() and pack_w4() make them.  The tensors are kept, not copied.
+    One that was saved is checked as a new one is, so it is read back onto a GPU
+    (torch.load's map_location)."""
 
     __slots__ = ("words", "scales", "n", "k", "group")
 
@@ -168,6 +170,9 @@ class W4Matrix:
         self.words, self.scales, self.n, self.k, self.group = words, scales, n, k, group
         return self
 
+    def __reduce__(self):
+        return type(self), (self.words, self.scales, self.n, self.k, self.group)
+
     @property
     def shape(self) -> tuple[int, int]:
         return self.n, self.k
@@ -192,7 +197,8 @@ def _w4_shapes(n: int, k: int, group: int) -> tuple[tuple, tuple]:
 class Q8Matrix:
     """An [r, n] matrix in Q8 storage: codes int8 [r, 32 ceil(n / 32)] and
     scales fp16 [r, ceil(n / 32)], as quantize_q8() makes them.  The tensors
-    are kept, not copied; a range of rows of both is a Q8Matrix too."""
+    are kept, not copied; a range of rows of both is a Q8Matrix too.  Saved and
+    read back as a W4Matrix is."""
 
     __slots__ = ("codes", "scales", "r", "n")
 
@@ -217,6 +223,9 @@ class Q8Matrix:
     def _set(self, codes, scales, r, n):
         self.codes, self.scales, self.r, self.n = codes, scales, r, n
         return self
+
+    def __reduce__(self):
+        return type(self), (self.codes, self.scales, self.n)
 
     @property
     def shape(self) -> tuple[int, int]:
@@ -358,6 +367,8 @@ def dequantize_w4(w: W4Matrix, out=None, stream=None):
     if not isinstance(w, W4Matrix):
         raise TypeError("w must be a W4Matrix")
     words = w.words
+    if not words.is_cuda:
+        raise ValueError("w must be on a GPU")
     out = _output(out, words, stream, (w.n, w.k))
     _call(words.get_device(), stream, _lib.gemm_f16_w4_dequantize, w.n, w.k, w.group,
           words.data_ptr(), w.scales.data_ptr(), out.data_ptr())
@@ -388,6 +399,8 @@ def dequantize_q8(x: Q8Matrix, out=None, stream=None):
     if not isinstance(x, Q8Matrix):
         raise TypeError("x must be a Q8Matrix")
     codes = x.codes
+    if not codes.is_cuda:
+        raise ValueError("x must be on a GPU")
     out = _output(out, codes, stream, (x.r, x.n))
     _call(codes.get_device(), stream, _lib.gemm_f16_q8_dequantize, x.r, x.n, codes.data_ptr(),
           x.scales.data_ptr(), out.data_ptr())

@@ -1,4 +1,8 @@
 """The low-bit operands at the edges of what gemm_f16_lowbit.h allows."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -59,3 +63,35 @@ def test_nt_w4_scales_past_the_matrix(g, kernel, m, n, k, group):  # noqa: F811
             q.scales[-1, :, n % 16:] = value
         assert torch.equal(g.gemm_nt_w4(a, q), want)
         assert g.dequantize_w4(q).isfinite().all()
+
+
+# ---- saved and read back ----------------------------------------------------------
+READ_BACK = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch, dense_fp16_gemm_amd as g
+safe = sys.argv[3] == "safe"
+if safe:
+    torch.serialization.add_safe_globals([g.W4Matrix, g.Q8Matrix])
+w, x, a, dy, y, dw = torch.load(sys.argv[2], weights_only=safe)
+assert torch.equal(g.gemm_nt_w4(a, w), y) and torch.equal(g.gemm_tn_q8(dy, x), dw)
+assert (w.shape, w.group, x.shape) == ((50, 200), 64, (30, 70))
+print("same")
+"""
+
+
+@pytest.mark.parametrize("how", ["safe", "any"])
+def test_saved_matrices_in_a_new_process(g, how, tmp_path):  # noqa: F811
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w = g.quantize_w4(torch.randn(50, 200, generator=gen, device="cuda").half(), 64)
+    x = g.quantize_q8(torch.randn(30, 70, generator=gen, device="cuda").half())
+    a = torch.randn(3, 200, generator=gen, device="cuda").half()
+    dy = torch.randn(30, 9, generator=gen, device="cuda").half()
+    path = str(tmp_path / "matrices.pt")
+    torch.save((w, x, a, dy, g.gemm_nt_w4(a, w), g.gemm_tn_q8(dy, x)), path)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", READ_BACK, root, path, how], timeout=100,
+                       capture_output=True)
+    assert r.returncode == 0 and r.stdout == b"same\n", r.stderr.decode()[-2000:]
