@@ -38,6 +38,16 @@ __device__ __forceinline__ T bits_as(S s)
 // it alone (which tile, its addresses) then takes no vector operations.
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
+// Between a wave's LDS writes and its other lanes' reads of them, and before the
+// next writes: a wave's LDS operations are done in order, so no instruction is
+// needed, but the compiler may move one lane's accesses past each other unless
+// it is told that the lanes exchange them.
+__device__ __forceinline__ void wave_lds_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // This workgroup's unit of work, where each XCD (workgroups mod 8) takes a
 // contiguous range of them: neighbours share cache lines in its L2.
 __device__ __forceinline__ int32_t xcd_unit()
@@ -593,16 +603,25 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
     const int rr = r < RL * 4 ? r : RL * 4 - 1;
     auto mma = [&](int buf, int) {
         half8_t a[4][MT];
-        // the wave alone uses these 4 RL rows, and its LDS operations keep
-        // their order
+        auto read_a = [&](int j, int mt) {
+            a[j][mt] = ab[(16 * mt + rr) * 16 + ((4 * j + kq) ^ rr)];
+        };
+        // the wave alone uses these 4 RL rows; the reads that the first MFMAs wait
+        // for start between the writes (after all of them: 48 x 14336 x 4096 takes
+        // 16.4 us for 15.0)
+        wave_lds_fence();
 #pragma unroll
-        for (int i = 0; i < RL; ++i)
-            ab[(4 * i + kq) * 16 + (r ^ ((4 * i + kq) & 15))] = af[buf][i];
+        for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+            for (int i = 4 * mt; i < 4 * mt + 4 && i < RL; ++i)
+                ab[(4 * i + kq) * 16 + (r ^ ((4 * i + kq) & 15))] = af[buf][i];
+            wave_lds_fence();
+            read_a(0, mt);
+        }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                a[j][mt] = ab[(16 * mt + rr) * 16 + ((4 * j + kq) ^ rr)];
+        for (int j = 1; j < 4; ++j)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) read_a(j, mt);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1284,6 +1303,7 @@ __global__ __launch_bounds__(64 * W, 2) void q8_tn_kernel(Q8TnParams p)
     };
     f32x4_t acc[MT][CB] = {};
     auto mma = [&](int buf) {
+        wave_lds_fence();
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             const int c = j * 64 + lane;
@@ -1292,6 +1312,7 @@ __global__ __launch_bounds__(64 * W, 2) void q8_tn_kernel(Q8TnParams p)
 #pragma unroll
         for (int g = 0; g < G / 2; ++g)
             my.s[(lane & 1) * (G / 2) + g][lane >> 1] = bits_as<_Float16>(sv[buf][g]);
+        wave_lds_fence();
         half8_t a[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 import lowbit_ref as ref
-from test_gpu_lowbit import W4_KERNELS, dev, g, host  # noqa: F401  (g: the fixture)
+from test_gpu_lowbit import Q8_KERNELS, W4_KERNELS, dev, g, host  # noqa: F401  (g: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -63,6 +63,66 @@ def test_nt_w4_scales_past_the_matrix(g, kernel, m, n, k, group):  # noqa: F811
             q.scales[-1, :, n % 16:] = value
         assert torch.equal(g.gemm_nt_w4(a, q), want)
         assert g.dequantize_w4(q).isfinite().all()
+
+
+# ---- sums of whole numbers -----------------------------------------------------------
+# Every sum of the two tests below is a whole number of at most 2048 (times a
+# power of two), so it is exact in fp32 in any order and in fp16: one product lost,
+# repeated or misplaced changes a result.  With factor 2^-24 the weights are fp16's
+# subnormal numbers, and A's 2^10 times larger.
+def few(gen, shape, one_in):
+    """-1, 0 and 1 in fp16, one in `one_in` not zero."""
+    import torch
+
+    r = torch.randint(0, 2 * one_in, shape, generator=gen, device="cuda", dtype=torch.int16)
+    return (r == 0).half() - (r == 1).half()
+
+
+def sign(gen, shape):
+    import torch
+
+    return torch.randint(0, 2, shape, generator=gen, device="cuda").half() * 2 - 1
+
+
+def check_whole(got, a, b, factor):
+    """got is a @ b exactly, times factor (a and b whole numbers)."""
+    import torch
+
+    want = torch.matmul(a.double(), b.double().contiguous())
+    assert want.abs().max() <= 2048
+    assert torch.equal(got.double(), want * factor)
+
+
+@pytest.mark.parametrize("small", [False, True])
+@pytest.mark.parametrize("kernel,m,n,k", W4_KERNELS)
+def test_nt_w4_whole_sums(g, kernel, m, n, k, small):  # noqa: F811
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(m + n + k)
+    codes = torch.randint(-8, 8, (n, k), generator=gen, device="cuda", dtype=torch.int8)
+    signs = sign(gen, (n, -(-k // 32)))
+    w = codes.half() * signs.repeat_interleave(32, 1)[:, :k]
+    a = few(gen, (m, k), 8)
+    scale, up = (2.0 ** -24, 2.0 ** 10) if small else (1.0, 1.0)
+    q = g.pack_w4(codes, signs * scale, 32)
+    check_whole(g.gemm_nt_w4(a * up, q), a, w.t(), scale * up)
+
+
+@pytest.mark.parametrize("small", [False, True])
+@pytest.mark.parametrize("kernel,splits,m,n,k", Q8_KERNELS)
+def test_tn_q8_whole_sums(g, kernel, splits, m, n, k, small):  # noqa: F811
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(m + n + k)
+    groups = -(-n // 32)
+    codes = torch.zeros((k, groups * 32), device="cuda", dtype=torch.int8)
+    codes[:, :n] = torch.randint(-20, 21, (k, n), generator=gen, device="cuda", dtype=torch.int8)
+    signs = sign(gen, (k, groups))
+    x = (codes.half() * signs.repeat_interleave(32, 1))[:, :n]
+    a = few(gen, (k, m), 20)
+    scale, up = (2.0 ** -24, 2.0 ** 10) if small else (1.0, 1.0)
+    got = g.gemm_tn_q8(a * up, g.Q8Matrix(codes, signs * scale, n))
+    check_whole(got, a.t().contiguous(), x, scale * up)
 
 
 # ---- saved and read back ----------------------------------------------------------

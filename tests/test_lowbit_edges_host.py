@@ -1,6 +1,8 @@
-"""Low-bit matrices that did not come from this process's own quantisers (no GPU)."""
+"""What the low-bit operands' tests on a GPU cannot show, or need not (no GPU):
+matrices read back in a new process, and how a wave's lanes exchange data in LDS."""
 import os
 import pickle
+import re
 import subprocess
 import sys
 
@@ -69,3 +71,21 @@ def test_dequantize_refuses_host_memory(g):
         for out in (None, torch.zeros(m.shape).half()):
             with pytest.raises(ValueError, match="GPU"):
                 call(m, out=out)
+
+
+@pytest.mark.parametrize("kernel,write,read", [
+    ("w4_rows_kernel", r"ab\[[^;]*\] = af", r"read_a\(0, mt\)"),
+    ("q8_tn_kernel", r"my\.(?:a|s)\[[^;]*(?:av|sv)\[buf\]", r"lds_read_tr16\(src\)|half8_t \*>\(&my\.s"),
+], ids=["w4_rows", "q8_tn"])
+def test_lanes_of_a_wave_exchange_data_across_a_fence(kernel, write, read):
+    """Without one the compiler may move a lane's reads past its own writes, since
+    it does not know that other lanes wrote what they read.  One fence stands
+    before the writes (of what may still have to be read), one before the reads."""
+    source = open(os.path.join(ROOT, "dense_fp16_gemm_amd", "csrc", "lowbit.hip")).read()
+    body = source[source.index(f"void {kernel}("):]
+    body = body[body.index("auto mma = "):]
+    body = body[:body.index("\n    };\n")]
+    steps = [m.lastgroup for m in re.finditer(
+        rf"(?P<fence>wave_lds_fence\(\);)|(?P<write>{write})|(?P<read>{read})", body)]
+    steps = [s for i, s in enumerate(steps) if i == 0 or s != steps[i - 1]]
+    assert steps == ["fence", "write", "fence", "read"]
