@@ -36,6 +36,37 @@ def test_w4_pack_every_scale(g):  # noqa: F811
                                   ref.values(want, r, 32, 64))
 
 
+# ---- every quotient --------------------------------------------------------------
+@pytest.mark.parametrize("form", ["w4", "q8"])
+def test_every_half_over_every_scale(g, form):  # noqa: F811
+    """All finite fp16 numbers of both signs in groups of every scale that
+    reaches them: the scale is found and each quotient rounded exactly."""
+    import torch
+
+    spec = ref.W4 if form == "w4" else ref.Q8
+    top = spec["top"]
+    all_scales = ref.scales_list(spec["bits"], spec["most"])
+    halves = torch.arange(0x7c00, device="cuda", dtype=torch.int16).view(torch.float16)
+    halves = torch.nn.functional.pad(halves, (0, -halves.numel() % 31)).view(-1, 31)
+    for first in range(0, len(all_scales), 256):
+        s = torch.from_numpy(all_scales[first:first + 256]).cuda()
+        # the group's largest, exact in fp16 where it is not past its largest
+        lead = (s * top).clamp(max=65504.0).half()
+        last = s == spec["most"]
+        x = halves.repeat(len(s), 1, 1)
+        x[(x > lead[:, None, None]) & ~last[:, None, None]] = 0
+        x = torch.cat([lead[:, None, None].expand(-1, halves.shape[0], 1), x], 2).view(len(s), -1)
+        code = (x.double() / s[:, None]).round().clamp_(-top, top)
+        code -= (code * s[:, None] > 65504).double()
+        for x, code in ((x, code), (-x, -code)):
+            q = g.quantize_w4(x, 32) if form == "w4" else g.quantize_q8(x)
+            stored = q.scales.permute(0, 2, 1).reshape(-1, x.shape[1] // 32)[:len(s)] \
+                if form == "w4" else q.scales
+            assert (stored.double() == s[:, None]).all()
+            back = g.dequantize_w4(q) if form == "w4" else g.dequantize_q8(q)
+            assert (back.double() == code * s[:, None]).all()
+
+
 # ---- storage that another program laid out ---------------------------------------
 def padded(k, group):
     """Whether the last tile of K has groups that lie past K."""
@@ -123,6 +154,96 @@ def test_tn_q8_whole_sums(g, kernel, splits, m, n, k, small):  # noqa: F811
     scale, up = (2.0 ** -24, 2.0 ** 10) if small else (1.0, 1.0)
     got = g.gemm_tn_q8(a * up, g.Q8Matrix(codes, signs * scale, n))
     check_whole(got, a.t().contiguous(), x, scale * up)
+
+
+# ---- streams --------------------------------------------------------------------
+LIVES = ["quantize_w4", "pack_w4", "dequantize_w4", "quantize_q8", "dequantize_q8",
+         "w4 streamed", "w4 tiles", "w4 tiles, workspace", "w4 decoded", "q8 streamed", "q8 decoded"]
+
+
+def operands_and_call(g, what):  # noqa: F811
+    """(call(**kw) giving tensors, the tensors that it is given)."""
+    import torch
+
+    rng = np.random.default_rng(3)
+    x = dev(rng.standard_normal((1024, 2048)).astype(np.float16))
+    if what == "quantize_w4":
+        def call(**kw):
+            q = g.quantize_w4(x, 64, **kw)
+            return q.words, q.scales
+        return call, [x]
+    if what == "quantize_q8":
+        def call(**kw):
+            q = g.quantize_q8(x, **kw)
+            return q.codes, q.scales
+        return call, [x]
+    if what == "pack_w4":
+        codes = dev(rng.integers(-8, 8, (1024, 2048)).astype(np.int8))
+        scales = dev(rng.uniform(0.5, 1, (1024, 32)).astype(np.float16))
+
+        def call(**kw):
+            q = g.pack_w4(codes, scales, 64, **kw)
+            return q.words, q.scales
+        return call, [codes, scales]
+    if what in ("dequantize_q8", "q8 streamed", "q8 decoded"):
+        q = g.quantize_q8(x)
+        if what == "dequantize_q8":
+            return lambda **kw: (g.dequantize_q8(q, **kw),), [q.codes, q.scales]
+        a = dev(rng.standard_normal((1024, 16 if what == "q8 streamed" else 1200)).astype(np.float16))
+        return lambda **kw: (g.gemm_tn_q8(a, q, **kw),), [a, q.codes, q.scales]
+    q = g.quantize_w4(x, 64)
+    if what == "dequantize_w4":
+        return lambda **kw: (g.dequantize_w4(q, **kw),), [q.words, q.scales]
+    rows = {"w4 streamed": 8, "w4 decoded": 8200}.get(what, 80)
+    a = dev(rng.standard_normal((rows, 2048)).astype(np.float16))
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    plan = g.gemm_f16_nt_w4_plan(rows, q.n, q.k, 64, cus)
+    assert plan.kernel == {"w4 streamed": g.LOWBIT_STREAM, "w4 decoded": g.LOWBIT_DECODE}.get(
+        what, g.LOWBIT_TILE)
+    if what != "w4 tiles, workspace":
+        return lambda **kw: (g.gemm_nt_w4(a, q, **kw),), [a, q.words, q.scales]
+    assert plan.workspace_bytes > 0
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    return lambda **kw: (g.gemm_nt_w4(a, q, workspace=ws, **kw),), [a, q.words, q.scales, ws]
+
+
+@pytest.mark.parametrize("what", LIVES)
+def test_operands_dropped_at_once(g, what):  # noqa: F811
+    """Operands (and a workspace) of the default stream, used on a busy stream
+    and dropped at once: their memory goes to no other tensor before they are
+    read."""
+    import torch
+
+    want = [host(t) for t in operands_and_call(g, what)[0]()]
+    s, done = torch.cuda.Stream(), torch.cuda.Event()
+    filler = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    # torch's memory for what both streams allocate later: new memory from the
+    # driver would wait for s
+    operands_and_call(g, what)[0](stream=s)
+    s.synchronize()
+    call, given = operands_and_call(g, what)
+    ranges = [(t.data_ptr(), t.numel() * t.element_size()) for t in given]
+    spare = [torch.empty(size, dtype=torch.uint8, device="cuda") for _, size in ranges
+             for _ in range(8)]
+    del spare
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(200):   # some 40 ms
+            filler[:1 << 29].copy_(filler[1 << 29:])
+    got = call(stream=s)
+    done.record(s)
+    del call, given
+    later = [torch.empty(size, dtype=torch.uint8, device="cuda") for _, size in ranges
+             for _ in range(4)]
+    # (asked before the default stream gets work: it may share a hardware queue with s)
+    assert not done.query(), "the stream was not busy for long enough to show anything"
+    for t in later:
+        for at, size in ranges:
+            assert t.data_ptr() + t.numel() <= at or at + size <= t.data_ptr()
+        t.fill_(0x55)
+    s.synchronize()
+    for t, w in zip(got, want):
+        np.testing.assert_array_equal(host(t), w)
 
 
 # ---- saved and read back ----------------------------------------------------------
