@@ -140,9 +140,10 @@ __device__ __forceinline__ float half_of(u32x4_t v, int i)
 // One wave per tile of 16 rows by 128 columns, each lane the 32 weights whose
 // words it writes: four loads of 16 bytes (8 for int8 codes), the group's
 // largest magnitude over the four lanes of a row, one 16-byte store.  Memory
-// bounds it (4096 x 14336: 33.3 us, 4.4 TB/s).  Loads of 256 bytes of four rows,
-// turned round in LDS, took 22 us for 28 where rows are not 16-byte aligned, and
-// 1 to 2 us more where they are, as weights' rows mostly are.
+// bounds quantising (8192 x 8192: 36.1 us, 4.7 TB/s); packing takes as long for 0.6
+// of the bytes, with the vector ALU at its checks for 68% of the cycles.  Loads of
+// 256 bytes of four rows, turned round in LDS, took 22 us for 28 where rows are not
+// 16-byte aligned, and 1 to 2 us more where they are, as weights' rows mostly are.
 struct W4EncodeParams {
     const uint16_t *W;       // fp16 [N, K], or
     const int8_t *codes;     // int8 [N, K] and
@@ -333,8 +334,9 @@ struct W4DecodeParams {
     int32_t shift;
 };
 
-// W4 back to fp16, one wave per tile; memory bounds it (8192 x 8192: 25.5 us, 6.6
-// TB/s; 28.3 with neighbouring tiles on different XCDs).
+// W4 back to fp16, one wave per tile; memory bounds it (8192 x 8192: 39 to 43 us,
+// 4.0 to 4.3 TB/s, and 25.8 where the words were written just before and come from
+// the last cache; 28.3 there with neighbouring tiles on different XCDs).
 __global__ __launch_bounds__(64 * WAVES) void w4_decode_kernel(W4DecodeParams p)
 {
     const int lane = threadIdx.x & 63;
@@ -460,10 +462,9 @@ __device__ __forceinline__ void w4_run_tiles(int32_t full, int wave, Load load, 
 // accumulators multiplies the words of its own step with the whole register,
 // and of its results only the columns of that step are used.
 //
-// JC = 4, eight waves with two tiles a buffer: 1 x 4096 x 14336 takes 7.0 us at
-// best from HBM (2.3 us of it an empty kernel's), 1 x 16384 x 16384 25.2 us (5.3
-// TB/s).  When that first one took 8.0 us, one tile a buffer took 9.1 (and 27.1),
-// four 9.8 (35.6).
+// JC = 4, eight waves with two tiles a buffer: 1 x 4096 x 14336 takes 7.9 us in the
+// median of a trace (7.6 at best; 2.3 of it an empty kernel's), 1 x 16384 x 16384
+// 25.2 us (5.3 TB/s).  One tile a buffer took 9.1 (and 27.1), four 9.8 (35.6).
 template <int SH, int JC, int NB, int W, int D>
 __global__ __launch_bounds__(64 * W) void w4_stream_kernel(W4Params p)
 {
@@ -669,11 +670,14 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(W4Params p)
 //
 // What bounds it is the vector ALU beside the matrix units: unpacking a word
 // of eight weights takes 12 operations of 4 cycles, while its MFMAs take 16 MT
-// cycles.  w4_tile_pair scales and centres in one fused operation to save three
-// of 15 (333 x 4096 x 14336: 51.7 to 48.1 us, 48 x 16384 x 16384: 47.1 to 43.0),
-// and a word is unpacked between the MFMAs of the word before it.  333 x 4096 x
-// 14336 now keeps the matrix units busy for 51% of the cycles, at a clock that
-// the power limit holds near 1.75 GHz; 512 x 16384 x 16384 runs at 1.2 PFLOP/s.
+// cycles.  At 48 x 16384 x 16384 the two keep a SIMD busy for 50% and 35% of the
+// cycles, and the waves stand at waits for 42% of theirs; the LDS is busy for
+// 22% (19 to 29% at all sizes traced), so it is not what holds them up.
+// w4_tile_pair scales and centres in one fused operation to save three of 15
+// (333 x 4096 x 14336: 51.7 to 48.1 us, 48 x 16384 x 16384: 47.1 to 43.0), and a
+// word is unpacked between the MFMAs of the word before it.  333 x 4096 x 14336
+// now keeps the matrix units busy for 52% of the cycles, at a clock that the
+// power limit holds near 1.75 GHz; 512 x 16384 x 16384 runs at 1.2 PFLOP/s.
 //
 // Few tiles leave CUs idle: K is then split, each range's fp32 sums go to the
 // workspace in the order in which lanes hold them (every store and load a
@@ -1774,9 +1778,11 @@ constexpr int64_t W4_STREAM_ROWS = 48;
 // 160 shapes (20 to 2048 rows, N and K of 512 to 32768, words from HBM): rounds
 // of workgroups over the CUs times the steps of a range, the clock that long
 // products lose to the power limit, and for a split the partial sums' way
-// through memory and the join.  Its error is 6%; what it chose took 1 to 2% longer
-// than the best of each shape in the mean, 16% in the worst.  (Of 17 to 48 rows,
-// the tile kernels alone took 25% longer: 32 x 4096 x 4096 9.8 us, streamed 7.5.)
+// through memory and the join.  (Those timings are not kept with the source.)  Its
+// error is 6%; what it chose took 1 to 2% longer than the best of each shape in
+// the mean, 16 to 17% in the worst (333 x 4096 x 4096: 96 x 128 in two ranges,
+// 24.3 us, where 64 x 128 unsplit took 20.7).  (Of 17 to 48 rows, the tile kernels
+// alone took 25% longer: 32 x 4096 x 4096 9.8 us, streamed 7.5.)
 static W4Choice w4_search(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
 {
     const double nk = static_cast<double>(s.nb) * 16 * K;
@@ -1819,6 +1825,9 @@ static W4Choice w4_search(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
 static W4Choice w4_choose(int64_t M, int64_t K, const W4Shape &s, int32_t cus)
 {
     if (s.nb > W4_MOST_WORKGROUPS) return {-1, 1};
+    // Streamed and never split, which is right where the blocks of 16 columns fill
+    // the CUs.  Few columns of a long K leave them empty: 16 x 64 x 2^20 takes 723 us
+    // and 17 rows, which a search splits, 81; 16 x 1024 x 16384 12.4 and 10.9.
     if (M <= 16) return {w4_choose_stream(M, s, cus, nullptr), 1};
     // the search takes microseconds: each thread keeps its last few choices
     struct Entry {
@@ -1919,7 +1928,7 @@ static int w4_run(const W4Choice &c, const gemm_f16_lowbit_plan_t &plan, int64_t
     if (K % 8 == 0 && reinterpret_cast<uintptr_t>(A) % 16 != 0) {
         // the tile kernels' loads need 16-byte aligned rows, and the workspace
         // is planned by sizes alone: 48 rows at a time by the kernels that take
-        // any alignment
+        // any alignment (64 x 4096 x 14336: 68 us for 18; 512 x 4096 x 4096: 186 for 24)
         for (int64_t m = 0; m < M; m += W4_STREAM_ROWS) {
             const int64_t rows = std::min(W4_STREAM_ROWS, M - m);
             double us = 0;
@@ -2012,7 +2021,8 @@ static Q8Choice q8_layout(int32_t id, int64_t M, int64_t K, const Q8Shape &s, in
 // Streaming the codes (in one range, or in as many as fill the CUs), or
 // decoding them for the GEMM, by models of their times in us, fitted to 2,900
 // timings of 870 shapes (8 to 7668 rows of C, 64 to 14336 columns, 3 to 8192
-// rows of X, sizes that are multiples of 8 and not).  Streaming reads the codes
+// rows of X, sizes that are multiples of 8 and not; not kept with the source).
+// Streaming reads the codes
 // again for each tile of rows of C; it wins up to some 64 rows everywhere (1.1
 // to 3.2 times), with hundreds of rows where the columns are few, and with
 // thousands where the rows of X are (3300 x 3613 over 54 rows: 31.4 us decoded,

@@ -11,7 +11,9 @@ As in the rest of the package, every arithmetic step runs in the library's HIP
 kernels and torch gives device memory and streams only.  Each function works
 on the current stream, or on `stream`: what it allocates then belongs to that
 stream, and the tensors passed in are recorded on it, so that the caller may
-drop them at once.
+drop them at once.  Like the rest of the package, none of them takes part in
+autograd: what they return is cut off from the graph of tensors that require
+gradients, and a torch.autograd.Function connects it.
 """
 from __future__ import annotations
 
@@ -340,8 +342,9 @@ def quantize_w4(w, group: int = 128, stream=None) -> W4Matrix:
 def pack_w4(codes, scales, group: int = 128, stream=None) -> W4Matrix:
     """A W4Matrix from another quantiser's codes [N, K] int8 in -8..7 and scales
     [N, ceil(K / group)] fp16, weight = code * scale.  Scales are rounded to 8
-    significant bits; a group that cannot be held (a code out of range, a scale
-    that is not finite or is rounded to 65536, a weight past 65504) becomes NaN."""
+    significant bits, by up to 2^-8 of their value; a group that cannot be held
+    (a code out of range, a scale that is not finite or is rounded to 65536, a
+    weight past 65504) becomes NaN."""
     if torch is None:
         _bind_torch()
     if not _is_matrix(codes, _int8):
@@ -437,7 +440,10 @@ def _workspace(need, on, workspace, stream):
 def gemm_nt_w4(a, w: W4Matrix, out=None, workspace=None, stream=None):
     """C = a @ W.T for a [M, K] fp16 and W [N, K] in 4 bits, fp16 [M, N]
     (gemm_f16_nt_w4).  The workspace that some sizes need (see
-    gemm_f16_nt_w4_plan) is allocated with torch unless `workspace` is given."""
+    gemm_f16_nt_w4_plan) is allocated with torch unless `workspace` is given.
+    More than 48 rows want an a that is 16-byte aligned, as torch's own tensors
+    are, or a K that is not a multiple of 8 (for which rows are copied): others
+    take several times as long."""
     if not isinstance(w, W4Matrix):
         raise TypeError("w must be a W4Matrix")
     if not _is_matrix(a, _f16):

@@ -71,9 +71,10 @@ extern "C" {
  *
  * gemm_f16_w4_pack: the same storage from codes int8 [N, K] row-major and
  * in_scales fp16 [N, ceil(K / group)] row-major that another quantiser made.
- * Scales are rounded to 8 significant bits (to nearest, ties to even).  A
- * group with a code outside -8 .. 7, a scale that is not finite (as given or,
- * from 65408, as rounded), or a product past 65504 gets s = NaN and codes 0.
+ * Scales are rounded to 8 significant bits (to nearest, ties to even), which
+ * changes each weight of a group by up to 2^-8 of its value.  A group with a
+ * code outside -8 .. 7, a scale that is not finite (as given or, from 65408, as
+ * rounded), or a product past 65504 gets s = NaN and codes 0.
  *
  * gemm_f16_w4_dequantize: words and scales to W fp16 [N, K] row-major.
  *
@@ -126,7 +127,11 @@ typedef struct {
  * workspaces unless they are ordered on one stream.
  *
  * gemm_f16_nt_w4_plan: pure host function.  What gemm_f16_nt_w4 runs on a
- * device with num_cus compute units.
+ * device with num_cus compute units, for an A that is 16-byte aligned.  Where K
+ * is a multiple of 8 and A is not so aligned, sizes planned for the tile kernels
+ * are streamed instead, 48 rows of A at a time, without the planned workspace
+ * (which is asked for all the same).  The weights are then read again for each
+ * 48 rows: some hundreds of rows take several times as long.
  *
  * M = 0 or N = 0: nothing to compute.  K = 0: C is filled with +0.
  * GEMM_F16_UNSUPPORTED for M above 2^31 - 1, for N and K as above, and for

@@ -81,12 +81,14 @@ def round8(s: np.ndarray) -> np.ndarray:
 def product_bound(a_abs_sum: np.ndarray, exact: np.ndarray, k: int) -> np.ndarray:
     """How far a correct kernel's fp16 result may be from the exact sum.
 
-    The operands' products are exact in fp32 (22 significant bits, 25 where a
-    scale is applied to a sum, which then costs one rounding more for each
-    group).  A path to a result passes at most 8 fp32 additions for each MFMA
-    of 32 products, one fused multiply-add for each group of 32 or more, and
-    a few to join partial sums: K / 4 + K / 32 + 72 roundings of at most 2^-24
-    of the sum of magnitudes.  Rounding to fp16 is half a step: 2^-11 of the
+    The operands' products are exact in fp32: scale times code is an fp16
+    number, and two of those make 22 significant bits.  A path to a result
+    passes at most 8 fp32 additions for each MFMA of 32 products, K / 4 in all,
+    and some to join partial sums (8 waves and 64 ranges: 72; more ranges leave
+    each a smaller share of the K / 4), each a rounding of at most 2^-24 of the
+    sum of magnitudes.
+    The K / 32 more is room that no kernel needs (one that scaled the sum of a
+    group of codes would).  Rounding to fp16 is half a step: 2^-11 of the
     value, or 2^-25 among the subnormals."""
     fp32 = (k / 4 + k / 32 + 72) * 2.0 ** -24 * a_abs_sum
     return fp32 + (np.abs(exact) + fp32) * 2.0 ** -11 + 2.0 ** -25
