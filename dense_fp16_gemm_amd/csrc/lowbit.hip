@@ -817,8 +817,9 @@ __global__ __launch_bounds__(64 * W, 2) void w4_tile_kernel(W4TileParams p)
         const int d = i * 64 + lane, blk = d / (NS * 8), rem = d % (NS * 8);
         vs[i] = blk < NB ? static_cast<uint32_t>(blk) * p.kt * (NS * 32u) + rem * 4u : OOB_OFFSET;
         // in the tile that K ends in, without the scales of groups past K, which may
-        // hold anything (chosen by a scalar condition: compared for each step, group
-        // against K, 20 x 4096 x 14336 took 1 to 2% longer)
+        // hold anything (chosen by a scalar condition, which costs up to 1.5% with
+        // groups of 64 and nothing with 128; compared for each step, group against K,
+        // 20 x 4096 x 14336 took 1 to 2% longer throughout)
         vp[i] = static_cast<uint32_t>(t_end) * 128u + ((rem / 8) << SH) < klen ? vs[i] : OOB_OFFSET;
     }
     int aoff[4];
