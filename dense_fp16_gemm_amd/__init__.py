@@ -128,7 +128,8 @@ def load():
         lib.gemm_f16_splitk_workspace_bytes.restype = ctypes.c_int
         lib.gemm_f16_device_cus.argtypes = [ctypes.POINTER(i32)]
         lib.gemm_f16_device_cus.restype = ctypes.c_int
-        lowbit._declare(lib)
+        for module in (lowbit, f8, experts):
+            module._declare(lib)
         _lib = lib
         return lib
 
@@ -572,3 +573,15 @@ from .lowbit import (  # noqa: E402,F401
     gemm_f16_nt_w4_plan, gemm_f16_q8_dequantize, gemm_f16_q8_quantize, gemm_f16_tn_q8,
     gemm_f16_tn_q8_plan, gemm_f16_w4_dequantize, gemm_f16_w4_pack, gemm_f16_w4_quantize,
     gemm_f16_w4_sizes, gemm_nt_w4, gemm_tn_q8, pack_w4, quantize_q8, quantize_w4)
+
+# Products in 8-bit floating point, and the layers of experts that use them.
+from . import experts, f8  # noqa: E402
+from .experts import (  # noqa: E402,F401
+    Routing, combine_experts, combine_experts_backward, gemm_f16_combine,
+    gemm_f16_combine_backward, gemm_f16_f8_experts_columns, gemm_f16_f8_quantize_experts,
+    gemm_f16_nt_f8_experts, gemm_f16_nt_f8_experts_grad, gemm_f16_nt_f8_experts_plan,
+    gemm_f16_nt_f8_experts_x, gemm_f16_route, gemm_f16_route_backward, gemm_f16_route_workspace,
+    gemm_nt_f8_experts, gemm_nt_f8_experts_grad, quantize_f8_experts, route, route_backward)
+from .f8 import (  # noqa: E402,F401
+    F8Matrix, dequantize_f8, gemm_f16_f8_dequantize, gemm_f16_f8_quantize, gemm_f16_f8_sizes,
+    gemm_f16_nt_f8, gemm_f16_nt_f8_plan, gemm_f16_nt_f8_x, gemm_nt_f8, quantize_f8)

@@ -1,0 +1,749 @@
+// Routing of tokens to experts, the order of their rows, and the weighted sum
+// that puts a token's rows together again (see gemm_f16_experts.h).
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gemm_f16_experts.h"
+
+namespace gemm_f16_experts {
+
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+// 16 bytes at any 2-byte alignment (the target's unaligned-access mode)
+typedef _Float16 half8_u_t __attribute__((ext_vector_type(8), aligned(2)));
+
+constexpr int MOST_EXPERTS = 1024, MOST_TOP = 32, MOST_GROUPS = 64;
+
+// The wave's index in its workgroup, in a scalar register.
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// Between a wave's LDS writes and its other lanes' reads of them: see that the
+// compiler keeps their order (a wave's LDS operations are done in order).
+__device__ __forceinline__ void wave_lds_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ double shfl_xor64(double v, int d)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __shfl_xor(static_cast<uint32_t>(b), d);
+    const uint32_t hi = __shfl_xor(static_cast<uint32_t>(b >> 32), d);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ double readlane64(double v, int lane)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(b), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), lane);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// The largest of 64 lanes' values, in every lane: five steps within the wave's
+// rows of 16 and across them, read from the last lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+#define STEP(CTRL, ROWS)                                                                         \
+    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false)))
+    STEP(0x111, 0xf);   // row_shr 1, 2, 4, 8
+    STEP(0x112, 0xf);
+    STEP(0x114, 0xf);
+    STEP(0x118, 0xf);
+    STEP(0x142, 0xa);   // row_bcast 15, 31
+    STEP(0x143, 0xc);
+#undef STEP
+    return __builtin_amdgcn_readlane(v, 63);
+}
+
+// Numbers as integers in the same order (no NaN among them).
+__device__ __forceinline__ uint64_t ordered(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
+
+// ---------------------------------------------------------------------------
+// The choice: one wave a token
+// ---------------------------------------------------------------------------
+struct RouteParams {
+    const void *logits;
+    const float *bias;
+    int32_t *experts;
+    float *weights;
+    double scale;
+    int32_t T, E, top, groups, top_groups;
+    bool f32, sigmoid, group_max, renormalize;
+};
+
+__device__ __forceinline__ double load_logit(const void *logits, bool f32, int64_t at)
+{
+    return f32 ? static_cast<double>(static_cast<const float *>(logits)[at])
+               : static_cast<double>(static_cast<float>(static_cast<const _Float16 *>(logits)[at]));
+}
+
+// Lane l holds experts l, l + 64, ...: their logits x to their scores s.  Absent
+// experts have x = -inf.  False where the row has none (a NaN, or +inf with
+// softmax).
+template <int V>
+__device__ __forceinline__ bool scores_of(const double (&x)[V], bool sigmoid, double (&s)[V])
+{
+    constexpr double inf = __builtin_huge_val();
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) bad |= !(x[i] == x[i]) || (!sigmoid && x[i] == inf);
+    if (__any(bad)) return false;
+    if (sigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = 1.0 / (1.0 + exp(-x[i]));
+        return true;
+    }
+    double m = -inf;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmax(m, x[i]);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) m = fmax(m, shfl_xor64(m, d));
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        s[i] = x[i] == -inf ? 0.0 : exp(x[i] - m);
+        sum += s[i];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) sum += shfl_xor64(sum, d);
+    const double by = sum > 0.0 ? sum : 1.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] /= by;
+    return true;
+}
+
+template <int V>
+__device__ __forceinline__ void route_token(const RouteParams &p, int32_t t, int lane, double *cs)
+{
+    constexpr double inf = __builtin_huge_val();
+    double x[V], s[V], c[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int32_t e = i * 64 + lane;
+        x[i] = e < p.E ? load_logit(p.logits, p.f32, static_cast<int64_t>(t) * p.E + e) : -inf;
+    }
+    bool fine = scores_of(x, p.sigmoid, s);
+    if (fine) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int32_t e = i * 64 + lane;
+            c[i] = s[i];
+            if (p.bias && e < p.E) c[i] += static_cast<double>(p.bias[e]);
+            if (x[i] == -inf) c[i] = -inf;
+            bad |= !(c[i] == c[i]);
+        }
+        fine = !__any(bad);
+    }
+    const int64_t out = static_cast<int64_t>(t) * p.top;
+    if (!fine) {
+        if (lane < p.top) {
+            p.experts[out + lane] = -1;
+            p.weights[out + lane] = __builtin_nanf("");
+        }
+        return;
+    }
+    if (p.groups > 1) {
+        const int32_t per = p.E / p.groups;
+        wave_lds_fence();
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * 64 + lane < p.E) cs[i * 64 + lane] = c[i];
+        wave_lds_fence();
+        // 64 / groups lanes a group (groups rounded up to a power of two)
+        int shift = 6;
+        while ((64 >> shift) < p.groups) --shift;
+        const int g = lane >> shift;
+        double first = -inf, second = -inf;
+        if (g < p.groups)
+            for (int32_t j = lane & ((1 << shift) - 1); j < per; j += 1 << shift) {
+                const double v = cs[g * per + j];
+                second = fmax(second, fmin(first, v));
+                first = fmax(first, v);
+            }
+        for (int d = 1; d < 1 << shift; d *= 2) {
+            const double f = shfl_xor64(first, d), o = shfl_xor64(second, d);
+            second = fmax(fmax(second, o), fmin(first, f));
+            first = fmax(first, f);
+        }
+        double score = first;
+        if (!p.group_max && second > -inf) score += second;
+        int rank = 0;
+        for (int q = 0; q < p.groups; ++q) {
+            const double o = readlane64(score, q << shift);
+            rank += o > score || (o == score && q < g) ? 1 : 0;
+        }
+        const uint64_t kept = __ballot(g < p.groups && first > -inf && rank < p.top_groups);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int32_t e = i * 64 + lane;
+            if (e < p.E && !(kept >> ((e / per) << shift) & 1)) c[i] = -inf;
+        }
+    }
+    uint64_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = ordered(c[i]);
+    const uint64_t none = ordered(-inf);
+    int32_t mine = -1;
+    double weight = 0.0, total = 0.0;
+    for (int j = 0; j < p.top; ++j) {
+        uint64_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
+        const uint32_t hi = wave_max(static_cast<uint32_t>(best >> 32));
+        const uint32_t lo = wave_max(best >> 32 == hi ? static_cast<uint32_t>(best) : 0u);
+        const uint64_t top = static_cast<uint64_t>(hi) << 32 | lo;
+        if (top <= none) break;
+        // the lowest expert that has it
+        uint32_t at = 0;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+            if (key[i] == top) at = ~static_cast<uint32_t>(i * 64 + lane);
+        const int32_t e = static_cast<int32_t>(~wave_max(at));
+        double v = 0.0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e == i * 64 + lane) {
+                key[i] = 0;
+                v = s[i];
+            }
+        v = readlane64(v, e & 63);
+        total += v;
+        if (lane == j) {
+            mine = e;
+            weight = v;
+        }
+    }
+    if (lane < p.top) {
+        weight *= p.scale;
+        if (p.renormalize) weight /= total + 1e-20;
+        p.experts[out + lane] = mine;
+        p.weights[out + lane] = mine < 0 ? 0.0f : static_cast<float>(weight);
+    }
+}
+
+template <int V>
+__global__ __launch_bounds__(256) void route_kernel(RouteParams p)
+{
+    __shared__ double cs[4][64 * V];
+    const int lane = threadIdx.x & 63, wave = wave_index();
+    const int32_t t = blockIdx.x * 4 + wave;
+    if (t < p.T) route_token<V>(p, t, lane, cs[wave]);
+}
+
+// ---------------------------------------------------------------------------
+// The order of the slots
+// ---------------------------------------------------------------------------
+struct OrderParams {
+    const int32_t *experts;
+    int32_t *rows, *places, *offsets;
+    int32_t S, E;
+};
+
+// The lanes of a wave with the same key below 2^bits, as a mask.
+__device__ __forceinline__ uint64_t same_key(uint32_t key, int bits)
+{
+    uint64_t same = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot(key >> b & 1);
+        same &= key >> b & 1 ? set : ~set;
+    }
+    return same;
+}
+
+__global__ __launch_bounds__(1024) void order_kernel(OrderParams p)
+{
+    __shared__ int32_t base[MOST_EXPERTS + 1];   // next position of each expert
+    __shared__ uint16_t counts[16][MOST_EXPERTS + 1];
+    __shared__ int32_t sums[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+    const int32_t E = p.E;
+    for (int32_t e = tid; e <= E; e += 1024) base[e] = 0;
+    __syncthreads();
+    for (int32_t s = tid; s < p.S; s += 1024) {
+        const int32_t e = p.experts[s];
+        if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) atomicAdd(&base[e], 1);
+    }
+    __syncthreads();
+    const int32_t count = tid < E ? base[tid] : 0;
+    int32_t upto = count;
+    for (int d = 1; d < 64; d *= 2) {
+        const int32_t o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 63) sums[wave] = upto;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) upto += sums[w];
+    if (tid < E) {
+        base[tid] = upto - count;
+        p.offsets[tid] = upto - count;
+    }
+    int32_t all = 0;
+    for (int w = 0; w < 16; ++w) all += sums[w];
+    if (tid == 0) p.offsets[E] = all;
+    for (int32_t s = all + tid; s < p.S; s += 1024) p.rows[s] = -1;
+    const int bits = 32 - __builtin_clz(E);
+    for (int32_t s0 = 0; s0 < p.S; s0 += 1024) {
+        __syncthreads();
+        for (int32_t e = tid; e < 16 * (MOST_EXPERTS + 1); e += 1024) (&counts[0][0])[e] = 0;
+        __syncthreads();
+        const int32_t s = s0 + tid;
+        uint32_t e = static_cast<uint32_t>(E);
+        if (s < p.S) e = min(static_cast<uint32_t>(p.experts[s]), e);
+        const uint64_t same = same_key(e, bits);
+        const int before = __popcll(same & ((1ull << lane) - 1));
+        if (before == 0) counts[wave][e] = static_cast<uint16_t>(__popcll(same));
+        __syncthreads();
+        int32_t at = -1;
+        if (e < static_cast<uint32_t>(E)) {
+            at = base[e] + before;
+            for (int w = 0; w < wave; ++w) at += counts[w][e];
+            p.rows[at] = s;
+        }
+        if (s < p.S) p.places[s] = at;
+        __syncthreads();
+        if (tid < E)
+            for (int w = 0; w < 16; ++w) base[tid] += counts[w][tid];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The logits' gradient: one wave a token
+// ---------------------------------------------------------------------------
+struct RouteBackParams {
+    const void *logits;
+    const int32_t *experts;
+    const float *weights, *dweights;
+    void *dlogits;
+    double scale;
+    int32_t T, E, top;
+    bool f32, sigmoid, renormalize;
+};
+
+template <int V>
+__global__ __launch_bounds__(256) void route_back_kernel(RouteBackParams p)
+{
+    constexpr double inf = __builtin_huge_val();
+    const int lane = threadIdx.x & 63;
+    const int32_t t = blockIdx.x * 4 + wave_index();
+    if (t >= p.T) return;
+    double x[V], s[V], d[V];
+    const int64_t row = static_cast<int64_t>(t) * p.E;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int32_t e = i * 64 + lane;
+        x[i] = e < p.E ? load_logit(p.logits, p.f32, row + e) : -inf;
+    }
+    int32_t mine = -1;
+    double dw = 0.0;
+    bool bad = false;
+    if (lane < p.top) {
+        const int64_t at = static_cast<int64_t>(t) * p.top + lane;
+        mine = p.experts[at];
+        if (mine < 0 || mine >= p.E) mine = -1;
+        if (mine >= 0) dw = static_cast<double>(p.dweights[at]);
+        const float w = p.weights[at];
+        bad = !(w == w);
+    }
+    bool fine = scores_of(x, p.sigmoid, s) && !__any(bad);
+    // sums over the choices: of their scores, and of those times dw
+    double total = 0.0, inner = 0.0;
+    if (fine) {
+        for (int j = 0; j < p.top; ++j) {
+            const int32_t e = __builtin_amdgcn_readlane(mine, j);
+            if (e < 0) continue;
+            double v = 0.0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (e == i * 64 + lane) v = s[i];
+            v = readlane64(v, e & 63);
+            total += v;
+            inner += v * readlane64(dw, j);
+        }
+    }
+    total += 1e-20;
+    const double by = p.renormalize ? p.scale / total : p.scale;
+    const double less = p.renormalize ? inner / total : 0.0;
+    double dot = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = 0.0;
+    for (int j = 0; j < p.top; ++j) {
+        const int32_t e = __builtin_amdgcn_readlane(mine, j);
+        const double g = by * (readlane64(dw, j) - less);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e == i * 64 + lane) d[i] += g;
+    }
+    if (!p.sigmoid && fine) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) dot += d[i] * s[i];
+#pragma unroll
+        for (int k = 1; k < 64; k *= 2) dot += shfl_xor64(dot, k);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int32_t e = i * 64 + lane;
+        if (e >= p.E) continue;
+        double g;
+        if (!fine)
+            g = __builtin_nan("");
+        else if (x[i] == -inf)
+            g = 0.0;
+        else if (p.sigmoid)
+            g = d[i] == 0.0 ? 0.0 : d[i] * s[i] * (1.0 / (1.0 + exp(x[i])));
+        else
+            g = s[i] * (d[i] - dot);
+        if (p.f32)
+            static_cast<float *>(p.dlogits)[row + e] = static_cast<float>(g);
+        else
+            static_cast<_Float16 *>(p.dlogits)[row + e] = static_cast<_Float16>(g);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A token's rows together
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ half8_t load8(const _Float16 *row, int32_t c, int32_t cols)
+{
+    if (c + 8 <= cols) return *reinterpret_cast<const half8_u_t *>(row + c);
+    half8_t v = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < cols) v[i] = row[c + i];
+    return v;
+}
+
+__device__ __forceinline__ void store8(_Float16 *row, int32_t c, int32_t cols, half8_t v)
+{
+    if (c + 8 <= cols) {
+        *reinterpret_cast<half8_u_t *>(row + c) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < cols) row[c + i] = v[i];
+}
+
+struct CombineParams {
+    const _Float16 *y, *dout;
+    const float *weights;
+    const int32_t *rows, *places;
+    _Float16 *out;             // or dy
+    float *dweights;
+    int32_t T, top, N, S;
+    int32_t chunks;            // of 8 columns a row
+};
+
+__global__ __launch_bounds__(256) void combine_kernel(CombineParams p)
+{
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t t = id / p.chunks;
+    if (t >= p.T) return;
+    const int32_t c = static_cast<int32_t>(id - t * p.chunks) * 8;
+    float sum[8] = {};
+    for (int32_t j = 0; j < p.top; ++j) {
+        const int32_t place = p.places[t * p.top + j];
+        const float w = p.weights ? p.weights[t * p.top + j] : 1.0f;
+        half8_t v = {};
+        if (static_cast<uint32_t>(place) < static_cast<uint32_t>(p.S))
+            v = load8(p.y + static_cast<int64_t>(place) * p.N, c, p.N);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w, static_cast<float>(v[i]), sum[i]);
+    }
+    half8_t h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = static_cast<_Float16>(sum[i]);
+    store8(p.out + t * p.N, c, p.N, h);
+}
+
+// A workgroup a token: its slots' rows of dy and, where asked for, their inner
+// products; and zeros for the positions t * top .. that are no slot's.
+__global__ __launch_bounds__(256) void combine_back_kernel(CombineParams p)
+{
+    __shared__ float part[4][MOST_TOP];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = wave_index();
+    const _Float16 *dout = p.dout + t * p.N;
+    for (int32_t j = 0; j < p.top; ++j) {
+        const int32_t place = p.places[t * p.top + j];
+        const float w = p.weights ? p.weights[t * p.top + j] : 1.0f;
+        const bool in = static_cast<uint32_t>(place) < static_cast<uint32_t>(p.S);
+        float dot = 0.0f;
+        if (in)
+            for (int32_t c = threadIdx.x * 8; c < p.N; c += 2048) {
+                const half8_t d = load8(dout, c, p.N);
+                half8_t h;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] = static_cast<_Float16>(w * static_cast<float>(d[i]));
+                store8(p.out + static_cast<int64_t>(place) * p.N, c, p.N, h);
+                if (p.dweights) {
+                    const half8_t y = load8(p.y + static_cast<int64_t>(place) * p.N, c, p.N);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dot = __builtin_fmaf(static_cast<float>(d[i]), static_cast<float>(y[i]), dot);
+                }
+            }
+        if (p.dweights) {
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
+            if (lane == 0) part[wave][j] = dot;
+        }
+        const int64_t pos = t * p.top + j;
+        if (p.rows[pos] < 0)
+            for (int32_t c = threadIdx.x * 8; c < p.N; c += 2048) store8(p.out + pos * p.N, c, p.N, half8_t{});
+    }
+    if (!p.dweights) return;
+    __syncthreads();
+    if (static_cast<int32_t>(threadIdx.x) < p.top)
+        p.dweights[t * p.top + threadIdx.x] = part[0][threadIdx.x] + part[1][threadIdx.x] +
+                                              part[2][threadIdx.x] + part[3][threadIdx.x];
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Array {
+    const void *p;
+    int64_t bytes;
+    int64_t align;
+    bool written;
+};
+
+// NULL, alignment and overlap of a call's arrays (any with one that is written).
+static int check_arrays(const Array *arrays, int count)
+{
+    for (int i = 0; i < count; ++i)
+        if (arrays[i].bytes > 0 && !arrays[i].p) return GEMM_F16_INVALID_ARG;
+    for (int i = 0; i < count; ++i)
+        for (int j = 0; j < i; ++j) {
+            if (!(arrays[i].written || arrays[j].written)) continue;
+            if (arrays[i].bytes <= 0 || arrays[j].bytes <= 0) continue;
+            const uintptr_t a = reinterpret_cast<uintptr_t>(arrays[i].p);
+            const uintptr_t b = reinterpret_cast<uintptr_t>(arrays[j].p);
+            if (a < b + static_cast<uintptr_t>(arrays[j].bytes) &&
+                b < a + static_cast<uintptr_t>(arrays[i].bytes))
+                return GEMM_F16_INVALID_ARG;
+        }
+    for (int i = 0; i < count; ++i)
+        if (arrays[i].bytes > 0 && reinterpret_cast<uintptr_t>(arrays[i].p) % arrays[i].align != 0)
+            return GEMM_F16_UNSUPPORTED;
+    return GEMM_F16_OK;
+}
+
+static int launch(const void *fn, int64_t grid, int threads, void *params, hipStream_t stream)
+{
+    // the launch's own status only: the thread's sticky error state is neither
+    // read nor cleared
+    void *args[] = {params};
+    const hipError_t err = hipLaunchKernel(fn, dim3(static_cast<uint32_t>(grid)),
+                                           dim3(static_cast<uint32_t>(threads)), args, 0, stream);
+    return err == hipSuccess ? GEMM_F16_OK : GEMM_F16_LAUNCH_FAILED;
+}
+template <class K>
+static const void *address(K *kernel) { return reinterpret_cast<const void *>(kernel); }
+
+constexpr int64_t MOST_THREADS = int64_t(1) << 32;
+
+static int check_sizes(int64_t T, int64_t E, int32_t top)
+{
+    if (T < 0 || E < 1 || E > MOST_EXPERTS || top < 1 || top > MOST_TOP || top > E)
+        return GEMM_F16_INVALID_ARG;
+    return T > (INT32_MAX - 1023) / top ? GEMM_F16_INVALID_ARG : GEMM_F16_OK;
+}
+
+// The kernel for E experts: 64 V of them, V a power of two.
+template <template <int> class Of>
+static const void *by_experts(int64_t E)
+{
+    if (E <= 64) return Of<1>::get();
+    if (E <= 128) return Of<2>::get();
+    if (E <= 256) return Of<4>::get();
+    if (E <= 512) return Of<8>::get();
+    return Of<16>::get();
+}
+template <int V>
+struct RouteOf { static const void *get() { return address(route_kernel<V>); } };
+template <int V>
+struct RouteBackOf { static const void *get() { return address(route_back_kernel<V>); } };
+
+static int combine_sizes(int64_t T, int32_t top, int64_t N)
+{
+    if (T < 0 || N < 0 || top < 1 || top > MOST_TOP || T > (INT32_MAX - 1023) / top)
+        return GEMM_F16_INVALID_ARG;
+    return N > INT32_MAX - 7 ? GEMM_F16_UNSUPPORTED : GEMM_F16_OK;
+}
+
+}  // namespace gemm_f16_experts
+
+using namespace gemm_f16_experts;
+
+extern "C" int gemm_f16_route_workspace(int64_t T, int64_t E, int32_t top, int64_t *bytes)
+{
+    if (!bytes) return GEMM_F16_INVALID_ARG;
+    const int v = check_sizes(T, E, top);
+    if (v != GEMM_F16_OK) return v;
+    *bytes = 0;
+    return GEMM_F16_OK;
+}
+
+extern "C" int gemm_f16_route(int64_t T, int64_t E, int32_t top, int32_t scores, int32_t groups,
+                              int32_t top_groups, int32_t group_max, int32_t renormalize,
+                              double scale, const void *logits, int32_t logits_f32,
+                              const void *bias, void *experts, void *weights, void *rows,
+                              void *places, void *offsets, void *workspace,
+                              int64_t workspace_bytes, hipStream_t stream)
+{
+    int v = check_sizes(T, E, top);
+    if (v != GEMM_F16_OK) return v;
+    if ((scores != GEMM_F16_ROUTE_SOFTMAX && scores != GEMM_F16_ROUTE_SIGMOID) || groups < 1 ||
+        groups > MOST_GROUPS || E % groups != 0 || top_groups < 1 || top_groups > groups ||
+        workspace_bytes < 0)
+        return GEMM_F16_INVALID_ARG;
+    const int64_t S = T * top, width = logits_f32 ? 4 : 2;
+    const Array arrays[8] = {{logits, T * E * width, width, false},
+                             {bias, bias ? E * 4 : 0, 4, false},
+                             {experts, S * 4, 4, true},
+                             {weights, S * 4, 4, true},
+                             {rows, S * 4, 4, true},
+                             {places, S * 4, 4, true},
+                             {offsets, (E + 1) * 4, 4, true},
+                             {workspace, workspace ? workspace_bytes : 0, 256, true}};
+    v = check_arrays(arrays, 8);
+    if (v != GEMM_F16_OK) return v;
+    if (T > 0) {
+        RouteParams p;
+        p.logits = logits;
+        p.bias = static_cast<const float *>(bias);
+        p.experts = static_cast<int32_t *>(experts);
+        p.weights = static_cast<float *>(weights);
+        p.scale = scale;
+        p.T = static_cast<int32_t>(T);
+        p.E = static_cast<int32_t>(E);
+        p.top = top;
+        p.groups = groups;
+        p.top_groups = top_groups;
+        p.f32 = logits_f32 != 0;
+        p.sigmoid = scores == GEMM_F16_ROUTE_SIGMOID;
+        p.group_max = group_max != 0;
+        p.renormalize = renormalize != 0;
+        const int64_t grid = cdiv(T, 4);
+        if (grid * 256 >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
+        v = launch(by_experts<RouteOf>(E), grid, 256, &p, stream);
+        if (v != GEMM_F16_OK) return v;
+    }
+    OrderParams o;
+    o.experts = static_cast<const int32_t *>(experts);
+    o.rows = static_cast<int32_t *>(rows);
+    o.places = static_cast<int32_t *>(places);
+    o.offsets = static_cast<int32_t *>(offsets);
+    o.S = static_cast<int32_t>(S);
+    o.E = static_cast<int32_t>(E);
+    return launch(address(order_kernel), 1, 1024, &o, stream);
+}
+
+extern "C" int gemm_f16_route_backward(int64_t T, int64_t E, int32_t top, int32_t scores,
+                                       int32_t renormalize, double scale, const void *logits,
+                                       int32_t logits_f32, const void *experts,
+                                       const void *weights, const void *dweights, void *dlogits,
+                                       hipStream_t stream)
+{
+    int v = check_sizes(T, E, top);
+    if (v != GEMM_F16_OK) return v;
+    if (scores != GEMM_F16_ROUTE_SOFTMAX && scores != GEMM_F16_ROUTE_SIGMOID)
+        return GEMM_F16_INVALID_ARG;
+    const int64_t S = T * top, width = logits_f32 ? 4 : 2;
+    const Array arrays[5] = {{logits, T * E * width, width, false},
+                             {experts, S * 4, 4, false},
+                             {weights, S * 4, 4, false},
+                             {dweights, S * 4, 4, false},
+                             {dlogits, T * E * width, width, true}};
+    v = check_arrays(arrays, 5);
+    if (v != GEMM_F16_OK || T == 0) return v;
+    RouteBackParams p;
+    p.logits = logits;
+    p.experts = static_cast<const int32_t *>(experts);
+    p.weights = static_cast<const float *>(weights);
+    p.dweights = static_cast<const float *>(dweights);
+    p.dlogits = dlogits;
+    p.scale = scale;
+    p.T = static_cast<int32_t>(T);
+    p.E = static_cast<int32_t>(E);
+    p.top = top;
+    p.f32 = logits_f32 != 0;
+    p.sigmoid = scores == GEMM_F16_ROUTE_SIGMOID;
+    p.renormalize = renormalize != 0;
+    const int64_t grid = cdiv(T, 4);
+    if (grid * 256 >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
+    return launch(by_experts<RouteBackOf>(E), grid, 256, &p, stream);
+}
+
+extern "C" int gemm_f16_combine(int64_t T, int32_t top, int64_t N, const void *y,
+                                const void *weights, const void *places, void *out,
+                                hipStream_t stream)
+{
+    int v = combine_sizes(T, top, N);
+    if (v != GEMM_F16_OK) return v;
+    const int64_t S = T * top;
+    const Array arrays[4] = {{y, S * N * 2, 2, false},
+                             {weights, weights ? S * 4 : 0, 4, false},
+                             {places, S * 4, 4, false},
+                             {out, T * N * 2, 2, true}};
+    v = check_arrays(arrays, 4);
+    if (v != GEMM_F16_OK || T == 0 || N == 0) return v;
+    CombineParams p{};
+    p.y = static_cast<const _Float16 *>(y);
+    p.weights = static_cast<const float *>(weights);
+    p.places = static_cast<const int32_t *>(places);
+    p.out = static_cast<_Float16 *>(out);
+    p.T = static_cast<int32_t>(T);
+    p.top = top;
+    p.N = static_cast<int32_t>(N);
+    p.S = static_cast<int32_t>(S);
+    p.chunks = static_cast<int32_t>(cdiv(N, 8));
+    if (T > MOST_THREADS / p.chunks - 256) return GEMM_F16_UNSUPPORTED;
+    return launch(address(combine_kernel), cdiv(T * p.chunks, 256), 256, &p, stream);
+}
+
+extern "C" int gemm_f16_combine_backward(int64_t T, int32_t top, int64_t N, const void *dout,
+                                         const void *y, const void *weights, const void *rows,
+                                         const void *places, void *dy, void *dweights,
+                                         hipStream_t stream)
+{
+    int v = combine_sizes(T, top, N);
+    if (v != GEMM_F16_OK) return v;
+    const int64_t S = T * top;
+    const Array arrays[7] = {{dout, T * N * 2, 2, false},
+                             {y, dweights ? S * N * 2 : 0, 2, false},
+                             {weights, weights ? S * 4 : 0, 4, false},
+                             {rows, S * 4, 4, false},
+                             {places, S * 4, 4, false},
+                             {dy, S * N * 2, 2, true},
+                             {dweights, dweights ? S * 4 : 0, 4, true}};
+    v = check_arrays(arrays, 7);
+    if (v != GEMM_F16_OK || T == 0) return v;
+    if (T * 256 >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
+    CombineParams p{};
+    p.y = static_cast<const _Float16 *>(y);
+    p.dout = static_cast<const _Float16 *>(dout);
+    p.weights = static_cast<const float *>(weights);
+    p.rows = static_cast<const int32_t *>(rows);
+    p.places = static_cast<const int32_t *>(places);
+    p.out = static_cast<_Float16 *>(dy);
+    p.dweights = static_cast<float *>(dweights);
+    p.T = static_cast<int32_t>(T);
+    p.top = top;
+    p.N = static_cast<int32_t>(N);
+    p.S = static_cast<int32_t>(S);
+    return launch(address(combine_back_kernel), T, 256, &p, stream);
+}
