@@ -20,6 +20,14 @@ constexpr int MOST_EXPERTS = 1024, MOST_TOP = 32, MOST_GROUPS = 64;
 // The wave's index in its workgroup, in a scalar register.
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
+// This workgroup's unit of work, where each XCD (workgroups mod 8) takes a
+// contiguous range of them: neighbours share cache lines in its L2.
+__device__ __forceinline__ int32_t xcd_unit()
+{
+    const int32_t q = gridDim.x >> 3, rem = gridDim.x & 7, x = blockIdx.x & 7;
+    return x * q + (x < rem ? x : rem) + (blockIdx.x >> 3);
+}
+
 // Between a wave's LDS writes and its other lanes' reads of them: see that the
 // compiler keeps their order (a wave's LDS operations are done in order).
 __device__ __forceinline__ void wave_lds_fence()
@@ -122,7 +130,7 @@ __device__ __forceinline__ bool scores_of(const double (&x)[V], bool sigmoid, do
 }
 
 template <int V>
-__device__ __forceinline__ void route_token(const RouteParams &p, int32_t t, int lane, double *cs)
+__device__ __forceinline__ int32_t route_token(const RouteParams &p, int32_t t, int lane, double *cs)
 {
     constexpr double inf = __builtin_huge_val();
     double x[V], s[V], c[V];
@@ -150,7 +158,7 @@ __device__ __forceinline__ void route_token(const RouteParams &p, int32_t t, int
             p.experts[out + lane] = -1;
             p.weights[out + lane] = __builtin_nanf("");
         }
-        return;
+        return -1;
     }
     if (p.groups > 1) {
         const int32_t per = p.E / p.groups;
@@ -229,6 +237,7 @@ __device__ __forceinline__ void route_token(const RouteParams &p, int32_t t, int
         p.experts[out + lane] = mine;
         p.weights[out + lane] = mine < 0 ? 0.0f : static_cast<float>(weight);
     }
+    return mine;
 }
 
 template <int V>
@@ -241,12 +250,18 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p)
 }
 
 // ---------------------------------------------------------------------------
-// The order of the slots
+// The order of the slots: a stable counting sort
 // ---------------------------------------------------------------------------
+// A workgroup orders a chunk of the slots, 1024 at a time: a wave finds for each
+// slot how many of its lanes before it go to the same expert, the waves' counts
+// and the chunk's first position of each expert give the rest.  Where there are
+// several chunks their counts come from a kernel before.  49146 slots of 128
+// experts: 6 us and 4 us before it (one workgroup for all slots: 109 us).
 struct OrderParams {
     const int32_t *experts;
     int32_t *rows, *places, *offsets;
-    int32_t S, E;
+    int32_t *counts;                 // [chunk][expert]; unused for one chunk
+    int32_t S, E, chunks, chunk;     // slots of a chunk: a multiple of 1024
 };
 
 // The lanes of a wave with the same key below 2^bits, as a mask.
@@ -260,60 +275,145 @@ __device__ __forceinline__ uint64_t same_key(uint32_t key, int bits)
     return same;
 }
 
-__global__ __launch_bounds__(1024) void order_kernel(OrderParams p)
+// An expert's index, E for none.
+__device__ __forceinline__ uint32_t expert_of(int32_t e, int32_t E)
 {
-    __shared__ int32_t base[MOST_EXPERTS + 1];   // next position of each expert
-    __shared__ uint16_t counts[16][MOST_EXPERTS + 1];
-    __shared__ int32_t sums[16];
-    const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
-    const int32_t E = p.E;
-    for (int32_t e = tid; e <= E; e += 1024) base[e] = 0;
+    return min(static_cast<uint32_t>(e), static_cast<uint32_t>(E));
+}
+
+__global__ __launch_bounds__(1024) void count_kernel(OrderParams p)
+{
+    __shared__ int32_t count[MOST_EXPERTS + 1];
+    const int tid = threadIdx.x;
+    const int32_t from = blockIdx.x * p.chunk, to = from + min(p.S - from, p.chunk);
+    if (tid < p.E) count[tid] = 0;
     __syncthreads();
-    for (int32_t s = tid; s < p.S; s += 1024) {
-        const int32_t e = p.experts[s];
-        if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) atomicAdd(&base[e], 1);
+    for (int32_t s = from + tid; s < to; s += 1024) {
+        const uint32_t e = expert_of(p.experts[s], p.E);
+        if (e < static_cast<uint32_t>(p.E)) atomicAdd(&count[e], 1);
     }
     __syncthreads();
-    const int32_t count = tid < E ? base[tid] : 0;
+    if (tid < p.E) p.counts[static_cast<int64_t>(blockIdx.x) * p.E + tid] = count[tid];
+}
+
+struct OrderMemory {
+    int32_t base[MOST_EXPERTS + 1];      // next position of each expert
+    int32_t parts[2][1024];
+    uint16_t counts[16 * (MOST_EXPERTS + 1)];
+    int32_t sums[16];
+};
+
+// Chunk `c`'s slots by a workgroup of 16 waves; ONE: the only one, and its slots'
+// experts, at most 1024, are in `mine` by thread.
+template <bool ONE>
+__device__ __forceinline__ void order_chunk(const OrderParams &p, int32_t c, int32_t mine, OrderMemory &m)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+    const int32_t E = p.E, from = c * p.chunk, to = from + min(p.S - from, p.chunk);
+    int32_t count = 0, before = 0;       // of expert `tid`: all slots, those of the chunks before
+    if (ONE || p.chunks == 1) {
+        if (tid < E) m.base[tid] = 0;
+        __syncthreads();
+        for (int32_t s = from + tid; s < to; s += 1024) {
+            const uint32_t e = expert_of(ONE ? mine : p.experts[s], E);
+            if (e < static_cast<uint32_t>(E)) atomicAdd(&m.base[e], 1);
+        }
+        __syncthreads();
+        if (tid < E) count = m.base[tid];
+    } else {
+        // 1024 / E threads an expert, each every so many chunks
+        const int32_t share = 1024 / E, e = tid % E, part = tid / E;
+        if (part < share)
+#pragma unroll 8
+            for (int32_t i = part; i < p.chunks; i += share) {
+                const int32_t n = p.counts[static_cast<int64_t>(i) * E + e];
+                count += n;
+                before += i < c ? n : 0;
+            }
+        m.parts[0][tid] = count;
+        m.parts[1][tid] = before;
+        __syncthreads();
+        count = before = 0;
+        if (tid < E)
+            for (int32_t i = 0; i < share; ++i) {
+                count += m.parts[0][i * E + tid];
+                before += m.parts[1][i * E + tid];
+            }
+    }
     int32_t upto = count;
+#pragma unroll
     for (int d = 1; d < 64; d *= 2) {
         const int32_t o = __shfl_up(upto, d);
         if (lane >= d) upto += o;
     }
-    if (lane == 63) sums[wave] = upto;
+    if (lane == 63) m.sums[wave] = upto;
     __syncthreads();
-    for (int w = 0; w < wave; ++w) upto += sums[w];
-    if (tid < E) {
-        base[tid] = upto - count;
-        p.offsets[tid] = upto - count;
-    }
     int32_t all = 0;
-    for (int w = 0; w < 16; ++w) all += sums[w];
-    if (tid == 0) p.offsets[E] = all;
-    for (int32_t s = all + tid; s < p.S; s += 1024) p.rows[s] = -1;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        const int32_t n = m.sums[w];
+        if (w < wave) upto += n;
+        all += n;
+    }
+    if (tid < E) {
+        m.base[tid] = upto - count + before;
+        if (c == 0) p.offsets[tid] = upto - count;
+    }
+    if (c == 0 && tid == 0) p.offsets[E] = all;
     const int bits = 32 - __builtin_clz(E);
-    for (int32_t s0 = 0; s0 < p.S; s0 += 1024) {
-        __syncthreads();
-        for (int32_t e = tid; e < 16 * (MOST_EXPERTS + 1); e += 1024) (&counts[0][0])[e] = 0;
+    for (int32_t s0 = from; s0 < to; s0 += 1024) {
+        for (int32_t e = tid; e < 16 * (E + 1); e += 1024) m.counts[e] = 0;
         __syncthreads();
         const int32_t s = s0 + tid;
         uint32_t e = static_cast<uint32_t>(E);
-        if (s < p.S) e = min(static_cast<uint32_t>(p.experts[s]), e);
+        if (s < to) e = expert_of(ONE ? mine : p.experts[s], E);
         const uint64_t same = same_key(e, bits);
-        const int before = __popcll(same & ((1ull << lane) - 1));
-        if (before == 0) counts[wave][e] = static_cast<uint16_t>(__popcll(same));
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        if (rank == 0) m.counts[wave * (E + 1) + e] = static_cast<uint16_t>(__popcll(same));
         __syncthreads();
         int32_t at = -1;
         if (e < static_cast<uint32_t>(E)) {
-            at = base[e] + before;
-            for (int w = 0; w < wave; ++w) at += counts[w][e];
+            at = m.base[e] + rank;
+            for (int w = 0; w < wave; ++w) at += m.counts[w * (E + 1) + e];
             p.rows[at] = s;
         }
-        if (s < p.S) p.places[s] = at;
+        if (s < to) {
+            p.places[s] = at;
+            if (s >= all) p.rows[s] = -1;
+        }
+        if (s0 + 1024 >= to) break;
         __syncthreads();
         if (tid < E)
-            for (int w = 0; w < 16; ++w) base[tid] += counts[w][tid];
+            for (int w = 0; w < 16; ++w) m.base[tid] += m.counts[w * (E + 1) + tid];
+        __syncthreads();
     }
+}
+
+__global__ __launch_bounds__(1024) void order_kernel(OrderParams p)
+{
+    __shared__ OrderMemory m;
+    order_chunk<false>(p, blockIdx.x, 0, m);
+}
+
+// Up to 16 tokens: their choice, a wave each, and the order in one launch.
+constexpr int FEW = 16;
+
+template <int V>
+__global__ __launch_bounds__(1024) void route_few_kernel(RouteParams p, OrderParams o)
+{
+    __shared__ union {
+        double cs[FEW][64 * V];
+        OrderMemory m;
+    } u;
+    __shared__ int32_t chosen[FEW * MOST_TOP];
+    const int lane = threadIdx.x & 63, wave = wave_index();
+    if (wave < p.T) {
+        const int32_t e = route_token<V>(p, wave, lane, u.cs[wave]);
+        if (lane < p.top) chosen[wave * p.top + lane] = e;
+    }
+    __syncthreads();
+    const int tid = threadIdx.x;
+    order_chunk<true>(o, 0, tid < o.S ? chosen[tid] : -1, u.m);
 }
 
 // ---------------------------------------------------------------------------
@@ -440,24 +540,39 @@ struct CombineParams {
     _Float16 *out;             // or dy
     float *dweights;
     int32_t T, top, N, S;
-    int32_t chunks;            // of 8 columns a row
+    int32_t chunks;            // of 512 columns a row
 };
+
+// A wave takes 512 columns of a token: places and weights are scalars, and the
+// rows of eight choices are on their way at once.
+constexpr int AT_ONCE = 8;
 
 __global__ __launch_bounds__(256) void combine_kernel(CombineParams p)
 {
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t t = id / p.chunks;
+    const int32_t unit = blockIdx.x * 4 + wave_index();   // below 2^26
+    const int64_t t = unit / p.chunks;
     if (t >= p.T) return;
-    const int32_t c = static_cast<int32_t>(id - t * p.chunks) * 8;
+    const int32_t c = (unit - static_cast<int32_t>(t) * p.chunks) * 512 + (threadIdx.x & 63) * 8;
+    if (c >= p.N) return;
+    const int32_t *places = p.places + t * p.top;
+    const float *weights = p.weights + t * p.top;
     float sum[8] = {};
-    for (int32_t j = 0; j < p.top; ++j) {
-        const int32_t place = p.places[t * p.top + j];
-        const float w = p.weights ? p.weights[t * p.top + j] : 1.0f;
-        half8_t v = {};
-        if (static_cast<uint32_t>(place) < static_cast<uint32_t>(p.S))
-            v = load8(p.y + static_cast<int64_t>(place) * p.N, c, p.N);
+    for (int32_t j0 = 0; j0 < p.top; j0 += AT_ONCE) {
+        half8_t v[AT_ONCE] = {};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w, static_cast<float>(v[i]), sum[i]);
+        for (int j = 0; j < AT_ONCE; ++j) {
+            if (j0 + j >= p.top) break;
+            const int32_t place = places[j0 + j];
+            if (static_cast<uint32_t>(place) < static_cast<uint32_t>(p.S))
+                v[j] = load8(p.y + static_cast<int64_t>(place) * p.N, c, p.N);
+        }
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j) {
+            if (j0 + j >= p.top) break;
+            const float w = p.weights ? weights[j0 + j] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w, static_cast<float>(v[j][i]), sum[i]);
+        }
     }
     half8_t h;
 #pragma unroll
@@ -465,47 +580,53 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineParams p)
     store8(p.out + t * p.N, c, p.N, h);
 }
 
-// A workgroup a token: its slots' rows of dy and, where asked for, their inner
-// products; and zeros for the positions t * top .. that are no slot's.
+// A wave a slot: its row of dy, its inner product, and zeros for the position of
+// the slot's number where that is no slot's.  Four times 512 columns are on their
+// way at once; the waves of a token read dout from its XCD's L2.
 __global__ __launch_bounds__(256) void combine_back_kernel(CombineParams p)
 {
-    __shared__ float part[4][MOST_TOP];
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = wave_index();
-    const _Float16 *dout = p.dout + t * p.N;
-    for (int32_t j = 0; j < p.top; ++j) {
-        const int32_t place = p.places[t * p.top + j];
-        const float w = p.weights ? p.weights[t * p.top + j] : 1.0f;
-        const bool in = static_cast<uint32_t>(place) < static_cast<uint32_t>(p.S);
-        float dot = 0.0f;
-        if (in)
-            for (int32_t c = threadIdx.x * 8; c < p.N; c += 2048) {
-                const half8_t d = load8(dout, c, p.N);
+    constexpr int U = 4;
+    const int32_t unit = xcd_unit() * 4 + wave_index();
+    if (unit >= p.S) return;
+    const int64_t slot = unit;
+    const int lane = threadIdx.x & 63;
+    const int32_t place = p.places[slot];
+    const bool in = static_cast<uint32_t>(place) < static_cast<uint32_t>(p.S);
+    const float w = p.weights ? p.weights[slot] : 1.0f;
+    float dot = 0.0f;
+    if (in) {
+        const _Float16 *dout = p.dout + static_cast<int64_t>(unit / p.top) * p.N;
+        const _Float16 *y = p.y + static_cast<int64_t>(place) * p.N;
+        _Float16 *dy = p.out + static_cast<int64_t>(place) * p.N;
+        for (int32_t c0 = lane * 8; c0 < p.N; c0 += U * 512) {
+            half8_t d[U], v[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (c0 + k * 512 < p.N) {
+                    d[k] = load8(dout, c0 + k * 512, p.N);
+                    if (p.dweights) v[k] = load8(y, c0 + k * 512, p.N);
+                }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (c0 + k * 512 >= p.N) break;
                 half8_t h;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] = static_cast<_Float16>(w * static_cast<float>(d[i]));
-                store8(p.out + static_cast<int64_t>(place) * p.N, c, p.N, h);
-                if (p.dweights) {
-                    const half8_t y = load8(p.y + static_cast<int64_t>(place) * p.N, c, p.N);
+                for (int i = 0; i < 8; ++i) h[i] = static_cast<_Float16>(w * static_cast<float>(d[k][i]));
+                store8(dy, c0 + k * 512, p.N, h);
+                if (p.dweights)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        dot = __builtin_fmaf(static_cast<float>(d[i]), static_cast<float>(y[i]), dot);
-                }
+                        dot = __builtin_fmaf(static_cast<float>(d[k][i]), static_cast<float>(v[k][i]), dot);
             }
-        if (p.dweights) {
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
-            if (lane == 0) part[wave][j] = dot;
         }
-        const int64_t pos = t * p.top + j;
-        if (p.rows[pos] < 0)
-            for (int32_t c = threadIdx.x * 8; c < p.N; c += 2048) store8(p.out + pos * p.N, c, p.N, half8_t{});
     }
-    if (!p.dweights) return;
-    __syncthreads();
-    if (static_cast<int32_t>(threadIdx.x) < p.top)
-        p.dweights[t * p.top + threadIdx.x] = part[0][threadIdx.x] + part[1][threadIdx.x] +
-                                              part[2][threadIdx.x] + part[3][threadIdx.x];
+    if (p.dweights) {
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
+        if (lane == 0) p.dweights[slot] = dot;
+    }
+    if (p.rows[slot] < 0)
+        for (int32_t c = lane * 8; c < p.N; c += 512) store8(p.out + slot * p.N, c, p.N, half8_t{});
 }
 
 // ---------------------------------------------------------------------------
@@ -541,11 +662,12 @@ static int check_arrays(const Array *arrays, int count)
     return GEMM_F16_OK;
 }
 
-static int launch(const void *fn, int64_t grid, int threads, void *params, hipStream_t stream)
+static int launch(const void *fn, int64_t grid, int threads, void *params, hipStream_t stream,
+                  void *more = nullptr)
 {
     // the launch's own status only: the thread's sticky error state is neither
     // read nor cleared
-    void *args[] = {params};
+    void *args[] = {params, more};
     const hipError_t err = hipLaunchKernel(fn, dim3(static_cast<uint32_t>(grid)),
                                            dim3(static_cast<uint32_t>(threads)), args, 0, stream);
     return err == hipSuccess ? GEMM_F16_OK : GEMM_F16_LAUNCH_FAILED;
@@ -573,9 +695,31 @@ static const void *by_experts(int64_t E)
     return Of<16>::get();
 }
 template <int V>
+struct RouteFewOf {
+    static const void *get()
+    {
+        // more scores than that leave too few registers to 16 waves
+        if constexpr (V <= 8) return address(route_few_kernel<V>);
+        return nullptr;
+    }
+};
+template <int V>
 struct RouteOf { static const void *get() { return address(route_kernel<V>); } };
 template <int V>
 struct RouteBackOf { static const void *get() { return address(route_back_kernel<V>); } };
+
+// The chunks of S slots, and the bytes of their counts.  Up to 2048 slots in one:
+// two passes of a workgroup cost less than a second launch.  No more than 256, whose
+// counts every workgroup reads.
+static int64_t order_chunks(int64_t S, int64_t E, OrderParams *o)
+{
+    const int64_t chunk = S <= 2048 ? 2048 : cdiv(cdiv(S, 256), 1024) * 1024;
+    o->S = static_cast<int32_t>(S);
+    o->E = static_cast<int32_t>(E);
+    o->chunk = static_cast<int32_t>(chunk);
+    o->chunks = static_cast<int32_t>(std::max<int64_t>(cdiv(S, chunk), 1));
+    return o->chunks > 1 ? o->chunks * E * 4 : 0;
+}
 
 static int combine_sizes(int64_t T, int32_t top, int64_t N)
 {
@@ -593,7 +737,8 @@ extern "C" int gemm_f16_route_workspace(int64_t T, int64_t E, int32_t top, int64
     if (!bytes) return GEMM_F16_INVALID_ARG;
     const int v = check_sizes(T, E, top);
     if (v != GEMM_F16_OK) return v;
-    *bytes = 0;
+    OrderParams o;
+    *bytes = order_chunks(T * top, E, &o);
     return GEMM_F16_OK;
 }
 
@@ -621,35 +766,35 @@ extern "C" int gemm_f16_route(int64_t T, int64_t E, int32_t top, int32_t scores,
                              {workspace, workspace ? workspace_bytes : 0, 256, true}};
     v = check_arrays(arrays, 8);
     if (v != GEMM_F16_OK) return v;
-    if (T > 0) {
-        RouteParams p;
-        p.logits = logits;
-        p.bias = static_cast<const float *>(bias);
-        p.experts = static_cast<int32_t *>(experts);
-        p.weights = static_cast<float *>(weights);
-        p.scale = scale;
-        p.T = static_cast<int32_t>(T);
-        p.E = static_cast<int32_t>(E);
-        p.top = top;
-        p.groups = groups;
-        p.top_groups = top_groups;
-        p.f32 = logits_f32 != 0;
-        p.sigmoid = scores == GEMM_F16_ROUTE_SIGMOID;
-        p.group_max = group_max != 0;
-        p.renormalize = renormalize != 0;
-        const int64_t grid = cdiv(T, 4);
-        if (grid * 256 >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
-        v = launch(by_experts<RouteOf>(E), grid, 256, &p, stream);
-        if (v != GEMM_F16_OK) return v;
-    }
     OrderParams o;
+    const int64_t need = order_chunks(S, E, &o);
+    if (need > (workspace ? workspace_bytes : 0)) return GEMM_F16_INVALID_ARG;
     o.experts = static_cast<const int32_t *>(experts);
     o.rows = static_cast<int32_t *>(rows);
     o.places = static_cast<int32_t *>(places);
     o.offsets = static_cast<int32_t *>(offsets);
-    o.S = static_cast<int32_t>(S);
-    o.E = static_cast<int32_t>(E);
-    return launch(address(order_kernel), 1, 1024, &o, stream);
+    o.counts = static_cast<int32_t *>(workspace);
+    RouteParams p;
+    p.logits = logits;
+    p.bias = static_cast<const float *>(bias);
+    p.experts = static_cast<int32_t *>(experts);
+    p.weights = static_cast<float *>(weights);
+    p.scale = scale;
+    p.T = static_cast<int32_t>(T);
+    p.E = static_cast<int32_t>(E);
+    p.top = top;
+    p.groups = groups;
+    p.top_groups = top_groups;
+    p.f32 = logits_f32 != 0;
+    p.sigmoid = scores == GEMM_F16_ROUTE_SIGMOID;
+    p.group_max = group_max != 0;
+    p.renormalize = renormalize != 0;
+    if (T <= FEW && E <= 512) return launch(by_experts<RouteFewOf>(E), 1, 1024, &p, stream, &o);
+    const int64_t grid = cdiv(T, 4);
+    if (grid * 256 >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
+    if (T > 0) v = launch(by_experts<RouteOf>(E), grid, 256, &p, stream);
+    if (v == GEMM_F16_OK && o.chunks > 1) v = launch(address(count_kernel), o.chunks, 1024, &o, stream);
+    return v != GEMM_F16_OK ? v : launch(address(order_kernel), o.chunks, 1024, &o, stream);
 }
 
 extern "C" int gemm_f16_route_backward(int64_t T, int64_t E, int32_t top, int32_t scores,
@@ -710,9 +855,9 @@ extern "C" int gemm_f16_combine(int64_t T, int32_t top, int64_t N, const void *y
     p.top = top;
     p.N = static_cast<int32_t>(N);
     p.S = static_cast<int32_t>(S);
-    p.chunks = static_cast<int32_t>(cdiv(N, 8));
-    if (T > MOST_THREADS / p.chunks - 256) return GEMM_F16_UNSUPPORTED;
-    return launch(address(combine_kernel), cdiv(T * p.chunks, 256), 256, &p, stream);
+    p.chunks = static_cast<int32_t>(cdiv(N, 512));
+    if (T > MOST_THREADS / 64 / p.chunks - 4) return GEMM_F16_UNSUPPORTED;
+    return launch(address(combine_kernel), cdiv(T * p.chunks, 4), 256, &p, stream);
 }
 
 extern "C" int gemm_f16_combine_backward(int64_t T, int32_t top, int64_t N, const void *dout,
@@ -732,7 +877,7 @@ extern "C" int gemm_f16_combine_backward(int64_t T, int32_t top, int64_t N, cons
                              {dweights, dweights ? S * 4 : 0, 4, true}};
     v = check_arrays(arrays, 7);
     if (v != GEMM_F16_OK || T == 0) return v;
-    if (T * 256 >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
+    if (S + 3 >= MOST_THREADS / 64) return GEMM_F16_UNSUPPORTED;
     CombineParams p{};
     p.y = static_cast<const _Float16 *>(y);
     p.dout = static_cast<const _Float16 *>(dout);
@@ -745,5 +890,5 @@ extern "C" int gemm_f16_combine_backward(int64_t T, int32_t top, int64_t N, cons
     p.top = top;
     p.N = static_cast<int32_t>(N);
     p.S = static_cast<int32_t>(S);
-    return launch(address(combine_back_kernel), T, 256, &p, stream);
+    return launch(address(combine_back_kernel), cdiv(S, 4), 256, &p, stream);
 }

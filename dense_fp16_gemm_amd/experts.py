@@ -214,6 +214,10 @@ def _logits(x):
         _refuse(x, x.dtype, "logits")
 
 
+# workspace bytes of route() by (tokens, experts, top)
+_route_bytes: dict = {}
+
+
 def route(logits, top: int, scores: str = "softmax", bias=None, groups: int = 1,
           top_groups: int = 1, group_score: str = "top2", renormalize: bool = True,
           scale: float = 1.0, stream=None) -> Routing:
@@ -249,7 +253,12 @@ def route(logits, top: int, scores: str = "softmax", bias=None, groups: int = 1,
     experts, weights, rows, places, offsets = memory.split((slots, slots, slots, slots, e + 1))
     experts, places = experts.view(t, top), places.view(t, top)
     weights = weights.view(_f32).view(t, top)
-    need = gemm_f16_route_workspace(t, e, top)
+    key = (t, e, top)
+    need = _route_bytes.get(key)
+    if need is None:
+        if len(_route_bytes) >= 1024:
+            _route_bytes.clear()
+        need = _route_bytes[key] = gemm_f16_route_workspace(t, e, top)
     ws = _new(logits, stream, (need,), _uint8) if need else None
     _call(index, stream, _lib.gemm_f16_route, t, e, top, ROUTE_SCORES[scores], groups, top_groups,
           group_score == "max", bool(renormalize), scale, logits.data_ptr(),
