@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -12,6 +13,7 @@
 
 namespace gemm_f16_f8 {
 
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 // 16 (8) bytes at any 2-byte alignment (the target's unaligned-access mode)
@@ -19,6 +21,7 @@ typedef _Float16 half8_u_t __attribute__((ext_vector_type(8), aligned(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
+typedef int16_t i16x2_t __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
@@ -211,9 +214,7 @@ __device__ __forceinline__ void columns8(const u32x4_t (&v)[8], u16x2_t (&m)[4])
     }
 }
 
-// Where position p's range of an experts' order lies, found by a whole wave:
-// the expert with the id-th unit, units being ceil(rows / size) an expert.
-// Returns the expert, or -1 and the units left over in `id`.
+// What an expert has of some units of work: ceil(rows / size) times `per`.
 struct Found {
     int32_t e;        // expert, -1: past the last
     int32_t index;    // which of its units (or of those past the last)
@@ -230,17 +231,42 @@ __device__ __forceinline__ int32_t inclusive_scan(int32_t v, int lane)
     return v;
 }
 
-__device__ __forceinline__ Found find_unit(const int32_t *offsets, int32_t E, int32_t S, int32_t size,
-                                           int32_t id, int lane)
+// The positions of expert e, held to 0 .. S whatever `offsets` says.
+__device__ __forceinline__ void positions(const int32_t *offsets, int32_t E, int32_t S, int32_t e,
+                                          int32_t &lo, int32_t &hi)
 {
-    for (int32_t c = 0; c < E; c += 64) {
-        int32_t lo = 0, hi = 0;
-        if (c + lane < E) {
-            lo = min(max(offsets[c + lane], 0), S);
-            hi = max(min(max(offsets[c + lane + 1], 0), S), lo);
+    lo = hi = 0;
+    if (e < E) {
+        lo = min(max(offsets[e], 0), S);
+        hi = max(min(max(offsets[e + 1], 0), S), lo);
+    }
+}
+
+// The expert that unit `id` of all experts' belongs to, found by a whole wave, 64
+// experts at a time.  PER_XCD: `id` counts workgroups, and each XCD (workgroups
+// mod 8) takes a contiguous range of the units that there are, the rows of no
+// expert (ceil(rows / size) times per, too) last.
+template <bool PER_XCD>
+__device__ __forceinline__ Found find_unit(const int32_t *offsets, int32_t E, int32_t S, int32_t size,
+                                           int32_t per, int32_t id, int lane)
+{
+    int32_t lo, hi;
+    positions(offsets, E, S, lane, lo, hi);
+    int32_t units = (hi - lo + size - 1) / size * per;
+    int32_t upto = inclusive_scan(units, lane);
+    const int32_t end = __builtin_amdgcn_readfirstlane(min(max(offsets[E], 0), S));
+    if constexpr (PER_XCD) {
+        int32_t total = __builtin_amdgcn_readlane(upto, 63) + (S - end + size - 1) / size * per;
+        for (int32_t c = 64; c < E; c += 64) {
+            int32_t l, h;
+            positions(offsets, E, S, c + lane, l, h);
+            total += __builtin_amdgcn_readlane(inclusive_scan((h - l + size - 1) / size * per, lane), 63);
         }
-        const int32_t units = (hi - lo + size - 1) / size;
-        const int32_t upto = inclusive_scan(units, lane);
+        const int32_t x = id & 7, i = id >> 3, q = total >> 3, rem = total & 7;
+        if (i >= q + (x < rem ? 1 : 0)) return Found{-1, 0, S, S};
+        id = x * q + min(x, rem) + i;
+    }
+    for (int32_t c = 0;;) {
         const int32_t all = __builtin_amdgcn_readlane(upto, 63);
         if (id < all) {
             const int l = __builtin_ctzll(__ballot(upto > id));
@@ -252,8 +278,13 @@ __device__ __forceinline__ Found find_unit(const int32_t *offsets, int32_t E, in
             return f;
         }
         id -= all;
+        c += 64;
+        if (c >= E) break;
+        positions(offsets, E, S, c + lane, lo, hi);
+        units = (hi - lo + size - 1) / size * per;
+        upto = inclusive_scan(units, lane);
     }
-    return Found{-1, id, __builtin_amdgcn_readfirstlane(min(max(offsets[E], 0), S)), S};
+    return Found{-1, id, end, S};
 }
 
 // BLOCK: one scale for all values.  TRANSPOSED: stored the other way round.
@@ -275,17 +306,20 @@ __global__ __launch_bounds__(256) void f8_square_kernel(SquareParams p)
     const int32_t c0 = tc * 128 + tx * 8;
     u32x4_t v[8];
     if constexpr (EXPERTS) {
-        const Found f = find_unit(p.offsets, p.E, p.XR, 128, tr, lane);
+        const Found f = find_unit<false>(p.offsets, p.E, p.XR, 128, 1, tr, lane);
         if (f.e < 0) return;
+        const int32_t pos = f.lo + f.index * 128 + ty * 8;
+        int32_t row[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int32_t pos = f.lo + f.index * 128 + ty * 8 + i;
-            v[i] = u32x4_t{0, 0, 0, 0};
-            if (pos < f.hi) {
-                int64_t row = pos;
-                if (p.top > 0) row = min(max(p.rows[pos], 0), p.XR - 1) / p.top;
-                v[i] = load8(X + row * p.XC, c0, p.XC);
-            }
+            row[i] = min(pos + i, f.hi - 1);
+            if (p.top > 0) row[i] = min(max(p.rows[row[i]], 0), p.XR - 1) / p.top;
+        }
+        // rows past the expert's last are read as that one, then dropped
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = load8(X + static_cast<int64_t>(row[i]) * p.XC, c0, p.XC);
+            if (pos + i >= f.hi) v[i] = u32x4_t{0, 0, 0, 0};
         }
     } else {
         const int32_t r0 = tr * 128 + ty * 8;
@@ -441,28 +475,37 @@ __global__ __launch_bounds__(256) void f8_decode_kernel(DecodeParams p)
 // ---------------------------------------------------------------------------
 enum { DENSE = 0, EXPERTS = 1, GRAD = 2 };
 
+// A scale of each operand for its row comes from the lane that holds the row, so
+// any order of a group's columns in the lanes' registers is right that is the
+// same for both operands.
 struct Params {
     const uint8_t *a, *b;
+    const uint16_t *x;          // A in fp16, quantised by the kernel
     const uint32_t *as, *bs;    // four scales of a row (block) a dword
     uint16_t *c;
     const int32_t *rows, *offsets;
     int64_t a_ld, b_ld;         // bytes a row
-    int32_t M, N;               // rows and columns of C (one matrix of it)
+    int32_t M, N, K;            // rows and columns of C (one matrix of it), columns of A
     int32_t kb;                 // groups of 128 columns
     int32_t a_rows;             // rows of A
     int32_t b_blocks, b_shift;  // blocks of rows of B, log2 of their size
     int32_t E, top;
     int32_t tiles_m, tiles_n;
+    int32_t splits, kb_split;   // ranges of K (dense), groups of each
+    float *partial;             // their sums
 };
 
-// A scale of each operand for its row comes from the lane that holds the row,
-// so any order of the 128 columns in the lanes' registers is right that is the
-// same for both.
-__device__ __forceinline__ i32x8_t load_codes(const uint8_t *row, int kq)
+// Four neighbouring columns of a row of C.
+__device__ __forceinline__ void store4(uint16_t *row, int32_t n, int32_t N, f32x4_t v)
 {
-    const i32x4_t lo = *reinterpret_cast<const i32x4_t *>(row + kq * 16);
-    const i32x4_t hi = *reinterpret_cast<const i32x4_t *>(row + 64 + kq * 16);
-    return i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    const half4_t h = __builtin_convertvector(v, half4_t);
+    if (n + 4 <= N) {
+        __builtin_memcpy(row + n, &h, 8);   // any 2-byte alignment
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (n + e < N) row[n + e] = bits_as<uint16_t>(_Float16(h[e]));
 }
 
 // A workgroup's part of C and of K.
@@ -470,37 +513,62 @@ struct Unit {
     int64_t matrix;             // of B (experts' products) and of C (gradients)
     int32_t m0, m1, n0;         // rows of C, its first column
     int32_t kb0, kb1;           // groups of 128 columns
+    int32_t split, tile;        // which range of K, which tile of C
     bool none;
 };
 
+// Tile `tile` of tiles_m x tiles_n: neighbours (which share an XCD's L2) are tiles
+// of a few rows of tiles at a time, one column after the other.
+constexpr int32_t RASTER = 8;
+
+__device__ __forceinline__ void find_tile(int32_t tile, int32_t tiles_m, int32_t tiles_n, int32_t &tm, int32_t &tn)
+{
+    if (tiles_m == 1) {
+        tm = 0;
+        tn = tile;
+        return;
+    }
+    const int32_t group = tile / (RASTER * tiles_n), first = group * RASTER;
+    const int32_t height = min(RASTER, tiles_m - first), rest = tile - group * RASTER * tiles_n;
+    tm = first + rest % height;
+    tn = rest / height;
+}
+
 template <int MODE, int BM, int BN>
-__device__ __forceinline__ Unit make_unit(const Params &p, int32_t unit, int lane)
+__device__ __forceinline__ Unit make_unit(const Params &p, int lane)
 {
     Unit u;
     u.none = false;
     u.matrix = 0;
     u.kb0 = 0;
     u.kb1 = p.kb;
+    int32_t tm, tn;
     if constexpr (MODE == EXPERTS) {
-        u.n0 = unit % p.tiles_n * BN;
-        const Found f = find_unit(p.offsets, p.E, p.M, BM, unit / p.tiles_n, lane);
-        u.m0 = f.lo + f.index * BM;
+        const Found f = find_unit<true>(p.offsets, p.E, p.M, BM, p.tiles_n, blockIdx.x, lane);
+        const int32_t tiles = max((f.hi - f.lo + BM - 1) / BM, 1);
+        tm = f.index % tiles;
+        tn = f.index / tiles;
+        u.m0 = f.lo + tm * BM;
         u.m1 = min(f.hi, u.m0 + BM);
-        u.none = u.m0 >= f.hi;
+        u.none = f.lo >= f.hi;
         if (f.e < 0) u.kb1 = 0;
         u.matrix = max(f.e, 0);
     } else {
-        u.n0 = unit % p.tiles_n * BN;
-        unit /= p.tiles_n;
-        u.m0 = unit % p.tiles_m * BM;
-        u.m1 = min(p.M, u.m0 + BM);
+        int32_t unit = xcd_unit();
+        if (MODE == DENSE && p.splits > 1) {
+            u.split = unit % p.splits;
+            unit /= p.splits;
+            u.kb0 = u.split * p.kb_split;
+            u.kb1 = min(u.kb0 + p.kb_split, p.kb);
+        }
         if constexpr (MODE == GRAD) {
-            u.matrix = unit / p.tiles_m;
+            u.matrix = unit / (p.tiles_m * p.tiles_n);
+            unit -= static_cast<int32_t>(u.matrix) * p.tiles_m * p.tiles_n;
             const int32_t S = p.top;   // slots
             int32_t before = 0, mine = 0;
             for (int32_t e = lane; e <= u.matrix; e += 64) {
-                const int32_t lo = min(max(p.offsets[e], 0), S);
-                const int32_t hi = max(min(max(p.offsets[e + 1], 0), S), lo);
+                int32_t lo, hi;
+                positions(p.offsets, p.E, S, e, lo, hi);
                 const int32_t groups = (hi - lo + 127) / 128;
                 if (e < u.matrix) before += groups; else mine = groups;
             }
@@ -512,50 +580,600 @@ __device__ __forceinline__ Unit make_unit(const Params &p, int32_t unit, int lan
             u.kb0 = min(__builtin_amdgcn_readfirstlane(before), p.kb);
             u.kb1 = min(u.kb0 + __builtin_amdgcn_readfirstlane(mine), p.kb);
         }
+        find_tile(unit, p.tiles_m, p.tiles_n, tm, tn);
+        u.m0 = tm * BM;
+        u.m1 = min(p.M, u.m0 + BM);
+        u.tile = unit;
     }
+    u.n0 = tn * BN;
     return u;
 }
 
-// 64 x 64 of C a workgroup, 16 x 64 a wave, operands straight from memory.
-template <int MODE>
-__global__ __launch_bounds__(256) void f8_product_kernel(Params p)
+__device__ __forceinline__ i32x8_t whole(const i32x4_t (&v)[2])
 {
+    return i32x8_t{v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
+}
+
+// ---- codes straight from memory ---------------------------------------------------
+// 16 halves to codes by the conversion that divides by a scale, the same codes as
+// codes4's of the products (every half, every scale).
+__device__ __forceinline__ u32x4_t codes16(u32x4_t lo, u32x4_t hi, uint32_t byte)
+{
+    const float s = bits_as<float>(byte << 23);
+    u32x4_t c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const u32x4_t v = i < 2 ? lo : hi;
+        i16x2_t w = {0, 0};
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, bits_as<half2_t>(v[2 * (i % 2)]), s, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, bits_as<half2_t>(v[2 * (i % 2) + 1]), s, true);
+        c[i] = bits_as<uint32_t>(w);
+    }
+    return c;
+}
+
+// The largest of eight neighbouring lanes' values.
+__device__ __forceinline__ uint32_t eight_max(uint32_t v)
+{
+    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0xb1, 0xf, 0xf, true)));   // lane ^ 1
+    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x4e, 0xf, 0xf, true)));   // lane ^ 2
+    return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x141, 0xf, 0xf, true)));   // 7 - lane
+}
+
+// A few rows of halves against 16 rows of B a workgroup, straight from memory.  The
+// workgroup quantises A's rows to LDS itself, which costs less than a launch for
+// it (a few microseconds) while they are short; its W waves then take every W-th Q
+// groups of 128 columns each and add up at the end.
+template <int MODE, int W, int Q>
+__global__ __launch_bounds__(64 * W) void f8_stream_kernel(Params p)
+{
+    static_assert(W * Q % 4 == 0, "a wave's groups all start at the same byte of a dword of scales");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = wave_index();
     const int r = lane & 15, kq = lane >> 4;
-    const Unit u = make_unit<MODE, 64, 64>(p, xcd_unit(), lane);
+    const Unit u = make_unit<MODE, 16, 16>(p, lane);
     if (u.none) return;
-    const int32_t m = min(u.m0 + wave * 16 + r, u.m1 - 1);
-    int64_t ar = m;
-    if (MODE == EXPERTS && p.top > 0)
-        ar = min(max(p.rows[m], 0) / p.top, p.a_rows - 1);
-    const uint8_t *a = p.a + ar * p.a_ld;
+    const int rows = u.m1 - u.m0;
     const int64_t bm = MODE == EXPERTS ? u.matrix : 0;
-    const uint32_t *bs = p.bs + bm * ((p.kb + 3) / 4) * p.b_blocks;
-    f32x4_t acc[4] = {};
+    const int32_t bn = min(u.n0 + r, p.N - 1);
+    const uint8_t *b = p.b + (bm * p.N + bn) * p.b_ld + kq * 16;
+    const uint32_t *bs = p.bs + bm * ((p.kb + 3) / 4) * p.b_blocks + (bn >> p.b_shift);
+    const int32_t kb = MODE == EXPERTS ? u.kb1 : p.kb;   // none for rows of no expert
+    i32x4_t bv[2][Q][2];
+    uint32_t sb[2];
+    // Groups Q i .. + Q - 1 for i = wave, wave + W, ..., in two buffers: one's loads
+    // fly while the other's are multiplied.  Past the end the last group is loaded
+    // again, so that the waits on one buffer leave the other's in flight.
+    auto load = [&](int buf, int32_t i) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const i32x4_t *at = reinterpret_cast<const i32x4_t *>(b + static_cast<int64_t>(min(i * Q + q, kb - 1)) * 128);
+            bv[buf][q][0] = __builtin_nontemporal_load(at);
+            bv[buf][q][1] = __builtin_nontemporal_load(at + 4);
+        }
+        sb[buf] = bs[static_cast<int64_t>(min(i * Q, kb - 1) >> 2) * p.b_blocks];
+    };
+    const int32_t steps = (kb + Q - 1) / Q;
+    const int32_t count = steps > wave ? (steps - wave + W - 1) / W : 0;
+    auto at = [&](int32_t i) { return wave + min(i, count - 1) * W; };
+    // A's codes and, after them, scales in LDS: rows apart by 16 bytes in the banks
+    const int pitch = kb * 128 + 16;
+    uint8_t *const lds_s = lds + rows * pitch;
+    {
+        // each thread 16 values of a row, eight threads a group; the codes' own loads
+        // go out before the last of them is waited for
+        const int per = kb * 8, all = rows * per;
+        int o = threadIdx.x;
+        u32x4_t lo, hi;
+        auto fetch = [&](int o) {
+            const int row = o / per, c = (o - row * per) * 16;
+            int64_t m = u.m0 + row;
+            if (MODE == EXPERTS && p.top > 0) m = min(max(p.rows[m], 0) / p.top, p.a_rows - 1);
+            const uint16_t *x = p.x + m * p.K;
+            lo = load8(x, c, p.K);
+            hi = load8(x, c + 8, p.K);
+        };
+        auto put = [&](int o) {
+            const int row = o / per, c = o - row * per;
+            const uint32_t byte = scale_byte(eight_max(max(largest8(lo), largest8(hi))));
+            *reinterpret_cast<u32x4_t *>(lds + row * pitch + c * 16) = codes16(lo, hi, byte);
+            if (c % 8 == 0) lds_s[row * kb + c / 8] = static_cast<uint8_t>(byte);
+        };
+        for (; o + 64 * W < all; o += 64 * W) {
+            fetch(o);
+            put(o);
+        }
+        if (o < all) fetch(o);
+        if (count > 0) load(0, at(0));
+        if (o < all) put(o);
+        __syncthreads();
+    }
+    // rows past the last are that row: not stored
+    const int ar = min(r, rows - 1);
+    const uint8_t *const la = lds + ar * pitch + kq * 16;
+    const uint8_t *const ls = lds_s + ar * kb;
+    const int first = wave * Q & 3;   // the byte of a step's first group
+    f32x4_t acc = {};
+    auto mma = [&](int buf, int32_t i) {
+        const int32_t g0 = (wave + i * W) * Q;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if (g0 + q >= kb) break;
+            const i32x4_t x[2] = {*reinterpret_cast<const i32x4_t *>(la + (g0 + q) * 128),
+                                  *reinterpret_cast<const i32x4_t *>(la + (g0 + q) * 128 + 64)};
+            acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(whole(bv[buf][q]), whole(x), acc, 0, 0, 0,
+                                                                   sb[buf] >> (8 * (first + q)), 0, ls[g0 + q]);
+        }
+    };
+    if (count > 0) {
+        int32_t i = 0;
+        for (; i + 2 <= count; i += 2) {
+            load(1, at(i + 1));
+            __builtin_amdgcn_sched_barrier(0);
+            mma(0, i);
+            __builtin_amdgcn_sched_barrier(0);
+            load(0, at(i + 2));
+            __builtin_amdgcn_sched_barrier(0);
+            mma(1, i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (i < count) mma(0, i);
+    }
+    // the waves' sums: lane l holds columns 4 (l / 16) .. + 3, row l % 16
+    __syncthreads();
+    f32x4_t *const red = reinterpret_cast<f32x4_t *>(lds);
+    red[wave * 64 + lane] = acc;
+    __syncthreads();
+    if (wave > 0) return;
+    f32x4_t v = red[lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += red[w * 64 + lane];
+    const int32_t m = u.m0 + r;
+    if (m < u.m1) store4(p.c + static_cast<int64_t>(m) * p.N, u.n0 + kq * 4, p.N, v);
+}
+
+// ---- tiles through LDS --------------------------------------------------------
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// Buffer resource for raw byte addressing from `base` on, 2^32 - 1 bytes: what
+// is loaded lies inside the arrays by its rows and columns, which are held to
+// those that exist.
+__device__ __forceinline__ i32x4_t make_rsrc(const void *base)
+{
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    i32x4_t r;
+    r.x = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(a & 0xffffffffu));
+    r.y = __builtin_amdgcn_readfirstlane(static_cast<int32_t>((a >> 32) & 0xffffu));
+    r.z = -1;
+    r.w = 0x00020000;
+    return r;
+}
+
+// Direct-to-LDS loads: lane l copies 16 (4) bytes from rsrc + voff + soff to LDS
+// byte address lds + 16 l (4 l).  M0 carries the wave-uniform LDS base; the s_nop
+// covers the M0-write hazard, which the compiler cannot see inside an asm.
+__device__ __forceinline__ void dma16(i32x4_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
+{
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds));
+}
+
+__device__ __forceinline__ void dma4(i32x4_t rsrc, uint32_t voff, uint32_t lds)
+{
+    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "{m0}"(lds));
+}
+
+// A workgroup's tile of WM x WN waves, each FM x FN blocks of 32 x 32, in LDS:
+// stages of 128 columns of A's rows, then B's, then a dword of scales for each.
+// Rows of 128 bytes start on two banks' worth of places, so the 16-byte chunks of
+// row r are XORed with a number of r that spreads a fragment's reads over them,
+// applied where the chunks are fetched.
+template <int WM_, int WN_, int FM_, int FN_, int S_>
+struct Tile {
+    static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, S = S_;
+    static constexpr int W = WM * WN, BM = WM * FM * 32, BN = WN * FN * 32;
+    static constexpr int AL = (BM / 8 + W - 1) / W, BL = (BN / 8 + W - 1) / W;   // loads of codes a wave and step
+    static constexpr int SA = (BM + 64 * W - 1) / (64 * W), SB = (BN + 64 * W - 1) / (64 * W);
+    static constexpr int LOADS = AL + BL + SA + SB;
+    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+    static constexpr int SCALES = (BM > 64 ? BM : 64) * 4;   // bytes of A's: whole loads
+    static constexpr int STAGE = (A_BYTES + B_BYTES + SCALES + BN * 4 + 1023) / 1024 * 1024;
+    static constexpr int PITCH = BN * 2 + 16;   // of C's rows
+    static constexpr int LDS = S * STAGE > BM * PITCH ? S * STAGE : BM * PITCH;
+    static_assert(BM % 64 == 0 || BM == 32, "whole loads of scales, or half a one");
+    static_assert(BN % 64 == 0, "whole loads of scales");
+    static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 3); }
+
+// Where a wave's loads come from, and the loads.  Rows past the tile's last are
+// that row again, columns past the last group that group: every load is inside
+// its array, and every step has the same number.
+template <int MODE, class T>
+struct Loads {
+    i32x4_t ra, rb;
+    uint32_t va[T::AL], vb[T::BL], vsa[T::SA], vsb[T::SB], lds0;
+    const uint32_t *as, *bs;
+    int32_t last, a_rows, b_blocks;
+    int wave;
+
+    __device__ __forceinline__ Loads(const Params &p, const Unit &u, const uint8_t *smem, int wave_, int lane)
+    {
+        constexpr int W = T::W, FM = T::FM, FN = T::FN;
+        wave = wave_;
+        const int32_t m0 = u.m0, rows = u.m1 - u.m0, cols = min(T::BN, p.N - u.n0);
+        const int64_t bm = MODE == EXPERTS ? u.matrix : 0;
+        const bool gather = MODE == EXPERTS && p.top > 0;
+        ra = make_rsrc(p.a + (gather ? 0 : m0) * p.a_ld);
+        rb = make_rsrc(p.b + (bm * p.N + u.n0) * p.b_ld);
+        auto a_row = [&](int row) -> uint32_t {   // from ra's
+            const int32_t m = min(row, rows - 1);
+            if (!gather) return m;
+            return min(max(p.rows[m0 + m], 0) / p.top, p.a_rows - 1);
+        };
+        // load d of a wave fills rows 8 (d W + wave) .. + 7: waves without rows
+        // of their own load the last ones again
+#pragma unroll
+        for (int i = 0; i < T::AL; ++i) {
+            const int row = min(i * W + wave, T::BM / 8 - 1) * 8 + lane / 8;
+            va[i] = a_row(row) * static_cast<uint32_t>(p.a_ld) + ((lane & 7) ^ swizzle(row)) * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < T::BL; ++i) {
+            const int row = min(i * W + wave, T::BN / 8 - 1) * 8 + lane / 8;
+            vb[i] = static_cast<uint32_t>(min(row, cols - 1)) * static_cast<uint32_t>(p.b_ld) +
+                    ((lane & 7) ^ swizzle(row)) * 16;
+        }
+        // scales in LDS: [wave][row of 32][block], so that a lane's are neighbours
+#pragma unroll
+        for (int i = 0; i < T::SA; ++i) {
+            const int d = min((i * W + wave) * 64, T::BM > 64 ? T::BM - 64 : 0) + lane;
+            vsa[i] = a_row(d / (32 * FM) * (32 * FM) + d % FM * 32 + d / FM % 32) * 4;
+        }
+#pragma unroll
+        for (int i = 0; i < T::SB; ++i) {
+            const int d = min((i * W + wave) * 64, T::BN - 64) + lane;
+            const int row = min(d / (32 * FN) * (32 * FN) + d % FN * 32 + d / FN % 32, cols - 1);
+            vsb[i] = static_cast<uint32_t>(((u.n0 + row) >> p.b_shift) - (u.n0 >> p.b_shift)) * 4;
+        }
+        lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
+        as = p.as + (gather ? 0 : m0);
+        bs = p.bs + bm * ((p.kb + 3) / 4) * p.b_blocks + (u.n0 >> p.b_shift);
+        a_rows = p.a_rows;
+        b_blocks = p.b_blocks;
+        last = u.kb1 - 1;
+    }
+
+    // Load d (a constant) of group kb to a stage.
+    __device__ __forceinline__ void fetch(int stage, int32_t kb, int d) const
+    {
+        constexpr int W = T::W;
+        kb = min(kb, last);
+        const uint32_t base = lds0 + stage * T::STAGE;
+        const uint32_t soff = static_cast<uint32_t>(kb) * 128u;
+        if (d < T::AL) {
+            dma16(ra, va[d], soff, base + min(d * W + wave, T::BM / 8 - 1) * 1024);
+        } else if (d < T::AL + T::BL) {
+            const int i = d - T::AL;
+            dma16(rb, vb[i], soff, base + T::A_BYTES + min(i * W + wave, T::BN / 8 - 1) * 1024);
+        } else if (d < T::AL + T::BL + T::SA) {
+            const int i = d - T::AL - T::BL;
+            dma4(make_rsrc(as + static_cast<int64_t>(kb >> 2) * a_rows), vsa[i],
+                 base + T::A_BYTES + T::B_BYTES + min((i * W + wave) * 64, T::BM > 64 ? T::BM - 64 : 0) * 4);
+        } else {
+            const int i = d - T::AL - T::BL - T::SA;
+            dma4(make_rsrc(bs + static_cast<int64_t>(kb >> 2) * b_blocks), vsb[i],
+                 base + T::A_BYTES + T::B_BYTES + T::SCALES + min((i * W + wave) * 64, T::BN - 64) * 4);
+        }
+    }
+};
+
+// C from the waves' sums, through LDS, so that a row's columns leave in one run.
+template <int MODE, class T>
+__device__ __forceinline__ void store_tile(const Params &p, const Unit &u, uint16_t *c, uint8_t *smem,
+                                           const f32x16_t (&acc)[T::FM][T::FN], int wm, int wn, int lane)
+{
+    const int r = lane & 31, h = lane >> 5, rows = u.m1 - u.m0;
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f32x4_t v = {acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2],
+                                   acc[i][j][4 * e + 3]};
+                *reinterpret_cast<half4_t *>(smem + ((wm * T::FM + i) * 32 + r) * T::PITCH +
+                                             ((wn * T::FN + j) * 32 + 8 * e + 4 * h) * 2) =
+                    __builtin_convertvector(v, half4_t);
+            }
+    __syncthreads();
+#pragma unroll 4
+    for (int o = threadIdx.x; o < T::BM * T::BN / 8; o += 64 * T::W) {
+        const int row = o / (T::BN / 8), col = o % (T::BN / 8) * 8;
+        if (row >= rows || u.n0 + col >= p.N) continue;
+        store8(c + static_cast<int64_t>(row) * p.N, u.n0 + col, p.N,
+               *reinterpret_cast<const half8_t *>(smem + row * T::PITCH + col * 2));
+    }
+}
+
+// A range's sums, in the order in which lanes hold them.
+template <class T>
+__device__ __forceinline__ void store_partial(const Params &p, const Unit &u, const f32x16_t (&acc)[T::FM][T::FN],
+                                              int wave, int lane)
+{
+    const int64_t tiles = p.tiles_m * p.tiles_n;
+    float *to = p.partial + ((u.split * tiles + u.tile) * T::W + wave) * (T::FM * T::FN * 1024) + lane * 4;
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<f32x4_t *>(to + ((i * T::FN + j) * 4 + e) * 256) =
+                    f32x4_t{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+}
+
+// Zeros: rows of no expert, an expert without rows.
+template <class T>
+__device__ __forceinline__ void store_zeros(const Params &p, const Unit &u, uint16_t *c)
+{
+    for (int o = threadIdx.x; o < T::BM * T::BN / 8; o += 64 * T::W) {
+        const int row = o / (T::BN / 8), col = o % (T::BN / 8) * 8;
+        if (row < u.m1 - u.m0 && u.n0 + col < p.N)
+            store8(c + static_cast<int64_t>(row) * p.N, u.n0 + col, p.N, half8_t{});
+    }
+}
+
+// A block's sums are held to the accumulation registers: a wave's 128 x 128 values
+// need all 256, and the compiler left to itself splits them between both files and
+// spills.  It then cannot see these MFMAs, so the kernel supplies the wait
+// states around them.  (The host's pass of the compiler knows no such registers.)
+__device__ __forceinline__ void mfma(f32x16_t &acc, i32x8_t b, i32x8_t a, uint32_t sb, uint32_t sa)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                 : "+a"(acc)
+                 : "v"(b), "v"(a), "v"(sb), "v"(sa));
+#endif
+}
+
+__device__ __forceinline__ void keep(f32x16_t &acc)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("" : "+a"(acc));
+#endif
+}
+
+// Two stages; a step's MFMAs are its two halves' (64 columns), each half's
+// fragments read from LDS while the other's are multiplied.
+template <int MODE, class T, int OCC>
+__global__ __launch_bounds__(64 * T::W)
+__attribute__((amdgpu_waves_per_eu(OCC, OCC)))
+void f8_tile_kernel(Params p)
+{
+    constexpr int FM = T::FM, FN = T::FN, LOADS = T::LOADS;
+    static_assert(T::S == 2, "two stages");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+    const int lane = threadIdx.x & 63, wave = wave_index();
+    const int wm = wave / T::WN, wn = wave % T::WN;
+    const int r = lane & 31, h = lane >> 5;
+    const Unit u = make_unit<MODE, T::BM, T::BN>(p, lane);
+    if (u.none) return;
+    uint16_t *c = p.c + (MODE == GRAD ? u.matrix * p.M * p.N : 0) + static_cast<int64_t>(u.m0) * p.N;
+    if (MODE != DENSE && u.kb0 >= u.kb1) return store_zeros<T>(p, u, c);
+    const Loads<MODE, T> loads(p, u, smem, wave, lane);
+    f32x16_t acc[FM][FN];
+    int off[4];   // a lane's 16-byte chunks in a tile's rows
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) off[kk * 2 + w] = r * 128 + (((kk * 4 + h * 2 + w) ^ swizzle(r)) * 16);
+    i32x4_t af[2][FM][2], bf[2][FN][2];
+    uint32_t sa[FM], sb[FN], na[FM], nb[FN];
+    auto read = [&](int stage, int kk, int d) {   // one of 2 (FM + FN)
+        const uint8_t *st = smem + stage * T::STAGE;
+        if (d < 2 * FM)
+            af[kk][d / 2][d % 2] = *reinterpret_cast<const i32x4_t *>(
+                st + wm * FM * 4096 + d / 2 * 4096 + off[kk * 2 + d % 2]);
+        else
+            bf[kk][d / 2 - FM][d % 2] = *reinterpret_cast<const i32x4_t *>(
+                st + T::A_BYTES + wn * FN * 4096 + (d / 2 - FM) * 4096 + off[kk * 2 + d % 2]);
+    };
+    auto read_scales = [&](int stage) {
+        const uint8_t *st = smem + stage * T::STAGE + T::A_BYTES + T::B_BYTES;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            na[i] = *reinterpret_cast<const uint32_t *>(st + ((wm * 32 + r) * FM + i) * 4);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+            nb[i] = *reinterpret_cast<const uint32_t *>(st + T::SCALES + ((wn * 32 + r) * FN + i) * 4);
+    };
+    auto take_scales = [&](int32_t kb) {
+        const int s = 8 * (min(kb, loads.last) & 3);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sa[i] = na[i] >> s;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) sb[i] = nb[i] >> s;
+        // two wait states between a VALU's result and an MFMA that reads it
+#pragma unroll
+        for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(sa[i]));
+#pragma unroll
+        for (int i = 0; i < FN; ++i) asm volatile("" : "+v"(sb[i]));
+        asm volatile("s_nop 1");
+    };
+    constexpr int READS = 2 * (FM + FN), MFMAS = FM * FN;
+    // the MFMAs of half a step, the next half's reads and the loads between them
+    auto compute = [&](int kk, auto each) {
+#pragma unroll
+        for (int t = 0; t < MFMAS; ++t) {
+            const int i = t / FN, j = t % FN;
+            mfma(acc[i][j], whole(bf[kk][j]), whole(af[kk][i]), sb[j], sa[i]);
+            each(t);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < LOADS; ++d) loads.fetch(0, u.kb0, d);
+#pragma unroll
+    for (int d = 0; d < LOADS; ++d) loads.fetch(1, u.kb0 + 1, d);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(LOADS) : "memory");
+#pragma unroll
+    for (int d = 0; d < READS; ++d) read(0, 0, d);
+    read_scales(0);
+    take_scales(u.kb0);
+    auto step = [&](int stage, int32_t kb) {
+        compute(0, [&](int t) {
+#pragma unroll
+            for (int d = 0; d < READS; ++d)
+                if (d * MFMAS / READS == t) read(stage, 1, d);
+        });
+        // this stage is read to the end, the next one has landed
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : : "memory");
+        read_scales(stage ^ 1);
+        compute(1, [&](int t) {
+#pragma unroll
+            for (int d = 0; d < READS; ++d)
+                if (d * MFMAS / READS == t) read(stage ^ 1, 0, d);
+#pragma unroll
+            for (int d = 0; d < LOADS; ++d)
+                if (d * MFMAS / LOADS == t) loads.fetch(stage, kb + 2, d);
+        });
+        take_scales(kb + 1);
+    };
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            acc[i][j] = f32x16_t{};
+            keep(acc[i][j]);
+        }
+    asm volatile("s_nop 4");   // between those writes and the first MFMA
+    for (int32_t kb = u.kb0;;) {
+        step(0, kb);
+        if (++kb >= u.kb1) break;
+        step(1, kb);
+        if (++kb >= u.kb1) break;
+    }
+    // wait states between the last MFMA and the first read of what it wrote: more
+    // than any MFMA asks for; and no load may still be on its way to this LDS
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_waitcnt vmcnt(0)" : : : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (MODE == DENSE && p.splits > 1) return store_partial<T>(p, u, acc, wave, lane);
+    __syncthreads();
+    store_tile<MODE, T>(p, u, c, smem, acc, wm, wn, lane);
+}
+
+// A ring of S stages for few rows, where reading B bounds the call: S - 1 groups
+// are on their way while one is multiplied.  With p.splits > 1 (dense) K is
+// split into ranges of p.kb_split groups, and the ranges' sums go to p.partial in
+// the order in which lanes hold them.
+template <int MODE, class T>
+__global__ __launch_bounds__(64 * T::W) void f8_ring_kernel(Params p)
+{
+    constexpr int FM = T::FM, FN = T::FN, LOADS = T::LOADS, S = T::S;
+    static_assert((S - 2) * LOADS <= 63, "vmcnt counts at most 63 loads");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+    const int lane = threadIdx.x & 63, wave = wave_index();
+    const int wm = wave / T::WN, wn = wave % T::WN;
+    const int r = lane & 31, h = lane >> 5;
+    Unit u = make_unit<MODE, T::BM, T::BN>(p, lane);
+    if (u.none) return;
+    uint16_t *c = p.c + (MODE == GRAD ? u.matrix * p.M * p.N : 0) + static_cast<int64_t>(u.m0) * p.N;
+    if (MODE != DENSE && u.kb0 >= u.kb1) return store_zeros<T>(p, u, c);
+    const Loads<MODE, T> loads(p, u, smem, wave, lane);
+    f32x16_t acc[FM][FN] = {};
+    int off[4];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) off[kk * 2 + w] = r * 128 + (((kk * 4 + h * 2 + w) ^ swizzle(r)) * 16);
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s)
+#pragma unroll
+        for (int d = 0; d < LOADS; ++d) loads.fetch(s, u.kb0 + s, d);
+    int stage = 0;
     for (int32_t kb = u.kb0; kb < u.kb1; ++kb) {
-        const i32x8_t af = load_codes(a + static_cast<int64_t>(kb) * 128, kq);
-        const int sa = p.as[static_cast<int64_t>(kb >> 2) * p.a_rows + ar] >> (8 * (kb & 3));
+        // this stage's loads (the oldest) have landed, and every wave is done with
+        // the stage before it, which is filled again
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"((S - 2) * LOADS) : "memory");
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int32_t n = min(u.n0 + j * 16 + r, p.N - 1);
-            const i32x8_t bf =
-                load_codes(p.b + (bm * p.N + n) * p.b_ld + static_cast<int64_t>(kb) * 128, kq);
-            const int sb = bs[static_cast<int64_t>(kb >> 2) * p.b_blocks + (n >> p.b_shift)] >> (8 * (kb & 3));
-            acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf, af, acc[j], 0, 0, 0, sb, 0, sa);
+        for (int d = 0; d < LOADS; ++d) loads.fetch(stage == 0 ? S - 1 : stage - 1, kb + S - 1, d);
+        const uint8_t *st = smem + stage * T::STAGE;
+        const uint8_t *ss = st + T::A_BYTES + T::B_BYTES;
+        const int s = 8 * (kb & 3);
+        uint32_t sa[FM], sb[FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            sa[i] = *reinterpret_cast<const uint32_t *>(ss + ((wm * 32 + r) * FM + i) * 4) >> s;
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+            sb[i] = *reinterpret_cast<const uint32_t *>(ss + T::SCALES + ((wn * 32 + r) * FN + i) * 4) >> s;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            i32x4_t af[FM][2], bf[FN][2];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+                    af[i][w] = *reinterpret_cast<const i32x4_t *>(st + (wm * FM + i) * 4096 + off[kk * 2 + w]);
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    bf[j][w] = *reinterpret_cast<const i32x4_t *>(st + T::A_BYTES + (wn * FN + j) * 4096 +
+                                                                  off[kk * 2 + w]);
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        whole(bf[j]), whole(af[i]), acc[i][j], 0, 0, 0, sb[j], 0, sa[i]);
         }
+        stage = stage == S - 1 ? 0 : stage + 1;
     }
-    const int32_t mo = u.m0 + wave * 16 + r;
-    if (mo >= u.m1) return;
-    uint16_t *c = p.c + (MODE == GRAD ? u.matrix * p.M * p.N : 0) + static_cast<int64_t>(mo) * p.N;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const half4_t h = __builtin_convertvector(acc[j], half4_t);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int32_t n = u.n0 + j * 16 + kq * 4 + e;
-            if (n < p.N) c[n] = bits_as<uint16_t>(_Float16(h[e]));
-        }
-    }
+    // no load may still be on its way to this LDS
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    if (MODE == DENSE && p.splits > 1) return store_partial<T>(p, u, acc, wave, lane);
+    __syncthreads();
+    store_tile<MODE, T>(p, u, c, smem, acc, wm, wn, lane);
+}
+
+// C from the ranges' sums, in order; four columns a thread.
+struct JoinParams {
+    const float *partial;
+    uint16_t *c;
+    int64_t stride;                    // values between two ranges' sums
+    int32_t M, N, tiles_m, tiles_n, splits;
+    int32_t wn, fm, fn, waves;
+};
+
+__global__ __launch_bounds__(256) void f8_join_kernel(JoinParams p)
+{
+    const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (idx * 4 >= p.stride) return;
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    int32_t rest = static_cast<int32_t>(idx >> 6);
+    const int e = rest % 4;
+    rest /= 4;
+    const int j = rest % p.fn;
+    rest /= p.fn;
+    const int i = rest % p.fm;
+    rest /= p.fm;
+    const int wave = rest % p.waves;
+    int32_t tm, tn;
+    find_tile(rest / p.waves, p.tiles_m, p.tiles_n, tm, tn);
+    const int wm = wave / p.wn, wn = wave % p.wn;
+    const int32_t m = ((tm * (p.waves / p.wn) + wm) * p.fm + i) * 32 + r;
+    const int32_t n = ((tn * p.wn + wn) * p.fn + j) * 32 + 8 * e + 4 * h;
+    if (m >= p.M || n >= p.N) return;
+    const float *from = p.partial + idx * 4;
+    f32x4_t sum = *reinterpret_cast<const f32x4_t *>(from);
+#pragma unroll 4
+    for (int32_t s = 1; s < p.splits; ++s) sum += *reinterpret_cast<const f32x4_t *>(from + s * p.stride);
+    store4(p.c + static_cast<int64_t>(m) * p.N, n, p.N, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -592,13 +1210,14 @@ static int check_arrays(const Array *arrays, int count)
     return GEMM_F16_OK;
 }
 
-static int launch(const void *fn, int64_t grid, int threads, void *params, hipStream_t stream)
+static int launch(const void *fn, int64_t grid, int threads, void *params, hipStream_t stream,
+                  int lds = 0)
 {
     // the launch's own status only: the thread's sticky error state is neither
     // read nor cleared
     void *args[] = {params};
     const hipError_t err = hipLaunchKernel(fn, dim3(static_cast<uint32_t>(grid)),
-                                           dim3(static_cast<uint32_t>(threads)), args, 0, stream);
+                                           dim3(static_cast<uint32_t>(threads)), args, lds, stream);
     return err == hipSuccess ? GEMM_F16_OK : GEMM_F16_LAUNCH_FAILED;
 }
 template <class K>
@@ -676,23 +1295,174 @@ struct Call {
 
 constexpr int64_t MOST_EXPERTS = 1024;
 
-static int plan_call(const Call &c, int32_t num_cus, gemm_f16_lowbit_plan_t *plan)
+struct Kernel {
+    int32_t kind, bm, bn, waves;
+    int32_t lds;               // for the waves' sums
+    int32_t wn, fm, fn;        // of a kernel whose K may be split
+    int32_t slots;             // workgroups on a compute unit
+    double start, step, full;  // us: a workgroup's start and end, 128 columns with one and with all slots taken
+    const void *run[3];        // by mode
+};
+#define STREAM(W, Q)                                                                              \
+    {GEMM_F16_LOWBIT_STREAM, 16, 16, W, W * 1024, 0, 0, 0, 0, 0, 0, 0,                            \
+     {address(f8_stream_kernel<DENSE, W, Q>), address(f8_stream_kernel<EXPERTS, W, Q>), nullptr}}
+#define TILE(WM, WN, FM, FN, OCC, START, STEP, FULL)                                              \
+    {GEMM_F16_LOWBIT_TILE, WM * FM * 32, WN * FN * 32, WM * WN, 0, WN, FM, FN, OCC, START, STEP, FULL, \
+     {address(f8_tile_kernel<DENSE, Tile<WM, WN, FM, FN, 2>, OCC>),                               \
+      address(f8_tile_kernel<EXPERTS, Tile<WM, WN, FM, FN, 2>, OCC>),                             \
+      address(f8_tile_kernel<GRAD, Tile<WM, WN, FM, FN, 2>, OCC>)}}
+#define RING(WM, WN, FM, FN, S, START, STEP, FULL)                                                \
+    {GEMM_F16_LOWBIT_TILE, WM * FM * 32, WN * FN * 32, WM * WN, 0, WN, FM, FN, 2, START, STEP, FULL, \
+     {address(f8_ring_kernel<DENSE, Tile<WM, WN, FM, FN, S>>),                                    \
+      address(f8_ring_kernel<EXPERTS, Tile<WM, WN, FM, FN, S>>),                                  \
+      address(f8_ring_kernel<GRAD, Tile<WM, WN, FM, FN, S>>)}}
+static const Kernel kKernels[] = {
+    TILE(2, 2, 4, 4, 1, 6.81, 0.936, 0.936), TILE(2, 2, 4, 3, 1, 6.02, 0.761, 0.761),
+    TILE(2, 2, 2, 2, 2, 2.35, 0.540, 0.721), RING(1, 2, 1, 1, 6, 1.25, 0.210, 0.254),
+    RING(2, 2, 1, 1, 4, 1.27, 0.239, 0.364), RING(1, 4, 2, 1, 3, 1.58, 0.351, 0.572),
+    STREAM(8, 2), STREAM(16, 2),
+};
+#undef TILE
+#undef RING
+#undef STREAM
+constexpr int32_t TILES = 6, STREAM8 = 6, STREAM16 = 7;
+
+// The kernel of a call, an index of kKernels, and the ranges of K (dense).
+struct Choice {
+    int32_t id, splits;
+};
+
+// Time in us of `wgs` workgroups with `steps` groups of columns each, their K in
+// `splits` ranges; bytes of the operands and C.  Rounds of workgroups over the CUs,
+// the memory's rate and the matrix units' at the power limit, and for ranges their
+// sums' way through memory and the join.
+static double model(const Kernel &e, double wgs, double steps, int64_t splits, double bytes, int32_t cus)
+{
+    const double slots = static_cast<double>(cus) * e.slots;
+    const double all = std::floor(wgs / slots), rest = wgs - all * slots;
+    const double taken = e.full * steps + e.start * e.slots, tile = static_cast<double>(e.bm) * e.bn;
+    double us = all * taken;
+    if (rest > 0) us += rest <= cus ? e.step * steps + e.start : taken;
+    const double memory = bytes / 5.757e6, matrix = wgs * tile * steps * GROUP / 1.052e9;
+    auto fourth = [](double x) { return x * x * x * x; };
+    us = std::sqrt(std::sqrt(fourth(us) + fourth(memory) + fourth(matrix)));
+    return us + 2.82 + (splits > 1 ? 1.93 + 4.0 * wgs * tile / 4.42e6 : 0.0);
+}
+
+// The tile and ring kernels and ranges of K by that model, fitted to 3,700 timings
+// of 182 shapes (1 to 8192 rows, N and K of 64 to 16384, 8 to 256 experts, operands from
+// HBM; they are not kept with the source).  Its error is 10 to 18%; what it chose took 1.7%
+// (products), 2.7% (experts) and 1.5% (gradients) longer than the best of each
+// shape in the mean, 15, 46 and 14% in the worst (2355 tokens, 8 of 64 experts, 1600 x 256:
+// 51.8 us, with 128 x 128 tiles 35.6).
+static Choice search(const Call &c, int32_t num_cus)
+{
+    const double M = static_cast<double>(c.M), N = static_cast<double>(c.N), K = static_cast<double>(c.a.kp);
+    const int64_t kb = std::max<int64_t>(c.a.kp / GROUP, 1);
+    // experts that have rows, if each row's is drawn alike
+    const double E = static_cast<double>(c.matrices);
+    const double used = c.mode == DENSE ? 1.0 : E * (1.0 - std::pow(1.0 - 1.0 / E, c.mode == EXPERTS ? M : c.top));
+    const double bytes = c.mode == GRAD ? c.top * (M + N) + 2.0 * E * M * N : used * N * K + M * K + 2.0 * M * N;
+    Choice best{};
+    // Halves that the product's kernel quantises itself: up to 16 rows, and 2^15
+    // values of them a workgroup; of experts' tiles not many more than run at once.
+    // (5 x 7001 x 4160 12.7 us, quantised first 13.3; 14 x 4544 x 8064 26.3 and 14.8; one token's 8
+    // experts of 1216 x 512 5.5 and 7.9, 48 experts of 256, 3328 x 192, 69 and 24.)  Sixteen waves
+    // where that is about one step each (16 x 448 x 1728 5.9 us, eight 6.8; 1 x 4096 x 14336 16.2
+    // and 14.6; 8 x 15936 x 832 10.4 and 8.3).
+    const double rows = c.mode == EXPERTS ? M / used : M;
+    if (c.a_f16 && c.mode != GRAD && rows <= 16 && std::min(M, 16.0) * K <= 32768 &&
+        (c.mode == DENSE || used * static_cast<double>(cdiv(c.N, 16)) <= 3.0 * num_cus)) {
+        best.id = kb > 12 && kb <= 36 ? STREAM16 : STREAM8;
+        best.splits = 1;
+        return best;
+    }
+    double best_us = 0;
+    for (int32_t id = 0; id < TILES; ++id) {
+        const Kernel &e = kKernels[id];
+        const int64_t tiles = cdiv(c.M, e.bm) * cdiv(c.N, e.bn);
+        auto consider = [&](double wgs, double steps, int64_t splits) {
+            const double us = model(e, wgs, steps, splits, bytes, num_cus);
+            if (best_us > 0 && us >= best_us) return;
+            best_us = us;
+            best = Choice{id, static_cast<int32_t>(splits)};
+        };
+        if (c.mode == GRAD) {
+            consider(E * static_cast<double>(tiles), c.top > 64.0 * E ? c.top / E / GROUP + 0.5 : 1.0, 1);
+        } else if (c.mode == EXPERTS) {
+            const double down = std::max(used, M / e.bm + (M > 0.5 * e.bm * used ? 0.5 : 1.0) * used);
+            consider(std::ceil(static_cast<double>(cdiv(c.N, e.bn)) * down), static_cast<double>(kb), 1);
+        } else {
+            int64_t last = 0;
+            for (int64_t sp = 1; sp <= std::min<int64_t>(kb, 32); ++sp) {
+                const int64_t per = cdiv(kb, sp), splits = cdiv(kb, per);
+                if (per == last) continue;   // the same ranges
+                last = per;
+                if (sp > 1 && tiles * splits > 4 * e.slots * num_cus) break;
+                consider(static_cast<double>(tiles * splits), static_cast<double>(per), splits);
+            }
+        }
+    }
+    return best;
+}
+
+// The search takes microseconds: each thread keeps its last few choices.
+static Choice choose(const Call &c, int32_t num_cus)
+{
+    struct Entry {
+        int64_t M, N, K, matrices;
+        int32_t mode, top, cus;
+        bool a_f16;
+        Choice choice;
+    };
+    static thread_local Entry cache[8] = {};
+    static thread_local int next = 0;
+    for (const Entry &o : cache)
+        if (o.cus == num_cus && o.M == c.M && o.N == c.N && o.K == c.K && o.matrices == c.matrices &&
+            o.mode == c.mode && o.top == c.top && o.a_f16 == c.a_f16)
+            return o.choice;
+    const Choice choice = search(c, num_cus);
+    cache[next] = Entry{c.M, c.N, c.K, c.matrices, c.mode, c.top, num_cus, c.a_f16, choice};
+    next = (next + 1) % 8;
+    return choice;
+}
+
+// The bytes of LDS in which a workgroup of a stream kernel quantises A's rows.
+static int64_t stream_lds(const Call &c, const Kernel &e)
+{
+    const int64_t rows = std::min<int64_t>(16, c.M);
+    return std::max<int64_t>(rows * (c.a.kp + 16) + round_up(rows * (c.a.kp / GROUP), 16), e.lds);
+}
+
+// The bytes of one range's sums.
+static int64_t partial_bytes(const Call &c, const Kernel &e)
+{
+    return cdiv(c.M, e.bm) * cdiv(c.N, e.bn) * e.bm * e.bn * 4;
+}
+
+static int plan_call(const Call &c, int32_t num_cus, gemm_f16_lowbit_plan_t *plan, Choice *r)
 {
     *plan = gemm_f16_lowbit_plan_t{};
     plan->splits = 1;
     if (num_cus <= 0) return GEMM_F16_INVALID_ARG;
-    if (cdiv(c.M, 16) * cdiv(c.N, 16) > INT32_MAX / (c.mode == GRAD ? c.matrices : 1))
-        return GEMM_F16_UNSUPPORTED;
+    const int64_t matrices = c.mode == GRAD ? c.matrices : 1;
+    if (cdiv(c.M, 16) * cdiv(c.N, 16) > INT32_MAX / matrices) return GEMM_F16_UNSUPPORTED;
     if (c.M == 0 || c.N == 0) return GEMM_F16_OK;
-    int64_t tiles = cdiv(c.M, 64);
-    if (c.mode == EXPERTS) tiles = c.M / 64 + std::min(c.matrices, c.M) + 1;
-    const int64_t grid = (c.mode == GRAD ? c.matrices : 1) * tiles * cdiv(c.N, 64);
-    if (grid * 256 >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
-    plan->kernel = GEMM_F16_LOWBIT_STREAM;
-    plan->block_m = plan->block_n = 64;
-    plan->waves = 4;
+    *r = choose(c, num_cus);
+    const Kernel &e = kKernels[r->id];
+    // every expert, and the rows of none, may end inside a tile
+    const int64_t tiles = c.mode == EXPERTS ? c.M / e.bm + std::min(c.matrices, c.M) + 1 : cdiv(c.M, e.bm);
+    const int64_t grid = matrices * tiles * cdiv(c.N, e.bn) * r->splits;
+    if (grid * 64 * e.waves >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
+    plan->kernel = e.kind;
+    plan->block_m = e.bm;
+    plan->block_n = e.bn;
+    plan->waves = e.waves;
+    plan->splits = r->splits;
     plan->grid = static_cast<int32_t>(grid);
-    if (c.a_f16) plan->workspace_bytes = round_up(c.a.codes, 256) + round_up(c.a.scales, 256);
+    if (r->splits > 1) plan->workspace_bytes = r->splits * partial_bytes(c, e);
+    if (c.a_f16 && r->id < TILES)
+        plan->workspace_bytes += round_up(c.a.codes, 256) + round_up(c.a.scales, 256);
     return GEMM_F16_OK;
 }
 
@@ -705,17 +1475,25 @@ static int run_call(const Call &c, const void *X, const void *a_codes, const voi
     int v = gemm_f16_device_cus(&cus);
     if (v != GEMM_F16_OK) return v;
     gemm_f16_lowbit_plan_t plan;
-    v = plan_call(c, cus, &plan);
+    Choice r{};
+    v = plan_call(c, cus, &plan, &r);
     if (v != GEMM_F16_OK) return v;
     if (plan.workspace_bytes > (workspace ? workspace_bytes : 0)) return GEMM_F16_INVALID_ARG;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    if (c.a_f16 && c.a.codes > 0) {
+    const Kernel &e = kKernels[r.id];
+    const bool fused = r.id >= TILES;
+    const int64_t a_bytes = c.a_f16 && !fused ? round_up(c.a.codes, 256) + round_up(c.a.scales, 256) : 0;
+    if (a_bytes > 0) {
         v = quantize(1, c.a_rows, c.K, 1, false, c.a, X, ws, ws + round_up(c.a.codes, 256), stream);
         if (v != GEMM_F16_OK) return v;
         a_codes = ws;
         a_scales = ws + round_up(c.a.codes, 256);
     }
     Params p;
+    const int64_t partial = plan.splits > 1 ? partial_bytes(c, e) : 0;
+    p.partial = reinterpret_cast<float *>(ws + a_bytes);
+    p.splits = plan.splits;
+    p.kb_split = static_cast<int32_t>(cdiv(c.a.kp / GROUP, plan.splits));
     p.a = static_cast<const uint8_t *>(a_codes);
     p.b = static_cast<const uint8_t *>(b_codes);
     p.as = static_cast<const uint32_t *>(a_scales);
@@ -727,18 +1505,33 @@ static int run_call(const Call &c, const void *X, const void *a_codes, const voi
     p.b_ld = c.b.kp;
     p.M = static_cast<int32_t>(c.M);
     p.N = static_cast<int32_t>(c.N);
+    p.K = static_cast<int32_t>(c.K);
+    p.x = static_cast<const uint16_t *>(X);
     p.kb = static_cast<int32_t>(c.a.kp / GROUP);
     p.a_rows = static_cast<int32_t>(c.a_rows);
     p.b_blocks = static_cast<int32_t>(c.b.blocks);
     p.b_shift = c.b.shift;
     p.E = static_cast<int32_t>(c.matrices);
     p.top = c.top;
-    p.tiles_m = static_cast<int32_t>(cdiv(c.M, 64));
-    p.tiles_n = static_cast<int32_t>(cdiv(c.N, 64));
-    const void *fn = c.mode == DENSE     ? address(f8_product_kernel<DENSE>)
-                     : c.mode == EXPERTS ? address(f8_product_kernel<EXPERTS>)
-                                         : address(f8_product_kernel<GRAD>);
-    return launch(fn, plan.grid, 256, &p, stream);
+    p.tiles_m = static_cast<int32_t>(cdiv(c.M, e.bm));
+    p.tiles_n = static_cast<int32_t>(cdiv(c.N, e.bn));
+    v = launch(e.run[c.mode], plan.grid, 64 * e.waves, &p, stream,
+               static_cast<int>(fused ? stream_lds(c, e) : 0));
+    if (v != GEMM_F16_OK || plan.splits == 1) return v;
+    JoinParams q;
+    q.partial = p.partial;
+    q.c = p.c;
+    q.stride = partial / 4;
+    q.M = p.M;
+    q.N = p.N;
+    q.tiles_m = p.tiles_m;
+    q.tiles_n = p.tiles_n;
+    q.splits = p.splits;
+    q.wn = e.wn;
+    q.fm = e.fm;
+    q.fn = e.fn;
+    q.waves = e.waves;
+    return launch(address(f8_join_kernel), cdiv(partial, 4096), 256, &q, stream);
 }
 
 static int dense_call(int64_t M, int64_t N, int64_t K, int32_t b_block, bool a_f16, Call *c)
@@ -894,8 +1687,9 @@ extern "C" int gemm_f16_nt_f8_plan(int64_t M, int64_t N, int64_t K, int32_t b_bl
 {
     if (!plan) return GEMM_F16_INVALID_ARG;
     Call c;
+    Choice r{};
     const int v = dense_call(M, N, K, b_block, a_f16 != 0, &c);
-    return v != GEMM_F16_OK ? v : plan_call(c, num_cus, plan);
+    return v != GEMM_F16_OK ? v : plan_call(c, num_cus, plan, &r);
 }
 
 extern "C" int gemm_f16_nt_f8(int64_t M, int64_t N, int64_t K, const void *a_codes,
@@ -921,8 +1715,9 @@ extern "C" int gemm_f16_nt_f8_experts_plan(int64_t S, int64_t E, int64_t N, int6
 {
     if (!plan) return GEMM_F16_INVALID_ARG;
     Call c;
+    Choice r{};
     const int v = experts_call(S, E, N, K, top, a_f16 != 0, &c);
-    return v != GEMM_F16_OK ? v : plan_call(c, num_cus, plan);
+    return v != GEMM_F16_OK ? v : plan_call(c, num_cus, plan, &r);
 }
 
 extern "C" int gemm_f16_nt_f8_experts(int64_t S, int64_t E, int64_t N, int64_t K, int32_t top,
