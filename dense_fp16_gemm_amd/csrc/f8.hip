@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -40,11 +41,12 @@ __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstl
 
 // This workgroup's unit of work, where each XCD (workgroups mod 8) takes a
 // contiguous range of them: neighbours share cache lines in its L2.
-__device__ __forceinline__ int32_t xcd_unit()
+__device__ __forceinline__ int32_t xcd_unit(int32_t id, int32_t count)
 {
-    const int32_t q = gridDim.x >> 3, rem = gridDim.x & 7, x = blockIdx.x & 7;
-    return x * q + (x < rem ? x : rem) + (blockIdx.x >> 3);
+    const int32_t q = count >> 3, rem = count & 7, x = id & 7;
+    return x * q + (x < rem ? x : rem) + (id >> 3);
 }
+__device__ __forceinline__ int32_t xcd_unit() { return xcd_unit(blockIdx.x, gridDim.x); }
 
 // Eight halves of a row at column c, as dwords; columns at or past `cols` are 0.
 __device__ __forceinline__ u32x4_t load8(const uint16_t *row, int32_t c, int32_t cols)
@@ -122,6 +124,14 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d)
 {
     int32_t v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true));
+}
+
+// Between a wave's LDS writes and its other lanes' reads of them: see that the
+// compiler keeps their order (a wave's LDS operations are done in order).
+__device__ __forceinline__ void wave_lds_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // ---------------------------------------------------------------------------
@@ -491,6 +501,7 @@ struct Params {
     int32_t b_blocks, b_shift;  // blocks of rows of B, log2 of their size
     int32_t E, top;
     int32_t tiles_m, tiles_n;
+    int32_t units;              // at most, where a workgroup takes more than one
     int32_t splits, kb_split;   // ranges of K (dense), groups of each
     float *partial;             // their sums
 };
@@ -534,60 +545,127 @@ __device__ __forceinline__ void find_tile(int32_t tile, int32_t tiles_m, int32_t
     tn = rest / height;
 }
 
+// Rows lo .. hi - 1 of expert e (-1: of none), `index` of their tiles.
+template <int BM, int BN>
+__device__ __forceinline__ Unit expert_unit(const Params &p, const Found &f)
+{
+    Unit u{};
+    const int32_t tiles = max((f.hi - f.lo + BM - 1) / BM, 1);
+    const int32_t tm = f.index % tiles, tn = f.index / tiles;
+    u.m0 = f.lo + tm * BM;
+    u.m1 = min(f.hi, u.m0 + BM);
+    u.n0 = tn * BN;
+    u.none = f.lo >= f.hi;
+    u.kb1 = f.e < 0 ? 0 : p.kb;
+    u.matrix = max(f.e, 0);
+    return u;
+}
+
+// Unit `id` of `count` of a product of two matrices, K in p.splits ranges, or of the
+// gradients (whose range of K is not found here).
+template <int MODE, int BM, int BN>
+__device__ __forceinline__ Unit matrix_unit(const Params &p, int32_t id, int32_t count)
+{
+    Unit u{};
+    int32_t unit = xcd_unit(id, count), tm, tn;
+    u.kb1 = p.kb;
+    if (MODE == DENSE && p.splits > 1) {
+        u.split = unit % p.splits;
+        unit /= p.splits;
+        u.kb0 = u.split * p.kb_split;
+        u.kb1 = min(u.kb0 + p.kb_split, p.kb);
+    }
+    if constexpr (MODE == GRAD) {
+        u.matrix = unit / (p.tiles_m * p.tiles_n);
+        unit -= static_cast<int32_t>(u.matrix) * p.tiles_m * p.tiles_n;
+    }
+    find_tile(unit, p.tiles_m, p.tiles_n, tm, tn);
+    u.m0 = tm * BM;
+    u.m1 = min(p.M, u.m0 + BM);
+    u.n0 = tn * BN;
+    u.tile = unit;
+    return u;
+}
+
+// A workgroup's only unit.
 template <int MODE, int BM, int BN>
 __device__ __forceinline__ Unit make_unit(const Params &p, int lane)
 {
-    Unit u;
-    u.none = false;
-    u.matrix = 0;
-    u.kb0 = 0;
-    u.kb1 = p.kb;
-    int32_t tm, tn;
-    if constexpr (MODE == EXPERTS) {
-        const Found f = find_unit<true>(p.offsets, p.E, p.M, BM, p.tiles_n, blockIdx.x, lane);
-        const int32_t tiles = max((f.hi - f.lo + BM - 1) / BM, 1);
-        tm = f.index % tiles;
-        tn = f.index / tiles;
-        u.m0 = f.lo + tm * BM;
-        u.m1 = min(f.hi, u.m0 + BM);
-        u.none = f.lo >= f.hi;
-        if (f.e < 0) u.kb1 = 0;
-        u.matrix = max(f.e, 0);
-    } else {
-        int32_t unit = xcd_unit();
-        if (MODE == DENSE && p.splits > 1) {
-            u.split = unit % p.splits;
-            unit /= p.splits;
-            u.kb0 = u.split * p.kb_split;
-            u.kb1 = min(u.kb0 + p.kb_split, p.kb);
+    if constexpr (MODE == EXPERTS)
+        return expert_unit<BM, BN>(p, find_unit<true>(p.offsets, p.E, p.M, BM, p.tiles_n, blockIdx.x, lane));
+    Unit u = matrix_unit<MODE, BM, BN>(p, blockIdx.x, gridDim.x);
+    if constexpr (MODE == GRAD) {
+        int32_t before = 0, mine = 0;
+        for (int32_t e = lane; e <= u.matrix; e += 64) {
+            int32_t lo, hi;
+            positions(p.offsets, p.E, p.top, e, lo, hi);   // top: slots
+            const int32_t groups = (hi - lo + 127) / 128;
+            if (e < u.matrix) before += groups; else mine = groups;
         }
-        if constexpr (MODE == GRAD) {
-            u.matrix = unit / (p.tiles_m * p.tiles_n);
-            unit -= static_cast<int32_t>(u.matrix) * p.tiles_m * p.tiles_n;
-            const int32_t S = p.top;   // slots
-            int32_t before = 0, mine = 0;
-            for (int32_t e = lane; e <= u.matrix; e += 64) {
-                int32_t lo, hi;
-                positions(p.offsets, p.E, S, e, lo, hi);
-                const int32_t groups = (hi - lo + 127) / 128;
-                if (e < u.matrix) before += groups; else mine = groups;
-            }
 #pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                before += __shfl_xor(before, d);
-                mine += __shfl_xor(mine, d);
-            }
-            u.kb0 = min(__builtin_amdgcn_readfirstlane(before), p.kb);
-            u.kb1 = min(u.kb0 + __builtin_amdgcn_readfirstlane(mine), p.kb);
+        for (int d = 1; d < 64; d *= 2) {
+            before += __shfl_xor(before, d);
+            mine += __shfl_xor(mine, d);
         }
-        find_tile(unit, p.tiles_m, p.tiles_n, tm, tn);
-        u.m0 = tm * BM;
-        u.m1 = min(p.M, u.m0 + BM);
-        u.tile = unit;
+        u.kb0 = min(__builtin_amdgcn_readfirstlane(before), p.kb);
+        u.kb1 = min(u.kb0 + __builtin_amdgcn_readfirstlane(mine), p.kb);
     }
-    u.n0 = tn * BN;
     return u;
 }
+
+// Up to and with each expert, units of ceil(rows / size) times `per`, in LDS, for workgroups that take one unit after the other.
+struct Experts {
+    int32_t upto[1024], sums[16];
+
+    // By all W waves of the workgroup, a barrier at the end.
+    template <int W>
+    __device__ __forceinline__ void fill(const int32_t *offsets, int32_t E, int32_t S, int32_t size, int32_t per)
+    {
+        const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+        int32_t before = 0;
+        for (int32_t e0 = 0; e0 < E; e0 += 64 * W) {
+            int32_t l, h;
+            positions(offsets, E, S, e0 + tid, l, h);
+            int32_t up = inclusive_scan((h - l + size - 1) / size * per, lane);
+            if (lane == 63) sums[wave] = up;
+            __syncthreads();
+            int32_t all = before;
+            for (int w = 0; w < W; ++w) {
+                if (w == wave) up += all;
+                all += sums[w];
+            }
+            before = all;
+            if (e0 + tid < E) upto[e0 + tid] = up;
+            __syncthreads();
+        }
+    }
+
+    // As find_unit<true>.
+    __device__ __forceinline__ Found find(const int32_t *offsets, int32_t E, int32_t S, int32_t size, int32_t per,
+                                          int32_t id, int lane) const
+    {
+        const int32_t last = min(max(offsets[E], 0), S);
+        const int32_t all = __builtin_amdgcn_readfirstlane(upto[E - 1]);
+        const int32_t total = all + (S - last + size - 1) / size * per;
+        const int32_t x = id & 7, i = id >> 3, q = total >> 3, rem = total & 7;
+        if (i >= q + (x < rem ? 1 : 0)) return Found{-1, 0, S, S};
+        id = x * q + min(x, rem) + i;
+        if (id >= all) return Found{-1, id - all, last, S};
+        int32_t e = 0;
+        for (;; e += 64) {
+            const uint64_t over = __ballot(upto[min(e + lane, E - 1)] > id);
+            if (over) {
+                e += __builtin_ctzll(over);
+                break;
+            }
+        }
+        Found f;
+        f.e = e;
+        f.index = id - (e > 0 ? __builtin_amdgcn_readfirstlane(upto[e - 1]) : 0);
+        positions(offsets, E, S, e, f.lo, f.hi);
+        return f;
+    }
+};
 
 __device__ __forceinline__ i32x8_t whole(const i32x4_t (&v)[2])
 {
@@ -735,6 +813,14 @@ __global__ __launch_bounds__(64 * W) void f8_stream_kernel(Params p)
 // ---- tiles through LDS --------------------------------------------------------
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
+// The lane, for a part of a loop over units: what is made of it there is not kept in
+// registers over the rest of the loop, which has none to spare.
+__device__ __forceinline__ int anew(int lane)
+{
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // Buffer resource for raw byte addressing from `base` on, 2^32 - 1 bytes: what
 // is loaded lies inside the arrays by its rows and columns, which are held to
 // those that exist.
@@ -782,6 +868,8 @@ struct Tile {
     static constexpr int SCALES = (BM > 64 ? BM : 64) * 4;   // bytes of A's: whole loads
     static constexpr int STAGE = (A_BYTES + B_BYTES + SCALES + BN * 4 + 1023) / 1024 * 1024;
     static constexpr int PITCH = BN * 2 + 16;   // of C's rows
+    // of the tile kernel: blocks and bytes of a wave's part for C, its stores of a tile
+    static constexpr int PJ = FM * FN <= 4 ? 1 : FN % 2 == 0 ? 2 : FN, PART = PJ * 32 * 64, STORES = FM * FN * 2;
     static constexpr int LDS = S * STAGE > BM * PITCH ? S * STAGE : BM * PITCH;
     static_assert(BM % 64 == 0 || BM == 32, "whole loads of scales, or half a one");
     static_assert(BN % 64 == 0, "whole loads of scales");
@@ -801,10 +889,15 @@ struct Loads {
     int32_t last, a_rows, b_blocks;
     int wave;
 
-    __device__ __forceinline__ Loads(const Params &p, const Unit &u, const uint8_t *smem, int wave_, int lane)
+    __device__ __forceinline__ Loads(const uint8_t *smem, int wave_) : wave(wave_)
+    {
+        lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
+    }
+
+    __device__ __forceinline__ void set(const Params &p, const Unit &u, int lane)
     {
         constexpr int W = T::W, FM = T::FM, FN = T::FN;
-        wave = wave_;
+        lane = anew(lane);
         const int32_t m0 = u.m0, rows = u.m1 - u.m0, cols = min(T::BN, p.N - u.n0);
         const int64_t bm = MODE == EXPERTS ? u.matrix : 0;
         const bool gather = MODE == EXPERTS && p.top > 0;
@@ -840,7 +933,6 @@ struct Loads {
             const int row = min(d / (32 * FN) * (32 * FN) + d % FN * 32 + d / FN % 32, cols - 1);
             vsb[i] = static_cast<uint32_t>(((u.n0 + row) >> p.b_shift) - (u.n0 >> p.b_shift)) * 4;
         }
-        lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
         as = p.as + (gather ? 0 : m0);
         bs = p.bs + bm * ((p.kb + 3) / 4) * p.b_blocks + (u.n0 >> p.b_shift);
         a_rows = p.a_rows;
@@ -900,44 +992,26 @@ __device__ __forceinline__ void store_tile(const Params &p, const Unit &u, uint1
     }
 }
 
-// A range's sums, in the order in which lanes hold them.
-template <class T>
-__device__ __forceinline__ void store_partial(const Params &p, const Unit &u, const f32x16_t (&acc)[T::FM][T::FN],
-                                              int wave, int lane)
-{
-    const int64_t tiles = p.tiles_m * p.tiles_n;
-    float *to = p.partial + ((u.split * tiles + u.tile) * T::W + wave) * (T::FM * T::FN * 1024) + lane * 4;
-#pragma unroll
-    for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<f32x4_t *>(to + ((i * T::FN + j) * 4 + e) * 256) =
-                    f32x4_t{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
-}
-
-// Zeros: rows of no expert, an expert without rows.
-template <class T>
-__device__ __forceinline__ void store_zeros(const Params &p, const Unit &u, uint16_t *c)
-{
-    for (int o = threadIdx.x; o < T::BM * T::BN / 8; o += 64 * T::W) {
-        const int row = o / (T::BN / 8), col = o % (T::BN / 8) * 8;
-        if (row < u.m1 - u.m0 && u.n0 + col < p.N)
-            store8(c + static_cast<int64_t>(row) * p.N, u.n0 + col, p.N, half8_t{});
-    }
-}
-
 // A block's sums are held to the accumulation registers: a wave's 128 x 128 values
 // need all 256, and the compiler left to itself splits them between both files and
-// spills.  It then cannot see these MFMAs, so the kernel supplies the wait
-// states around them.  (The host's pass of the compiler knows no such registers.)
+// spills.  It then cannot see these MFMAs, so the kernel supplies the wait states
+// around them.  LAST: before the code's next branch, where the compiler may copy
+// sums from register to register, as it did: the wait states of a read of the
+// result, more than any MFMA asks for, are part of the statement.  (The host's
+// pass of the compiler knows no such registers.)
+template <bool LAST>
 __device__ __forceinline__ void mfma(f32x16_t &acc, i32x8_t b, i32x8_t a, uint32_t sb, uint32_t sa)
 {
 #ifdef __HIP_DEVICE_COMPILE__
-    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
-                 : "+a"(acc)
-                 : "v"(b), "v"(a), "v"(sb), "v"(sa));
+    if constexpr (LAST)
+        asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]\n\t"
+                     "s_nop 7\n\ts_nop 7\n\ts_nop 7"
+                     : "+a"(acc)
+                     : "v"(b), "v"(a), "v"(sb), "v"(sa));
+    else
+        asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                     : "+a"(acc)
+                     : "v"(b), "v"(a), "v"(sb), "v"(sa));
 #endif
 }
 
@@ -948,8 +1022,103 @@ __device__ __forceinline__ void keep(f32x16_t &acc)
 #endif
 }
 
+// A range's sums, in the order in which lanes hold them.
+template <class T>
+__device__ __forceinline__ void store_partial(const Params &p, const Unit &u, f32x16_t (&acc)[T::FM][T::FN],
+                                              int wave, int lane)
+{
+    lane = anew(lane);
+    const int64_t tiles = p.tiles_m * p.tiles_n;
+    float *to = p.partial + ((u.split * tiles + u.tile) * T::W + wave) * (T::FM * T::FN * 1024) + lane * 4;
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) {
+            keep(acc[i][j]);   // read here, not before
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<f32x4_t *>(to + ((i * T::FN + j) * 4 + e) * 256) =
+                    f32x4_t{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+            __builtin_amdgcn_sched_barrier(0);
+        }
+}
+
+// Zeros: rows of no expert, an expert without rows.
+template <class T>
+__device__ __forceinline__ void store_zeros(const Params &p, const Unit &u, uint16_t *c)
+{
+    for (int o = anew(threadIdx.x); o < T::BM * T::BN / 8; o += 64 * T::W) {
+        const int row = o / (T::BN / 8), col = o % (T::BN / 8) * 8;
+        if (row < u.m1 - u.m0 && u.n0 + col < p.N)
+            store8(c + static_cast<int64_t>(row) * p.N, u.n0 + col, p.N, half8_t{});
+    }
+}
+
+// C from the waves' sums, by T::STORES stores of the wave where no part of the tile is
+// missing, else after its loads have landed: 32 rows of T::PJ blocks at a time
+// through the wave's own part of LDS, so that lanes write neighbouring columns.
+template <class T, bool ALL>
+__device__ __forceinline__ void store_blocks(const Params &p, const Unit &u, uint16_t *c,
+                                             f32x16_t (&acc)[T::FM][T::FN], uint8_t *part, int wm, int wn, int lane)
+{
+    lane = anew(lane);
+    const int r = lane & 31, h = lane >> 5, rows = u.m1 - u.m0;
+    auto put = [&](int row, int32_t n, half8_t v) {
+        uint16_t *to = c + static_cast<int64_t>(row) * p.N;
+        if constexpr (ALL)
+            *reinterpret_cast<half8_u_t *>(to + n) = v;
+        else if (row < rows && n < p.N)
+            store8(to, n, p.N, v);
+    };
+    auto four = [&](int i, int j, int e) {
+        return __builtin_convertvector(
+            f32x4_t{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]}, half4_t);
+    };
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) {
+        const int row0 = (wm * T::FM + i) * 32;
+        constexpr int CH = T::PJ * 4;   // 16-byte chunks of a row
+#pragma unroll
+        for (int j0 = 0; j0 < T::FN; j0 += T::PJ) {
+            // chunks XORed within fours with the row: lanes' writes spread over the banks
+#pragma unroll
+            for (int j = 0; j < T::PJ; ++j) {
+                keep(acc[i][j0 + j]);   // read here, not before
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<half4_t *>(part + r * (CH * 16) + (j * 4 + (e ^ (r & 3))) * 16 + h * 8) =
+                        four(i, j0 + j, e);
+            }
+            wave_lds_fence();
+#pragma unroll
+            for (int o0 = 0; o0 < 32 * CH; o0 += 64) {
+                const int o = o0 + lane, row = o / CH, ch = o % CH;
+                put(row0 + row, u.n0 + (wn * T::FN + j0) * 32 + ch * 8,
+                    *reinterpret_cast<const half8_t *>(part + row * (CH * 16) + (ch ^ (row & 3)) * 16));
+            }
+            wave_lds_fence();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store_sums(const Params &p, const Unit &u, uint16_t *c,
+                                           f32x16_t (&acc)[T::FM][T::FN], uint8_t *part, int wm, int wn, int lane)
+{
+    if (u.m1 - u.m0 == T::BM && u.n0 + T::BN <= p.N) {
+        store_blocks<T, true>(p, u, c, acc, part, wm, wn, lane);
+    } else {
+        asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+        store_blocks<T, false>(p, u, c, acc, part, wm, wn, lane);
+    }
+}
+
 // Two stages; a step's MFMAs are its two halves' (64 columns), each half's
-// fragments read from LDS while the other's are multiplied.
+// fragments read from LDS while the other's are multiplied.  A workgroup takes one
+// unit after the other without a pause: the last two steps of one load the first
+// groups of the next, and C leaves from registers, its stores waited for by no
+// one.
 template <int MODE, class T, int OCC>
 __global__ __launch_bounds__(64 * T::W)
 __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
@@ -957,15 +1126,45 @@ void f8_tile_kernel(Params p)
 {
     constexpr int FM = T::FM, FN = T::FN, LOADS = T::LOADS;
     static_assert(T::S == 2, "two stages");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+    static_assert(T::STORES <= 63 && T::STORES <= FM * FN * 4, "vmcnt counts at most 63");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::S * T::STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t parts[T::W][T::PART];
+    __shared__ Experts experts;
     const int lane = threadIdx.x & 63, wave = wave_index();
     const int wm = wave / T::WN, wn = wave % T::WN;
     const int r = lane & 31, h = lane >> 5;
-    const Unit u = make_unit<MODE, T::BM, T::BN>(p, lane);
-    if (u.none) return;
-    uint16_t *c = p.c + (MODE == GRAD ? u.matrix * p.M * p.N : 0) + static_cast<int64_t>(u.m0) * p.N;
-    if (MODE != DENSE && u.kb0 >= u.kb1) return store_zeros<T>(p, u, c);
-    const Loads<MODE, T> loads(p, u, smem, wave, lane);
+    if constexpr (MODE == EXPERTS) experts.template fill<T::W>(p.offsets, p.E, p.M, T::BM, p.tiles_n);
+    if constexpr (MODE == GRAD) experts.template fill<T::W>(p.offsets, p.E, p.top, 128, 1);
+    auto c_of = [&](const Unit &u) {
+        return p.c + (MODE == GRAD ? u.matrix * p.M * p.N : 0) + static_cast<int64_t>(u.m0) * p.N;
+    };
+    int32_t id = blockIdx.x;
+    // the next unit that has something to multiply; zeros for those before it
+    auto next = [&](Unit &u) {
+        for (; id < p.units; id += gridDim.x) {
+            if constexpr (MODE == EXPERTS)
+                u = expert_unit<T::BM, T::BN>(p, experts.find(p.offsets, p.E, p.M, T::BM, p.tiles_n, id, lane));
+            else
+                u = matrix_unit<MODE, T::BM, T::BN>(p, id, p.units);
+            if constexpr (MODE == GRAD) {
+                const int32_t e = static_cast<int32_t>(u.matrix);
+                u.kb0 = e > 0 ? min(__builtin_amdgcn_readfirstlane(experts.upto[e - 1]), p.kb) : 0;
+                u.kb1 = min(__builtin_amdgcn_readfirstlane(experts.upto[e]), p.kb);
+            }
+            if (u.none) continue;
+            if (MODE != DENSE && u.kb0 >= u.kb1) {
+                store_zeros<T>(p, u, c_of(u));
+                continue;
+            }
+            id += gridDim.x;
+            return true;
+        }
+        return false;
+    };
+    Unit u, nu;
+    if (!next(u)) return;
+    Loads<MODE, T> loads(smem, wave);
+    loads.set(p, u, lane);
     f32x16_t acc[FM][FN];
     int off[4];   // a lane's 16-byte chunks in a tile's rows
 #pragma unroll
@@ -993,7 +1192,7 @@ void f8_tile_kernel(Params p)
             nb[i] = *reinterpret_cast<const uint32_t *>(st + T::SCALES + ((wn * 32 + r) * FN + i) * 4);
     };
     auto take_scales = [&](int32_t kb) {
-        const int s = 8 * (min(kb, loads.last) & 3);
+        const int s = 8 * (kb & 3);
 #pragma unroll
         for (int i = 0; i < FM; ++i) sa[i] = na[i] >> s;
 #pragma unroll
@@ -1011,28 +1210,25 @@ void f8_tile_kernel(Params p)
 #pragma unroll
         for (int t = 0; t < MFMAS; ++t) {
             const int i = t / FN, j = t % FN;
-            mfma(acc[i][j], whole(bf[kk][j]), whole(af[kk][i]), sb[j], sa[i]);
+            if (kk == 1 && t == MFMAS - 1)
+                mfma<true>(acc[i][j], whole(bf[kk][j]), whole(af[kk][i]), sb[j], sa[i]);
+            else
+                mfma<false>(acc[i][j], whole(bf[kk][j]), whole(af[kk][i]), sb[j], sa[i]);
             each(t);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-#pragma unroll
-    for (int d = 0; d < LOADS; ++d) loads.fetch(0, u.kb0, d);
-#pragma unroll
-    for (int d = 0; d < LOADS; ++d) loads.fetch(1, u.kb0 + 1, d);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(LOADS) : "memory");
-#pragma unroll
-    for (int d = 0; d < READS; ++d) read(0, 0, d);
-    read_scales(0);
-    take_scales(u.kb0);
-    auto step = [&](int stage, int32_t kb) {
+    // One group from `stage`; group `fetch` of `loads` then takes its place, and the
+    // next step's is group `after`.  FIRST of a unit: T::STORES stores of the unit
+    // before or more are behind the loads that are waited for, or those are there.
+    auto step = [&](auto first, int stage, int32_t fetch, int32_t after) {
         compute(0, [&](int t) {
 #pragma unroll
             for (int d = 0; d < READS; ++d)
                 if (d * MFMAS / READS == t) read(stage, 1, d);
         });
         // this stage is read to the end, the next one has landed
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(first ? T::STORES : 0) : "memory");
         read_scales(stage ^ 1);
         compute(1, [&](int t) {
 #pragma unroll
@@ -1040,31 +1236,63 @@ void f8_tile_kernel(Params p)
                 if (d * MFMAS / READS == t) read(stage ^ 1, 0, d);
 #pragma unroll
             for (int d = 0; d < LOADS; ++d)
-                if (d * MFMAS / LOADS == t) loads.fetch(stage, kb + 2, d);
+                if (d * MFMAS / LOADS == t) loads.fetch(stage, fetch, d);
         });
-        take_scales(kb + 1);
+        take_scales(after);
     };
+    auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            acc[i][j] = f32x16_t{};
-            keep(acc[i][j]);
+            for (int j = 0; j < FN; ++j) {
+                acc[i][j] = f32x16_t{};
+                keep(acc[i][j]);
+            }
+        asm volatile("s_nop 4");   // between those writes and the first MFMA
+    };
+    auto fetch_all = [&](int stage, int32_t kb) {
+#pragma unroll
+        for (int d = 0; d < LOADS; ++d) loads.fetch(stage, kb, d);
+    };
+    fetch_all(0, u.kb0);
+    fetch_all(1, u.kb0 + 1);
+    bool more = next(nu);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" : : : "memory");
+#pragma unroll
+    for (int d = 0; d < READS; ++d) read(0, 0, d);
+    read_scales(0);
+    take_scales(u.kb0);
+    clear();
+    for (int stage = 0;;) {
+        if (u.kb1 - u.kb0 == 1 && more) {
+            // the step before could not know the unit after this one
+            loads.set(p, nu, lane);
+            fetch_all(stage ^ 1, nu.kb0);
+            asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
         }
-    asm volatile("s_nop 4");   // between those writes and the first MFMA
-    for (int32_t kb = u.kb0;;) {
-        step(0, kb);
-        if (++kb >= u.kb1) break;
-        step(1, kb);
-        if (++kb >= u.kb1) break;
+        const int32_t over = more ? nu.kb0 - u.kb1 : 0;   // of a group past this unit's last
+        auto group = [&](int32_t kb) { return kb < u.kb1 ? kb : kb + over; };
+        if (u.kb0 + 2 == u.kb1 && more) loads.set(p, nu, lane);
+        step(std::true_type{}, stage, group(u.kb0 + 2), group(u.kb0 + 1));
+        stage ^= 1;
+        for (int32_t kb = u.kb0 + 1; kb < u.kb1; ++kb) {
+            if (kb + 2 == u.kb1 && more) loads.set(p, nu, lane);
+            step(std::false_type{}, stage, group(kb + 2), group(kb + 1));
+            stage ^= 1;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (MODE == DENSE && p.splits > 1)
+            store_partial<T>(p, u, acc, wave, lane);
+        else
+            store_sums<T>(p, u, c_of(u), acc, parts[wave], wm, wn, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        if (!more) break;
+        clear();
+        u = nu;
+        more = next(nu);
     }
-    // wait states between the last MFMA and the first read of what it wrote: more
-    // than any MFMA asks for; and no load may still be on its way to this LDS
-    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_waitcnt vmcnt(0)" : : : "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    if (MODE == DENSE && p.splits > 1) return store_partial<T>(p, u, acc, wave, lane);
-    __syncthreads();
-    store_tile<MODE, T>(p, u, c, smem, acc, wm, wn, lane);
+    // no load may still be on its way to this LDS
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 }
 
 // A ring of S stages for few rows, where reading B bounds the call: S - 1 groups
@@ -1084,7 +1312,8 @@ __global__ __launch_bounds__(64 * T::W) void f8_ring_kernel(Params p)
     if (u.none) return;
     uint16_t *c = p.c + (MODE == GRAD ? u.matrix * p.M * p.N : 0) + static_cast<int64_t>(u.m0) * p.N;
     if (MODE != DENSE && u.kb0 >= u.kb1) return store_zeros<T>(p, u, c);
-    const Loads<MODE, T> loads(p, u, smem, wave, lane);
+    Loads<MODE, T> loads(smem, wave);
+    loads.set(p, u, lane);
     f32x16_t acc[FM][FN] = {};
     int off[4];
 #pragma unroll
@@ -1300,19 +1529,20 @@ struct Kernel {
     int32_t lds;               // for the waves' sums
     int32_t wn, fm, fn;        // of a kernel whose K may be split
     int32_t slots;             // workgroups on a compute unit
+    bool persistent;           // which take one unit after the other
     double start, step, full;  // us: a workgroup's start and end, 128 columns with one and with all slots taken
     const void *run[3];        // by mode
 };
 #define STREAM(W, Q)                                                                              \
-    {GEMM_F16_LOWBIT_STREAM, 16, 16, W, W * 1024, 0, 0, 0, 0, 0, 0, 0,                            \
+    {GEMM_F16_LOWBIT_STREAM, 16, 16, W, W * 1024, 0, 0, 0, 0, false, 0, 0, 0,                            \
      {address(f8_stream_kernel<DENSE, W, Q>), address(f8_stream_kernel<EXPERTS, W, Q>), nullptr}}
 #define TILE(WM, WN, FM, FN, OCC, START, STEP, FULL)                                              \
-    {GEMM_F16_LOWBIT_TILE, WM * FM * 32, WN * FN * 32, WM * WN, 0, WN, FM, FN, OCC, START, STEP, FULL, \
+    {GEMM_F16_LOWBIT_TILE, WM * FM * 32, WN * FN * 32, WM * WN, 0, WN, FM, FN, OCC, true, START, STEP, FULL, \
      {address(f8_tile_kernel<DENSE, Tile<WM, WN, FM, FN, 2>, OCC>),                               \
       address(f8_tile_kernel<EXPERTS, Tile<WM, WN, FM, FN, 2>, OCC>),                             \
       address(f8_tile_kernel<GRAD, Tile<WM, WN, FM, FN, 2>, OCC>)}}
 #define RING(WM, WN, FM, FN, S, START, STEP, FULL)                                                \
-    {GEMM_F16_LOWBIT_TILE, WM * FM * 32, WN * FN * 32, WM * WN, 0, WN, FM, FN, 2, START, STEP, FULL, \
+    {GEMM_F16_LOWBIT_TILE, WM * FM * 32, WN * FN * 32, WM * WN, 0, WN, FM, FN, 2, false, START, STEP, FULL, \
      {address(f8_ring_kernel<DENSE, Tile<WM, WN, FM, FN, S>>),                                    \
       address(f8_ring_kernel<EXPERTS, Tile<WM, WN, FM, FN, S>>),                                  \
       address(f8_ring_kernel<GRAD, Tile<WM, WN, FM, FN, S>>)}}
@@ -1329,7 +1559,7 @@ constexpr int32_t TILES = 6, STREAM8 = 6, STREAM16 = 7;
 
 // The kernel of a call, an index of kKernels, and the ranges of K (dense).
 struct Choice {
-    int32_t id, splits;
+    int32_t id, splits, units;
 };
 
 // Time in us of `wgs` workgroups with `steps` groups of columns each, their K in
@@ -1385,7 +1615,7 @@ static Choice search(const Call &c, int32_t num_cus)
             const double us = model(e, wgs, steps, splits, bytes, num_cus);
             if (best_us > 0 && us >= best_us) return;
             best_us = us;
-            best = Choice{id, static_cast<int32_t>(splits)};
+            best = Choice{id, static_cast<int32_t>(splits), 0};
         };
         if (c.mode == GRAD) {
             consider(E * static_cast<double>(tiles), c.top > 64.0 * E ? c.top / E / GROUP + 0.5 : 1.0, 1);
@@ -1459,7 +1689,9 @@ static int plan_call(const Call &c, int32_t num_cus, gemm_f16_lowbit_plan_t *pla
     plan->block_n = e.bn;
     plan->waves = e.waves;
     plan->splits = r->splits;
-    plan->grid = static_cast<int32_t>(grid);
+    // the tile kernels' workgroups take several units each
+    plan->grid = static_cast<int32_t>(e.persistent ? std::min<int64_t>(grid, int64_t(num_cus) * e.slots) : grid);
+    r->units = static_cast<int32_t>(grid);
     if (r->splits > 1) plan->workspace_bytes = r->splits * partial_bytes(c, e);
     if (c.a_f16 && r->id < TILES)
         plan->workspace_bytes += round_up(c.a.codes, 256) + round_up(c.a.scales, 256);
@@ -1492,6 +1724,7 @@ static int run_call(const Call &c, const void *X, const void *a_codes, const voi
     Params p;
     const int64_t partial = plan.splits > 1 ? partial_bytes(c, e) : 0;
     p.partial = reinterpret_cast<float *>(ws + a_bytes);
+    p.units = r.units;
     p.splits = plan.splits;
     p.kb_split = static_cast<int32_t>(cdiv(c.a.kp / GROUP, plan.splits));
     p.a = static_cast<const uint8_t *>(a_codes);

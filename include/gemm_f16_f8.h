@@ -93,7 +93,8 @@ int gemm_f16_f8_dequantize(int64_t count, int64_t R, int64_t K, int32_t block,
  * workspaces unless they are ordered on one stream.
  *
  * gemm_f16_nt_f8_plan: pure host function, what a call on a device with num_cus
- * compute units runs; a_f16: A given in fp16.
+ * compute units runs; a_f16: A given in fp16.  (Where there are more tiles than fit
+ * on the device at once, the plan's workgroups take several each.)
  *
  * M = 0 or N = 0: nothing to compute.  K = 0: C is filled with +0.
  * GEMM_F16_UNSUPPORTED for sizes that gemm_f16_f8_sizes refuses for A or B, or
