@@ -68,7 +68,36 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
     return __builtin_amdgcn_readlane(v, 63);
 }
 
+// The sum of 64 lanes' values, in every lane: the same steps, added pairwise.
+__device__ __forceinline__ double wave_sum64(double v)
+{
+#define STEP(CTRL, ROWS)                                                                          \
+    {                                                                                             \
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);                                       \
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(b), CTRL, ROWS, 0xf, false); \
+        const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(b >> 32), CTRL, ROWS, 0xf, false); \
+        v += __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);                    \
+    }
+    STEP(0x111, 0xf);   // row_shr 1, 2, 4, 8
+    STEP(0x112, 0xf);
+    STEP(0x114, 0xf);
+    STEP(0x118, 0xf);
+    STEP(0x142, 0xa);   // row_bcast 15, 31
+    STEP(0x143, 0xc);
+#undef STEP
+    return readlane64(v, 63);
+}
+
 // Numbers as integers in the same order (no NaN among them).
+__device__ __forceinline__ uint32_t ordered(float v)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    return b >> 31 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t b)
+{
+    return __builtin_bit_cast(float, b >> 31 ? b & 0x7fffffffu : ~b);
+}
 __device__ __forceinline__ uint64_t ordered(double v)
 {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -110,19 +139,18 @@ __device__ __forceinline__ bool scores_of(const double (&x)[V], bool sigmoid, do
         for (int i = 0; i < V; ++i) s[i] = 1.0 / (1.0 + exp(-x[i]));
         return true;
     }
-    double m = -inf;
+    // the largest, exactly: logits are fp32 numbers
+    uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = fmax(m, x[i]);
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) m = fmax(m, shfl_xor64(m, d));
+    for (int i = 0; i < V; ++i) most = max(most, ordered(static_cast<float>(x[i])));
+    const double m = static_cast<double>(unordered(wave_max(most)));
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         s[i] = x[i] == -inf ? 0.0 : exp(x[i] - m);
         sum += s[i];
     }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) sum += shfl_xor64(sum, d);
+    sum = wave_sum64(sum);
     const double by = sum > 0.0 ? sum : 1.0;
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] /= by;
@@ -395,10 +423,11 @@ __global__ __launch_bounds__(1024) void order_kernel(OrderParams p)
     order_chunk<false>(p, blockIdx.x, 0, m);
 }
 
-// Up to 16 tokens: their choice, a wave each, and the order in one launch.
+// Up to 16 tokens: their choice, a wave each, and the order in one launch.  SMALL: up
+// to 64 slots, which the first wave orders by comparing them all.
 constexpr int FEW = 16;
 
-template <int V>
+template <int V, bool SMALL>
 __global__ __launch_bounds__(1024) void route_few_kernel(RouteParams p, OrderParams o)
 {
     __shared__ union {
@@ -406,14 +435,37 @@ __global__ __launch_bounds__(1024) void route_few_kernel(RouteParams p, OrderPar
         OrderMemory m;
     } u;
     __shared__ int32_t chosen[FEW * MOST_TOP];
-    const int lane = threadIdx.x & 63, wave = wave_index();
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
     if (wave < p.T) {
         const int32_t e = route_token<V>(p, wave, lane, u.cs[wave]);
         if (lane < p.top) chosen[wave * p.top + lane] = e;
     }
     __syncthreads();
-    const int tid = threadIdx.x;
-    order_chunk<true>(o, 0, tid < o.S ? chosen[tid] : -1, u.m);
+    if constexpr (!SMALL) {
+        order_chunk<true>(o, 0, tid < o.S ? chosen[tid] : -1, u.m);
+        return;
+    }
+    if (wave > 0) return;
+    const uint32_t E = static_cast<uint32_t>(o.E), mine = lane < o.S ? expert_of(chosen[lane], o.E) : E;
+    int32_t at = 0, all = 0, before[V] = {};   // slots of the experts before l, l + 64, ...
+    for (int32_t s = 0; s < o.S; ++s) {
+        const uint32_t e = __builtin_amdgcn_readlane(mine, s);
+        if (e == E) continue;
+        ++all;
+        if (e < mine || (e == mine && s < lane)) ++at;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e < static_cast<uint32_t>(i * 64 + lane)) ++before[i];
+    }
+    if (lane < o.S) {
+        if (mine < E) o.rows[at] = lane;
+        if (lane >= all) o.rows[lane] = -1;
+        o.places[lane] = mine < E ? at : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (i * 64 + lane < o.E) o.offsets[i * 64 + lane] = before[i];
+    if (lane == 0) o.offsets[E] = all;
 }
 
 // ---------------------------------------------------------------------------
@@ -486,8 +538,7 @@ __global__ __launch_bounds__(256) void route_back_kernel(RouteBackParams p)
     if (!p.sigmoid && fine) {
 #pragma unroll
         for (int i = 0; i < V; ++i) dot += d[i] * s[i];
-#pragma unroll
-        for (int k = 1; k < 64; k *= 2) dot += shfl_xor64(dot, k);
+        dot = wave_sum64(dot);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -695,14 +746,9 @@ static const void *by_experts(int64_t E)
     return Of<16>::get();
 }
 template <int V>
-struct RouteFewOf {
-    static const void *get()
-    {
-        // more scores than that leave too few registers to 16 waves
-        if constexpr (V <= 8) return address(route_few_kernel<V>);
-        return nullptr;
-    }
-};
+struct RouteFewOf { static const void *get() { return address(route_few_kernel<V, false>); } };
+template <int V>
+struct RouteSmallOf { static const void *get() { return address(route_few_kernel<V, true>); } };
 template <int V>
 struct RouteOf { static const void *get() { return address(route_kernel<V>); } };
 template <int V>
@@ -789,7 +835,9 @@ extern "C" int gemm_f16_route(int64_t T, int64_t E, int32_t top, int32_t scores,
     p.sigmoid = scores == GEMM_F16_ROUTE_SIGMOID;
     p.group_max = group_max != 0;
     p.renormalize = renormalize != 0;
-    if (T <= FEW && E <= 512) return launch(by_experts<RouteFewOf>(E), 1, 1024, &p, stream, &o);
+    if (T <= FEW && S <= 64)
+        return launch(by_experts<RouteSmallOf>(E), 1, static_cast<int>(std::max<int64_t>(T, 1)) * 64, &p, stream, &o);
+    if (T <= FEW) return launch(by_experts<RouteFewOf>(E), 1, 1024, &p, stream, &o);
     const int64_t grid = cdiv(T, 4);
     if (grid * 256 >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
     if (T > 0) v = launch(by_experts<RouteOf>(E), grid, 256, &p, stream);

@@ -1547,9 +1547,9 @@ struct Kernel {
       address(f8_ring_kernel<EXPERTS, Tile<WM, WN, FM, FN, S>>),                                  \
       address(f8_ring_kernel<GRAD, Tile<WM, WN, FM, FN, S>>)}}
 static const Kernel kKernels[] = {
-    TILE(2, 2, 4, 4, 1, 6.81, 0.936, 0.936), TILE(2, 2, 4, 3, 1, 6.02, 0.761, 0.761),
-    TILE(2, 2, 2, 2, 2, 2.35, 0.540, 0.721), RING(1, 2, 1, 1, 6, 1.25, 0.210, 0.254),
-    RING(2, 2, 1, 1, 4, 1.27, 0.239, 0.364), RING(1, 4, 2, 1, 3, 1.58, 0.351, 0.572),
+    TILE(2, 2, 4, 4, 1, 6.26, 1.022, 1.022), TILE(2, 2, 4, 3, 1, 5.43, 0.849, 0.849),
+    TILE(2, 2, 2, 2, 2, 1.91, 0.586, 0.794), RING(1, 2, 1, 1, 6, 1.26, 0.208, 0.249),
+    RING(2, 2, 1, 1, 4, 1.27, 0.231, 0.341), RING(1, 4, 2, 1, 3, 1.54, 0.347, 0.563),
     STREAM(8, 2), STREAM(16, 2),
 };
 #undef TILE
@@ -1573,18 +1573,18 @@ static double model(const Kernel &e, double wgs, double steps, int64_t splits, d
     const double taken = e.full * steps + e.start * e.slots, tile = static_cast<double>(e.bm) * e.bn;
     double us = all * taken;
     if (rest > 0) us += rest <= cus ? e.step * steps + e.start : taken;
-    const double memory = bytes / 5.757e6, matrix = wgs * tile * steps * GROUP / 1.052e9;
+    const double memory = bytes / 5.475e6, matrix = wgs * tile * steps * GROUP / 9.928e8;
     auto fourth = [](double x) { return x * x * x * x; };
     us = std::sqrt(std::sqrt(fourth(us) + fourth(memory) + fourth(matrix)));
-    return us + 2.82 + (splits > 1 ? 1.93 + 4.0 * wgs * tile / 4.42e6 : 0.0);
+    return us + 3.16 + (splits > 1 ? 1.76 + 4.0 * wgs * tile / 5.045e6 : 0.0);
 }
 
-// The tile and ring kernels and ranges of K by that model, fitted to 3,700 timings
-// of 182 shapes (1 to 8192 rows, N and K of 64 to 16384, 8 to 256 experts, operands from
-// HBM; they are not kept with the source).  Its error is 10 to 18%; what it chose took 1.7%
-// (products), 2.7% (experts) and 1.5% (gradients) longer than the best of each
-// shape in the mean, 15, 46 and 14% in the worst (2355 tokens, 8 of 64 experts, 1600 x 256:
-// 51.8 us, with 128 x 128 tiles 35.6).
+// The tile and ring kernels and ranges of K by that model, fitted to 2,200 timings
+// of 144 shapes (1 to 8192 rows, N and K of 64 to 16384, 8 to 256 experts, operands from
+// HBM; they are not kept with the source).  Its error is 6 to 19%; what it chose took 2.7%
+// (products), 1.6% (experts) and 2.3% (gradients) longer than the best of each
+// shape in the mean, 13, 40 and 12% in the worst (2095 tokens, 2 of 256 experts, 3264 x 192:
+// 91.6 us, with 128 x 128 tiles 65.3).
 static Choice search(const Call &c, int32_t num_cus)
 {
     const double M = static_cast<double>(c.M), N = static_cast<double>(c.N), K = static_cast<double>(c.a.kp);
@@ -1620,7 +1620,9 @@ static Choice search(const Call &c, int32_t num_cus)
         if (c.mode == GRAD) {
             consider(E * static_cast<double>(tiles), c.top > 64.0 * E ? c.top / E / GROUP + 0.5 : 1.0, 1);
         } else if (c.mode == EXPERTS) {
-            const double down = std::max(used, M / e.bm + (M > 0.5 * e.bm * used ? 0.5 : 1.0) * used);
+            // tiles of an expert whose rows are anything up to twice the mean
+            const double most = 2.0 * M / (used * e.bm), whole = std::floor(most);
+            const double down = used * (most <= 1.0 ? 1.0 : (0.5 * whole + most - whole) * (whole + 1.0) / most);
             consider(std::ceil(static_cast<double>(cdiv(c.N, e.bn)) * down), static_cast<double>(kb), 1);
         } else {
             int64_t last = 0;
