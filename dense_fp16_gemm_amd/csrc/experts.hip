@@ -162,19 +162,19 @@ __device__ __forceinline__ int32_t route_token(const RouteParams &p, int32_t t, 
 {
     constexpr double inf = __builtin_huge_val();
     double x[V], s[V], c[V];
+    float bias[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int32_t e = i * 64 + lane;
         x[i] = e < p.E ? load_logit(p.logits, p.f32, static_cast<int64_t>(t) * p.E + e) : -inf;
+        bias[i] = p.bias && e < p.E ? p.bias[e] : 0.0f;
     }
     bool fine = scores_of(x, p.sigmoid, s);
     if (fine) {
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int32_t e = i * 64 + lane;
-            c[i] = s[i];
-            if (p.bias && e < p.E) c[i] += static_cast<double>(p.bias[e]);
+            c[i] = s[i] + static_cast<double>(bias[i]);
             if (x[i] == -inf) c[i] = -inf;
             bad |= !(c[i] == c[i]);
         }

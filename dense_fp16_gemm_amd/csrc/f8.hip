@@ -567,17 +567,31 @@ template <int MODE, int BM, int BN>
 __device__ __forceinline__ Unit matrix_unit(const Params &p, int32_t id, int32_t count)
 {
     Unit u{};
-    int32_t unit = xcd_unit(id, count), tm, tn;
+    int32_t unit = 0, tm, tn;
     u.kb1 = p.kb;
+    if constexpr (MODE == GRAD) {
+        // Each XCD (workgroups mod 8) takes a share of every expert's tiles, since some
+        // have many more rows than others: of the e-th expert the share x + e mod 8,
+        // which makes eight experts' shares even.
+        const int32_t tiles = p.tiles_m * p.tiles_n, q = tiles >> 3, rem = tiles & 7;
+        const int32_t x = id & 7, i = id >> 3, eight = i / tiles;
+        int32_t at = i - eight * tiles, e = 0, share = x;
+        for (; e < 7; ++e, share = (share + 1) & 7) {
+            const int32_t mine = q + (share < rem ? 1 : 0);
+            if (at < mine) break;
+            at -= mine;
+        }
+        u.matrix = eight * 8 + e;
+        u.none = u.matrix >= p.E;
+        unit = share * q + min(share, rem) + at;
+    } else {
+        unit = xcd_unit(id, count);
+    }
     if (MODE == DENSE && p.splits > 1) {
         u.split = unit % p.splits;
         unit /= p.splits;
         u.kb0 = u.split * p.kb_split;
         u.kb1 = min(u.kb0 + p.kb_split, p.kb);
-    }
-    if constexpr (MODE == GRAD) {
-        u.matrix = unit / (p.tiles_m * p.tiles_n);
-        unit -= static_cast<int32_t>(u.matrix) * p.tiles_m * p.tiles_n;
     }
     find_tile(unit, p.tiles_m, p.tiles_n, tm, tn);
     u.m0 = tm * BM;
@@ -594,7 +608,7 @@ __device__ __forceinline__ Unit make_unit(const Params &p, int lane)
     if constexpr (MODE == EXPERTS)
         return expert_unit<BM, BN>(p, find_unit<true>(p.offsets, p.E, p.M, BM, p.tiles_n, blockIdx.x, lane));
     Unit u = matrix_unit<MODE, BM, BN>(p, blockIdx.x, gridDim.x);
-    if constexpr (MODE == GRAD) {
+    if (MODE == GRAD && !u.none) {
         int32_t before = 0, mine = 0;
         for (int32_t e = lane; e <= u.matrix; e += 64) {
             int32_t lo, hi;
@@ -1146,7 +1160,7 @@ void f8_tile_kernel(Params p)
                 u = expert_unit<T::BM, T::BN>(p, experts.find(p.offsets, p.E, p.M, T::BM, p.tiles_n, id, lane));
             else
                 u = matrix_unit<MODE, T::BM, T::BN>(p, id, p.units);
-            if constexpr (MODE == GRAD) {
+            if (MODE == GRAD && !u.none) {
                 const int32_t e = static_cast<int32_t>(u.matrix);
                 u.kb0 = e > 0 ? min(__builtin_amdgcn_readfirstlane(experts.upto[e - 1]), p.kb) : 0;
                 u.kb1 = min(__builtin_amdgcn_readfirstlane(experts.upto[e]), p.kb);
@@ -1677,7 +1691,7 @@ static int plan_call(const Call &c, int32_t num_cus, gemm_f16_lowbit_plan_t *pla
     *plan = gemm_f16_lowbit_plan_t{};
     plan->splits = 1;
     if (num_cus <= 0) return GEMM_F16_INVALID_ARG;
-    const int64_t matrices = c.mode == GRAD ? c.matrices : 1;
+    const int64_t matrices = c.mode == GRAD ? round_up(c.matrices, 8) : 1;
     if (cdiv(c.M, 16) * cdiv(c.N, 16) > INT32_MAX / matrices) return GEMM_F16_UNSUPPORTED;
     if (c.M == 0 || c.N == 0) return GEMM_F16_OK;
     *r = choose(c, num_cus);
@@ -2038,7 +2052,7 @@ extern "C" int gemm_f16_nt_f8_experts_grad(int64_t S, int64_t E, int64_t M, int6
     v = shape_of(1, M, columns, 1, &c.a);
     if (v == GEMM_F16_OK) v = shape_of(1, N, columns, 1, &c.b);
     if (v != GEMM_F16_OK) return v;
-    if (cdiv(M, 16) * cdiv(N, 16) > INT32_MAX / E) return GEMM_F16_UNSUPPORTED;
+    if (cdiv(M, 16) * cdiv(N, 16) > INT32_MAX / round_up(E, 8)) return GEMM_F16_UNSUPPORTED;
     const Array arrays[6] = {{a_codes, c.a.codes, 16, false}, {a_scales, c.a.scales, 4, false},
                              {b_codes, c.b.codes, 16, false}, {b_scales, c.b.scales, 4, false},
                              {offsets, (E + 1) * 4, 4, false}, {C, E * M * N * 2, 2, true}};

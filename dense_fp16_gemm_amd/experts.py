@@ -25,10 +25,10 @@ ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 def _bind_torch() -> None:
-    global torch, _f16, _f32, _int32, _uint8, _lib
+    global torch, _f16, _f32, _int32, _uint8, _empty, _lib
     f8._bind_torch()
     t = f8.torch
-    _f16, _f32, _int32, _uint8 = t.float16, t.float32, t.int32, t.uint8
+    _f16, _f32, _int32, _uint8, _empty = t.float16, t.float32, t.int32, t.uint8, t.empty_strided
     _lib = load()
     torch = t
 
@@ -249,8 +249,11 @@ def route(logits, top: int, scores: str = "softmax", bias=None, groups: int = 1,
     top, index = int(top), logits.get_device()
     # one allocation: experts, weights, rows, places and offsets
     slots = t * top
-    memory = _new(logits, stream, (4 * slots + e + 1,), _int32)
-    experts, weights, rows, places, offsets = memory.split((slots, slots, slots, slots, e + 1))
+    size = 4 * slots + e + 1
+    memory = _empty((size,), (1,), dtype=_int32, device=logits.device) if stream is None else \
+        _new(logits, stream, (size,), _int32)
+    experts, weights, rows, places, offsets = \
+        memory.split_with_sizes((slots, slots, slots, slots, e + 1))
     experts, places = experts.view(t, top), places.view(t, top)
     weights = weights.view(_f32).view(t, top)
     key = (t, e, top)
@@ -260,11 +263,11 @@ def route(logits, top: int, scores: str = "softmax", bias=None, groups: int = 1,
             _route_bytes.clear()
         need = _route_bytes[key] = gemm_f16_route_workspace(t, e, top)
     ws = _new(logits, stream, (need,), _uint8) if need else None
+    at, each = memory.data_ptr(), 4 * slots
     _call(index, stream, _lib.gemm_f16_route, t, e, top, ROUTE_SCORES[scores], groups, top_groups,
           group_score == "max", bool(renormalize), scale, logits.data_ptr(),
-          logits.dtype is _f32, 0 if bias is None else bias.data_ptr(), experts.data_ptr(),
-          weights.data_ptr(), rows.data_ptr(), places.data_ptr(), offsets.data_ptr(),
-          0 if ws is None else ws.data_ptr(), need)
+          logits.dtype is _f32, 0 if bias is None else bias.data_ptr(), at, at + each,
+          at + 2 * each, at + 3 * each, at + 4 * each, 0 if ws is None else ws.data_ptr(), need)
     if stream is not None:
         _record(stream, logits, bias, ws)
     return Routing.__new__(Routing)._set(experts, weights, rows, places, offsets, scores,

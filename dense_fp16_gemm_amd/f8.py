@@ -161,7 +161,12 @@ class F8Matrix:
 def _new_f8(on, stream, count: tuple, r: int, k: int, block: int) -> F8Matrix:
     codes, scales = _f8_shapes(count, r, k, block)
     q = F8Matrix.__new__(F8Matrix)
-    return q._set(_new(on, stream, codes, _f8), _new(on, stream, scales, _uint8), k, block)
+    if stream is not None or count:
+        return q._set(_new(on, stream, codes, _f8), _new(on, stream, scales, _uint8), k, block)
+    # by torch's quickest way
+    device, blocks = on.device, scales[1]
+    return q._set(_empty(codes, (codes[1], 1), dtype=_f8, device=device),
+                  _empty(scales, (4 * blocks, 4, 1), dtype=_uint8, device=device), k, block)
 
 
 def quantize_f8(x, block: int = 1, transposed: bool = False, stream=None) -> F8Matrix:

@@ -430,7 +430,8 @@ def _plan_workspace(key) -> int:
 def _workspace(need, on, workspace, stream):
     """(tensor, its address, its bytes)."""
     if workspace is None:
-        workspace = _new(on, stream, (need,), torch.uint8)
+        workspace = _empty((need,), (1,), dtype=torch.uint8, device=on.device) if stream is None \
+            else _new(on, stream, (need,), torch.uint8)
         return workspace, workspace.data_ptr(), need
     if not workspace.is_cuda or workspace.device != on.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the operands' device")
