@@ -44,12 +44,14 @@ __device__ __forceinline__ double shfl_xor64(double v, int d)
     return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-__device__ __forceinline__ double readlane64(double v, int lane)
+template <class T>
+__device__ __forceinline__ T readlane64(T v, int lane)
 {
+    static_assert(sizeof(T) == 8, "two registers");
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(b), lane);
     const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), lane);
-    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+    return __builtin_bit_cast(T, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
 // The largest of 64 lanes' values, in every lane: five steps within the wave's
@@ -232,30 +234,41 @@ __device__ __forceinline__ int32_t route_token(const RouteParams &p, int32_t t, 
     int32_t mine = -1;
     double weight = 0.0, total = 0.0;
     for (int j = 0; j < p.top; ++j) {
+        // the lane's highest, its lowest index first
         uint64_t best = key[0];
+        int at = 0;
 #pragma unroll
-        for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
-        const uint32_t hi = wave_max(static_cast<uint32_t>(best >> 32));
-        const uint32_t lo = wave_max(best >> 32 == hi ? static_cast<uint32_t>(best) : 0u);
-        const uint64_t top = static_cast<uint64_t>(hi) << 32 | lo;
-        if (top <= none) break;
-        // the lowest expert that has it
-        uint32_t at = 0;
-#pragma unroll
-        for (int i = V - 1; i >= 0; --i)
-            if (key[i] == top) at = ~static_cast<uint32_t>(i * 64 + lane);
-        const int32_t e = static_cast<int32_t>(~wave_max(at));
+        for (int i = 1; i < V; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const uint32_t hi = static_cast<uint32_t>(best >> 32);
+        uint32_t e = static_cast<uint32_t>(at * 64 + lane);
+        const uint32_t most = wave_max(hi);
+        uint64_t has = __ballot(hi == most);
+        if (has & (has - 1)) {
+            // several lanes with the same upper halves: the lower ones, then the lowest
+            // expert
+            const uint32_t lo = wave_max(hi == most ? static_cast<uint32_t>(best) : 0u);
+            const bool top = hi == most && static_cast<uint32_t>(best) == lo;
+            const uint32_t first = ~wave_max(top ? ~e : 0u);
+            has = __ballot(top && e == first);
+        }
+        const int from = __builtin_ctzll(has);
+        if (readlane64(best, from) <= none) break;
+        e = __builtin_amdgcn_readlane(e, from);
         double v = 0.0;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (e == i * 64 + lane) {
+            if (e == static_cast<uint32_t>(i * 64 + lane)) {
                 key[i] = 0;
                 v = s[i];
             }
-        v = readlane64(v, e & 63);
+        v = readlane64(v, from);
         total += v;
         if (lane == j) {
-            mine = e;
+            mine = static_cast<int32_t>(e);
             weight = v;
         }
     }
@@ -481,13 +494,17 @@ struct RouteBackParams {
     bool f32, sigmoid, renormalize;
 };
 
+// Scores go to LDS, where lane j takes that of choice j, and the choices' gradients
+// come back the same way.  8191 tokens of 128 experts, 6 chosen:
 template <int V>
 __global__ __launch_bounds__(256) void route_back_kernel(RouteBackParams p)
 {
     constexpr double inf = __builtin_huge_val();
-    const int lane = threadIdx.x & 63;
-    const int32_t t = blockIdx.x * 4 + wave_index();
+    __shared__ double memory[4][64 * V];
+    const int lane = threadIdx.x & 63, wave = wave_index();
+    const int32_t t = blockIdx.x * 4 + wave;
     if (t >= p.T) return;
+    double *const ls = memory[wave];
     double x[V], s[V], d[V];
     const int64_t row = static_cast<int64_t>(t) * p.E;
 #pragma unroll
@@ -502,43 +519,39 @@ __global__ __launch_bounds__(256) void route_back_kernel(RouteBackParams p)
         const int64_t at = static_cast<int64_t>(t) * p.top + lane;
         mine = p.experts[at];
         if (mine < 0 || mine >= p.E) mine = -1;
-        if (mine >= 0) dw = static_cast<double>(p.dweights[at]);
-        const float w = p.weights[at];
+        const float w = p.weights[at], g = p.dweights[at];
+        if (mine >= 0) dw = static_cast<double>(g);
         bad = !(w == w);
     }
-    bool fine = scores_of(x, p.sigmoid, s) && !__any(bad);
-    // sums over the choices: of their scores, and of those times dw
-    double total = 0.0, inner = 0.0;
-    if (fine) {
-        for (int j = 0; j < p.top; ++j) {
-            const int32_t e = __builtin_amdgcn_readlane(mine, j);
-            if (e < 0) continue;
-            double v = 0.0;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (e == i * 64 + lane) v = s[i];
-            v = readlane64(v, e & 63);
-            total += v;
-            inner += v * readlane64(dw, j);
-        }
-    }
-    total += 1e-20;
-    const double by = p.renormalize ? p.scale / total : p.scale;
-    const double less = p.renormalize ? inner / total : 0.0;
-    double dot = 0.0;
+    const bool fine = scores_of(x, p.sigmoid, s) && !__any(bad);
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = 0.0;
-    for (int j = 0; j < p.top; ++j) {
-        const int32_t e = __builtin_amdgcn_readlane(mine, j);
-        const double g = by * (readlane64(dw, j) - less);
+    double dot = 0.0;
+    if (fine) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (e == i * 64 + lane) d[i] += g;
-    }
-    if (!p.sigmoid && fine) {
+        for (int i = 0; i < V; ++i) ls[i * 64 + lane] = s[i];
+        wave_lds_fence();
+        const double own = mine >= 0 ? ls[mine] : 0.0;
+        wave_lds_fence();
 #pragma unroll
-        for (int i = 0; i < V; ++i) dot += d[i] * s[i];
-        dot = wave_sum64(dot);
+        for (int i = 0; i < V; ++i) ls[i * 64 + lane] = 0.0;
+        wave_lds_fence();
+        // sums over the choices: of their scores, and of those times dw
+        double by = p.scale, less = 0.0;
+        if (p.renormalize) {
+            const double total = wave_sum64(own) + 1e-20;
+            by = p.scale / total;
+            less = wave_sum64(own * dw) / total;
+        }
+        const double g = by * (dw - less);
+        if (mine >= 0) atomicAdd(&ls[mine], g);   // an expert is chosen once, unless the caller says so
+        wave_lds_fence();
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = ls[i * 64 + lane];
+        if (!p.sigmoid) {
+            // sum of d s, which is where an expert was chosen
+            dot = wave_sum64(mine >= 0 ? g * own : 0.0);
+        }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
