@@ -70,11 +70,6 @@ __device__ __forceinline__ void store8(uint16_t *row, int32_t c, int32_t cols, h
         if (c + i < cols) row[c + i] = bits_as<uint16_t>(_Float16(v[i]));
 }
 
-__device__ __forceinline__ float half_of(u32x4_t v, int i)
-{
-    return static_cast<float>(bits_as<_Float16>(static_cast<uint16_t>(v[i / 2] >> (16 * (i % 2)))));
-}
-
 __device__ __forceinline__ u16x2_t max2(u16x2_t a, uint32_t b)
 {
     return __builtin_elementwise_max(a, bits_as<u16x2_t>(b & 0x7fff7fffu));
@@ -115,15 +110,22 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t big)
     return big == 0 ? 95u : max(static_cast<int32_t>(s), 95);
 }
 
-// 1 / scale; byte from 95 to 135.
-__device__ __forceinline__ float inverse(uint32_t byte) { return bits_as<float>((254u - byte) << 23); }
-
-// Four codes of products that are exact (a half times a power of two), rounded
-// by the conversion to nearest, ties to even.
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d)
+// Four codes of two pairs of halves over the scale of `byte` (95 to 135): quotients by
+// a power of two are exact, and the conversion rounds them to nearest, ties to
+// even.  (Through fp32 and a product a value takes 3.5 instructions instead of one
+// half.)
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, uint32_t byte)
 {
-    int32_t v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true));
+    const float s = bits_as<float>(byte << 23);
+    i16x2_t w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, bits_as<half2_t>(a), s, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, bits_as<half2_t>(b), s, true);
+    return bits_as<uint32_t>(w);
+}
+
+__device__ __forceinline__ u32x2_t codes8(u32x4_t v, uint32_t byte)
+{
+    return u32x2_t{codes4(v[0], v[1], byte), codes4(v[2], v[3], byte)};
 }
 
 // Between a wave's LDS writes and its other lanes' reads of them: see that the
@@ -174,13 +176,7 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(RowsParams p)
         const int64_t r = r0 + i;
         if (r >= p.rows) break;
         const uint32_t byte = scale_byte(row16_max(largest8(v[i])));
-        const float inv = inverse(byte);
-        u32x2_t codes;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            codes[h] = codes4(half_of(v[i], 4 * h) * inv, half_of(v[i], 4 * h + 1) * inv,
-                              half_of(v[i], 4 * h + 2) * inv, half_of(v[i], 4 * h + 3) * inv);
-        if (c < p.kp) *reinterpret_cast<u32x2_t *>(p.codes + r * p.kp + c) = codes;
+        if (c < p.kp) *reinterpret_cast<u32x2_t *>(p.codes + r * p.kp + c) = codes8(v[i], byte);
         const int64_t matrix = r / p.R;
         const int64_t at = (matrix * p.kq + q) * p.R + (r - matrix * p.R);
         if ((lane & 15) == 0) p.scales[at * 4 + lane / 16] = static_cast<uint8_t>(byte);
@@ -360,20 +356,16 @@ __global__ __launch_bounds__(256) void f8_square_kernel(SquareParams p)
         for (int j = 0; j < 4; ++j) m[j] = __builtin_elementwise_max(m[j], bits_as<u16x2_t>(o[j]));
     }
     uint32_t byte[8];
-    float inv[8];
     if constexpr (BLOCK) {
         uint32_t big = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) big = max(big, static_cast<uint32_t>(m[j / 2][j % 2]));
         byte[0] = scale_byte(row16_max(big));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) inv[j] = inverse(byte[0]);
+        for (int j = 1; j < 8; ++j) byte[j] = byte[0];
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            byte[j] = scale_byte(m[j / 2][j % 2]);
-            inv[j] = inverse(byte[j]);
-        }
+        for (int j = 0; j < 8; ++j) byte[j] = scale_byte(m[j / 2][j % 2]);
     }
     // scales: bytes past the last group (of a dword's four) are written too
     const int32_t group = TRANSPOSED ? tr : tc, block0 = TRANSPOSED ? tc : tr;
@@ -397,13 +389,8 @@ __global__ __launch_bounds__(256) void f8_square_kernel(SquareParams p)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int32_t r = tr * 128 + ty * 8 + i;
-            u32x2_t codes;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                codes[h] = codes4(half_of(v[i], 4 * h) * inv[0], half_of(v[i], 4 * h + 1) * inv[0],
-                                  half_of(v[i], 4 * h + 2) * inv[0], half_of(v[i], 4 * h + 3) * inv[0]);
             if (r < p.XR)
-                *reinterpret_cast<u32x2_t *>(p.codes + (matrix * p.XR + r) * p.kp + c0) = codes;
+                *reinterpret_cast<u32x2_t *>(p.codes + (matrix * p.XR + r) * p.kp + c0) = codes8(v[i], byte[0]);
         }
         return;
     }
@@ -411,12 +398,11 @@ __global__ __launch_bounds__(256) void f8_square_kernel(SquareParams p)
     // places of a row XORed with tx so that 16 threads write to 16 of them
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        u32x2_t codes;
+        u32x4_t w;   // column j's halves of two rows a dword
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            codes[h] = codes4(half_of(v[4 * h], j) * inv[j], half_of(v[4 * h + 1], j) * inv[j],
-                              half_of(v[4 * h + 2], j) * inv[j], half_of(v[4 * h + 3], j) * inv[j]);
-        *reinterpret_cast<u32x2_t *>(&smem[(tx * 8 + j) * 128 + ((ty ^ tx) * 8)]) = codes;
+        for (int i = 0; i < 4; ++i)
+            w[i] = __builtin_amdgcn_perm(v[2 * i + 1][j / 2], v[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+        *reinterpret_cast<u32x2_t *>(&smem[(tx * 8 + j) * 128 + ((ty ^ tx) * 8)]) = codes8(w, byte[j]);
     }
     __syncthreads();
 #pragma unroll
@@ -687,23 +673,6 @@ __device__ __forceinline__ i32x8_t whole(const i32x4_t (&v)[2])
 }
 
 // ---- codes straight from memory ---------------------------------------------------
-// 16 halves to codes by the conversion that divides by a scale, the same codes as
-// codes4's of the products (every half, every scale).
-__device__ __forceinline__ u32x4_t codes16(u32x4_t lo, u32x4_t hi, uint32_t byte)
-{
-    const float s = bits_as<float>(byte << 23);
-    u32x4_t c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const u32x4_t v = i < 2 ? lo : hi;
-        i16x2_t w = {0, 0};
-        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, bits_as<half2_t>(v[2 * (i % 2)]), s, false);
-        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, bits_as<half2_t>(v[2 * (i % 2) + 1]), s, true);
-        c[i] = bits_as<uint32_t>(w);
-    }
-    return c;
-}
-
 // The largest of eight neighbouring lanes' values.
 __device__ __forceinline__ uint32_t eight_max(uint32_t v)
 {
@@ -768,7 +737,8 @@ __global__ __launch_bounds__(64 * W) void f8_stream_kernel(Params p)
         auto put = [&](int o) {
             const int row = o / per, c = o - row * per;
             const uint32_t byte = scale_byte(eight_max(max(largest8(lo), largest8(hi))));
-            *reinterpret_cast<u32x4_t *>(lds + row * pitch + c * 16) = codes16(lo, hi, byte);
+            const u32x2_t first = codes8(lo, byte), second = codes8(hi, byte);
+            *reinterpret_cast<u32x4_t *>(lds + row * pitch + c * 16) = u32x4_t{first[0], first[1], second[0], second[1]};
             if (c % 8 == 0) lds_s[row * kb + c / 8] = static_cast<uint8_t>(byte);
         };
         for (; o + 64 * W < all; o += 64 * W) {
