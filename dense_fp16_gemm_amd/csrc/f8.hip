@@ -1050,7 +1050,8 @@ __device__ __forceinline__ void store_blocks(const Params &p, const Unit &u, uin
     auto put = [&](int row, int32_t n, half8_t v) {
         uint16_t *to = c + static_cast<int64_t>(row) * p.N;
         if constexpr (ALL)
-            *reinterpret_cast<half8_u_t *>(to + n) = v;
+            // past the L2, which they would fill (16396 rows of 32 experts, 2048 x 1408: 87 us, 82 so)
+            __builtin_nontemporal_store(v, reinterpret_cast<half8_u_t *>(to + n));
         else if (row < rows && n < p.N)
             store8(to, n, p.N, v);
     };
