@@ -495,7 +495,8 @@ struct RouteBackParams {
 };
 
 // Scores go to LDS, where lane j takes that of choice j, and the choices' gradients
-// come back the same way.  8191 tokens of 128 experts, 6 chosen:
+// come back the same way: 8191 tokens of 128 experts, 6 chosen, 8.3 us (by
+// exchanges between the lanes for every choice 10.6).
 template <int V>
 __global__ __launch_bounds__(256) void route_back_kernel(RouteBackParams p)
 {
@@ -576,9 +577,15 @@ __global__ __launch_bounds__(256) void route_back_kernel(RouteBackParams p)
 // ---------------------------------------------------------------------------
 // A token's rows together
 // ---------------------------------------------------------------------------
+// What is written, and what is read for the last time (LAST), leaves the caches to
+// the other rows: 4999 x 4160, 6 choices, with the gradients 159 us without, 142 so.
+template <bool LAST = false>
 __device__ __forceinline__ half8_t load8(const _Float16 *row, int32_t c, int32_t cols)
 {
-    if (c + 8 <= cols) return *reinterpret_cast<const half8_u_t *>(row + c);
+    if (c + 8 <= cols) {
+        const half8_u_t *at = reinterpret_cast<const half8_u_t *>(row + c);
+        return LAST ? __builtin_nontemporal_load(at) : *at;
+    }
     half8_t v = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -589,7 +596,7 @@ __device__ __forceinline__ half8_t load8(const _Float16 *row, int32_t c, int32_t
 __device__ __forceinline__ void store8(_Float16 *row, int32_t c, int32_t cols, half8_t v)
 {
     if (c + 8 <= cols) {
-        *reinterpret_cast<half8_u_t *>(row + c) = v;
+        __builtin_nontemporal_store(v, reinterpret_cast<half8_u_t *>(row + c));
         return;
     }
 #pragma unroll
@@ -668,7 +675,7 @@ __global__ __launch_bounds__(256) void combine_back_kernel(CombineParams p)
             for (int k = 0; k < U; ++k)
                 if (c0 + k * 512 < p.N) {
                     d[k] = load8(dout, c0 + k * 512, p.N);
-                    if (p.dweights) v[k] = load8(y, c0 + k * 512, p.N);
+                    if (p.dweights) v[k] = load8<true>(y, c0 + k * 512, p.N);
                 }
 #pragma unroll
             for (int k = 0; k < U; ++k) {
