@@ -227,12 +227,19 @@ struct Found {
     int32_t lo, hi;   // its positions (or those of no expert)
 };
 
+// Sums of units stop here: only offsets that overlap reach it, and what is computed
+// of those does not matter, but stays inside the arrays.
+constexpr int32_t MOST_UNITS = 1 << 29;
+
+__device__ __forceinline__ int32_t add_units(int32_t a, int32_t b) { return min(a + b, MOST_UNITS); }
+
 __device__ __forceinline__ int32_t inclusive_scan(int32_t v, int lane)
 {
+    v = min(v, MOST_UNITS);
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
         const int32_t o = __shfl_up(v, d);
-        if (lane >= d) v += o;
+        if (lane >= d) v = add_units(v, o);
     }
     return v;
 }
@@ -266,7 +273,7 @@ __device__ __forceinline__ Found find_unit(const int32_t *offsets, int32_t E, in
         for (int32_t c = 64; c < E; c += 64) {
             int32_t l, h;
             positions(offsets, E, S, c + lane, l, h);
-            total += __builtin_amdgcn_readlane(inclusive_scan((h - l + size - 1) / size * per, lane), 63);
+            total = add_units(total, __builtin_amdgcn_readlane(inclusive_scan((h - l + size - 1) / size * per, lane), 63));
         }
         const int32_t x = id & 7, i = id >> 3, q = total >> 3, rem = total & 7;
         if (i >= q + (x < rem ? 1 : 0)) return Found{-1, 0, S, S};
@@ -600,11 +607,11 @@ __device__ __forceinline__ Unit make_unit(const Params &p, int lane)
             int32_t lo, hi;
             positions(p.offsets, p.E, p.top, e, lo, hi);   // top: slots
             const int32_t groups = (hi - lo + 127) / 128;
-            if (e < u.matrix) before += groups; else mine = groups;
+            if (e < u.matrix) before = add_units(before, groups); else mine = groups;
         }
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
-            before += __shfl_xor(before, d);
+            before = add_units(before, __shfl_xor(before, d));
             mine += __shfl_xor(mine, d);
         }
         u.kb0 = min(__builtin_amdgcn_readfirstlane(before), p.kb);
@@ -631,8 +638,8 @@ struct Experts {
             __syncthreads();
             int32_t all = before;
             for (int w = 0; w < W; ++w) {
-                if (w == wave) up += all;
-                all += sums[w];
+                if (w == wave) up = add_units(up, all);
+                all = add_units(all, sums[w]);
             }
             before = all;
             if (e0 + tid < E) upto[e0 + tid] = up;
