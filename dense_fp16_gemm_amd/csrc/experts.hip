@@ -109,6 +109,9 @@ __device__ __forceinline__ uint64_t ordered(double v)
 // ---------------------------------------------------------------------------
 // The choice: one wave a token
 // ---------------------------------------------------------------------------
+// Bound by the vector ALU's issue: 470 instructions a token of 128 experts, 6 chosen,
+// some half of them 64-bit exponentials and quotients, the others the choices' six
+// reductions: 8191 tokens in 10.7 us.
 struct RouteParams {
     const void *logits;
     const float *bias;
@@ -297,7 +300,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p)
 // slot how many of its lanes before it go to the same expert, the waves' counts
 // and the chunk's first position of each expert give the rest.  Where there are
 // several chunks their counts come from a kernel before.  49146 slots of 128
-// experts: 6 us and 4 us before it (one workgroup for all slots: 109 us).
+// experts: 5.5 to 6.5 us and 1.6 to 4 before it (one workgroup for all slots: 109 us).
 struct OrderParams {
     const int32_t *experts;
     int32_t *rows, *places, *offsets;
@@ -615,7 +618,8 @@ struct CombineParams {
 };
 
 // A wave takes 512 columns of a token: places and weights are scalars, and the
-// rows of eight choices are on their way at once.
+// rows of eight choices are on their way at once.  Bound by HBM and the last cache:
+// 4999 x 4160, 6 choices, in 50 us (291 MB).
 constexpr int AT_ONCE = 8;
 
 __global__ __launch_bounds__(256) void combine_kernel(CombineParams p)
@@ -653,7 +657,8 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineParams p)
 
 // A wave a slot: its row of dy, its inner product, and zeros for the position of
 // the slot's number where that is no slot's.  Four times 512 columns are on their
-// way at once; the waves of a token read dout from its XCD's L2.
+// way at once; the waves of a token read dout from its XCD's L2.  Bound by HBM: 4999 x
+// 4160, 6 choices, in 93 us (541 MB, 5.8 TB/s).
 __global__ __launch_bounds__(256) void combine_back_kernel(CombineParams p)
 {
     constexpr int U = 4;
