@@ -218,3 +218,108 @@ def test_few_as_many(g, t, e, top, scores):
     order = torch.where(flat < 0, e, flat).sort(stable=True)
     assert torch.equal(few.rows, torch.where(order.values < e, order.indices, -1).int())
     assert torch.equal(few.offsets, torch.searchsorted(order.values, torch.arange(e + 1, device="cuda")).int())
+
+
+def test_threads(g):
+    """Products, routing and combination from four host threads at once, each on its
+    own stream, with plans that differ from call to call."""
+    import threading
+
+    gen = generator(5)
+    cases = []
+    for m, n, k in ((1, 300, 2000), (70, 300, 200), (333, 1001, 4000), (1000, 2050, 300), (3001, 4096, 130)):
+        ac, as_, a = whole(gen, m, k, 1)
+        bc, bs, b = whole(gen, n, k, 128)
+        cases.append((g.F8Matrix(ac, as_, k, 1), g.F8Matrix(bc, bs, k, 128), product(a, b)))
+    logits = uneven(gen, 900, 40, 3)
+    want = g.route(logits, 3)
+    y = torch.randn(2700, 520, generator=gen, device="cuda").half()
+    out = g.combine_experts(y, want)
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(i):
+        try:
+            torch.cuda.set_device(0)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for j in range(20):
+                    a, b, c = cases[(i + j) % len(cases)]
+                    got = g.gemm_nt_f8(a, b)
+                    r = g.route(logits, 3)
+                    mixed = g.combine_experts(y, r)
+                    stream.synchronize()
+                    assert torch.equal(got, c)
+                    assert torch.equal(r.rows, want.rows) and torch.equal(r.weights.nan_to_num(-1), want.weights.nan_to_num(-1))
+                    assert torch.equal(mixed, out)
+        except BaseException as e:   # noqa: BLE001  (reported by the test's own thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[0]
+
+
+def test_graphs_share_a_workspace(g):
+    """Two captured products that use one workspace in turn."""
+    gen = generator(6)
+    graphs, cus = [], g.gemm_f16_device_cus()
+    sizes = [(300, 264, 2048), (333, 2050, 4000)]
+    need = max(g.gemm_f16_nt_f8_plan(m, n, k, 128, True, cus).workspace_bytes for m, n, k in sizes)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for m, n, k in sizes:
+        x = torch.empty(m, k, dtype=torch.float16, device="cuda")
+        bc, bs, b = whole(gen, n, k, 128)
+        w, out = g.F8Matrix(bc, bs, k, 128), torch.empty(m, n, dtype=torch.float16, device="cuda")
+        x.copy_(whole_halves(gen, m, k))
+        g.gemm_nt_f8(x, w, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            g.gemm_nt_f8(x, w, out=out, workspace=ws)
+        graphs.append((graph, x, b, out, w))
+    for _ in range(3):
+        for graph, x, *_ in graphs:
+            x.copy_(whole_halves(gen, *x.shape))
+            ws.random_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, x, b, out, _ in graphs:
+            assert torch.equal(out, product(x.double(), b))
+
+
+def test_routing_of_other_numbers(g):
+    """A routing whose offsets and rows are no routing's: whatever is computed, nothing
+    around the outputs changes."""
+    gen = generator(7)
+    t, e, top, n, k = 2500, 64, 2, 264, 200
+    s = t * top
+    ac, as_, _ = whole(gen, t, k, 1)
+    wc, ws, _ = whole(gen, n, k, 128, count=e)
+    y = torch.randn(s, n, generator=gen, device="cuda").half()
+    x = torch.randn(t, k, generator=gen, device="cuda").half()
+    for kind in range(4):
+        offsets = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
+        if kind == 0:      # every expert has all rows
+            offsets[1::2] = s
+        elif kind == 1:
+            offsets.random_(-2 ** 31, 2 ** 31 - 1, generator=gen)
+        elif kind == 2:
+            offsets[:] = 2 ** 31 - 1
+        else:
+            offsets[:] = torch.arange(e, -1, -1, device="cuda") * 100
+        any_ = torch.randint(-2 ** 31, 2 ** 31 - 1, (3, s), generator=gen, device="cuda").int()
+        r = g.Routing(any_[0].view(t, top), torch.ones(t, top, device="cuda"), any_[1].contiguous(),
+                      any_[2].view(t, top), offsets)
+        out, around = guarded((s, n))
+        g.gemm_nt_f8_experts(g.F8Matrix(ac, as_, k, 1), g.F8Matrix(wc, ws, k, 128), r, gather=True, out=out)
+        dw, beyond = guarded((e, n, k))
+        g.gemm_nt_f8_experts_grad(g.quantize_f8_experts(y, r), g.quantize_f8_experts(x, r, gather=True), r, out=dw)
+        mixed, outside = guarded((t, n))
+        g.combine_experts(y, r, out=mixed)
+        g.combine_experts_backward(mixed, y, r)
+        torch.cuda.synchronize()
+        assert all((v == 3).all() for v in around + beyond + outside)
