@@ -54,40 +54,64 @@ __device__ __forceinline__ T readlane64(T v, int lane)
     return __builtin_bit_cast(T, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// The largest of 64 lanes' values, in every lane: five steps within the wave's
-// rows of 16 and across them, read from the last lane.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+// The largest of L neighbouring lanes' values (32 or 64), in each of them: rotations
+// within rows of 16 lanes, then rows and halves of the wave exchanged.
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v)
 {
-#define STEP(CTRL, ROWS)                                                                         \
-    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false)))
-    STEP(0x111, 0xf);   // row_shr 1, 2, 4, 8
-    STEP(0x112, 0xf);
-    STEP(0x114, 0xf);
-    STEP(0x118, 0xf);
-    STEP(0x142, 0xa);   // row_bcast 15, 31
-    STEP(0x143, 0xc);
+    static_assert(L == 32 || L == 64, "lanes of a token");
+#define STEP(CTRL) v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true)))
+    STEP(0x128);   // row_ror 8, 4, 2, 1
+    STEP(0x124);
+    STEP(0x122);
+    STEP(0x121);
 #undef STEP
-    return __builtin_amdgcn_readlane(v, 63);
+    const auto rows = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(rows[0], rows[1]);
+    if constexpr (L == 64) {
+        const auto halves = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = max(halves[0], halves[1]);
+    }
+    return v;
 }
 
-// The sum of 64 lanes' values, in every lane: the same steps, added pairwise.
-__device__ __forceinline__ double wave_sum64(double v)
+// Their sum, halves of the wave first: a token has the same sums in 32 lanes, which
+// add experts l and l + 32 of each 64 (below), as in 64.
+template <int L>
+__device__ __forceinline__ double lanes_sum(double v)
 {
-#define STEP(CTRL, ROWS)                                                                          \
-    {                                                                                             \
-        const uint64_t b = __builtin_bit_cast(uint64_t, v);                                       \
-        const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(b), CTRL, ROWS, 0xf, false); \
-        const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(b >> 32), CTRL, ROWS, 0xf, false); \
-        v += __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);                    \
+#define STEP(CTRL)                                                                               \
+    {                                                                                            \
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);                                      \
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(b), CTRL, 0xf, 0xf, true); \
+        const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(b >> 32), CTRL, 0xf, 0xf, true); \
+        v += __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);                   \
     }
-    STEP(0x111, 0xf);   // row_shr 1, 2, 4, 8
-    STEP(0x112, 0xf);
-    STEP(0x114, 0xf);
-    STEP(0x118, 0xf);
-    STEP(0x142, 0xa);   // row_bcast 15, 31
-    STEP(0x143, 0xc);
+#define SWAP(HOW)                                                                                \
+    {                                                                                            \
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);                                      \
+        const auto lo = HOW(static_cast<uint32_t>(b), static_cast<uint32_t>(b), false, false);   \
+        const auto hi = HOW(static_cast<uint32_t>(b >> 32), static_cast<uint32_t>(b >> 32), false, false); \
+        v = __builtin_bit_cast(double, static_cast<uint64_t>(hi[0]) << 32 | lo[0]) +             \
+            __builtin_bit_cast(double, static_cast<uint64_t>(hi[1]) << 32 | lo[1]);              \
+    }
+    if constexpr (L == 64) SWAP(__builtin_amdgcn_permlane32_swap)
+    SWAP(__builtin_amdgcn_permlane16_swap)
+    STEP(0x128);   // row_ror 8, 4, 2, 1
+    STEP(0x124);
+    STEP(0x122);
+    STEP(0x121);
 #undef STEP
-    return readlane64(v, 63);
+#undef SWAP
+    return v;
+}
+
+// Whether a condition holds in any of the lane's L lanes.
+template <int L>
+__device__ __forceinline__ bool lanes_any(bool v)
+{
+    const uint64_t b = __ballot(v);
+    return L == 64 ? b != 0 : (threadIdx.x & 32 ? b >> 32 : b & 0xffffffffu) != 0;
 }
 
 // Numbers as integers in the same order (no NaN among them).
@@ -107,11 +131,10 @@ __device__ __forceinline__ uint64_t ordered(double v)
 }
 
 // ---------------------------------------------------------------------------
-// The choice: one wave a token
+// The choice: one wave a token, or two tokens a wave
 // ---------------------------------------------------------------------------
-// Bound by the vector ALU's issue: 470 instructions a token of 128 experts, 6 chosen,
-// some half of them 64-bit exponentials and quotients, the others the choices' six
-// reductions: 8191 tokens in 10.7 us.
+// Bound by the vector ALU: by its issue where tokens fill the card, below that by the
+// chain of a token's 64-bit exponentials, quotients and the choices' reductions.
 struct RouteParams {
     const void *logits;
     const float *bias;
@@ -128,38 +151,40 @@ __device__ __forceinline__ double load_logit(const void *logits, bool f32, int64
                : static_cast<double>(static_cast<float>(static_cast<const _Float16 *>(logits)[at]));
 }
 
-// Lane l holds experts l, l + 64, ...: their logits x to their scores s.  Absent
-// experts have x = -inf.  False where the row has none (a NaN, or +inf with
-// softmax).
-template <int V>
+// (The exchanges above need every lane: none stands behind a condition on the lane.)
+
+// Of a token's L lanes lane l holds experts l, l + L, ...: their logits x to their
+// scores s.  Absent experts have x = -inf.  False where the row has none (a NaN, or
+// +inf with softmax).
+template <int L, int V>
 __device__ __forceinline__ bool scores_of(const double (&x)[V], bool sigmoid, double (&s)[V])
 {
     constexpr double inf = __builtin_huge_val();
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) bad |= !(x[i] == x[i]) || (!sigmoid && x[i] == inf);
-    if (__any(bad)) return false;
+    const bool fine = !lanes_any<L>(bad);
     if (sigmoid) {
 #pragma unroll
         for (int i = 0; i < V; ++i) s[i] = 1.0 / (1.0 + exp(-x[i]));
-        return true;
+        return fine;
     }
     // the largest, exactly: logits are fp32 numbers
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) most = max(most, ordered(static_cast<float>(x[i])));
-    const double m = static_cast<double>(unordered(wave_max(most)));
-    double sum = 0.0;
+    const double m = static_cast<double>(unordered(lanes_max<L>(most)));
+    double sums[2] = {0.0, 0.0};   // with 32 lanes, of the first and the second of each 64
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         s[i] = x[i] == -inf ? 0.0 : exp(x[i] - m);
-        sum += s[i];
+        sums[L == 32 ? i % 2 : 0] += s[i];
     }
-    sum = wave_sum64(sum);
+    const double sum = lanes_sum<L>(sums[0] + sums[1]);
     const double by = sum > 0.0 ? sum : 1.0;
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] /= by;
-    return true;
+    return fine;
 }
 
 template <int V>
@@ -174,7 +199,7 @@ __device__ __forceinline__ int32_t route_token(const RouteParams &p, int32_t t, 
         x[i] = e < p.E ? load_logit(p.logits, p.f32, static_cast<int64_t>(t) * p.E + e) : -inf;
         bias[i] = p.bias && e < p.E ? p.bias[e] : 0.0f;
     }
-    bool fine = scores_of(x, p.sigmoid, s);
+    bool fine = scores_of<64>(x, p.sigmoid, s);
     if (fine) {
         bool bad = false;
 #pragma unroll
@@ -235,7 +260,7 @@ __device__ __forceinline__ int32_t route_token(const RouteParams &p, int32_t t, 
     for (int i = 0; i < V; ++i) key[i] = ordered(c[i]);
     const uint64_t none = ordered(-inf);
     int32_t mine = -1;
-    double weight = 0.0, total = 0.0;
+    double weight = 0.0;
     for (int j = 0; j < p.top; ++j) {
         // the lane's highest, its lowest index first
         uint64_t best = key[0];
@@ -248,14 +273,14 @@ __device__ __forceinline__ int32_t route_token(const RouteParams &p, int32_t t, 
             }
         const uint32_t hi = static_cast<uint32_t>(best >> 32);
         uint32_t e = static_cast<uint32_t>(at * 64 + lane);
-        const uint32_t most = wave_max(hi);
+        const uint32_t most = lanes_max<64>(hi);
         uint64_t has = __ballot(hi == most);
         if (has & (has - 1)) {
             // several lanes with the same upper halves: the lower ones, then the lowest
             // expert
-            const uint32_t lo = wave_max(hi == most ? static_cast<uint32_t>(best) : 0u);
+            const uint32_t lo = lanes_max<64>(hi == most ? static_cast<uint32_t>(best) : 0u);
             const bool top = hi == most && static_cast<uint32_t>(best) == lo;
-            const uint32_t first = ~wave_max(top ? ~e : 0u);
+            const uint32_t first = ~lanes_max<64>(top ? ~e : 0u);
             has = __ballot(top && e == first);
         }
         const int from = __builtin_ctzll(has);
@@ -269,12 +294,12 @@ __device__ __forceinline__ int32_t route_token(const RouteParams &p, int32_t t, 
                 v = s[i];
             }
         v = readlane64(v, from);
-        total += v;
         if (lane == j) {
             mine = static_cast<int32_t>(e);
             weight = v;
         }
     }
+    const double total = lanes_sum<64>(weight);
     if (lane < p.top) {
         weight *= p.scale;
         if (p.renormalize) weight /= total + 1e-20;
@@ -291,6 +316,88 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p)
     const int lane = threadIdx.x & 63, wave = wave_index();
     const int32_t t = blockIdx.x * 4 + wave;
     if (t < p.T) route_token<V>(p, t, lane, cs[wave]);
+}
+
+// Two tokens a wave, 32 lanes each: up to 128 experts in one group.  A choice is one
+// reduction where the scores' upper halves tell all apart; the lane that has it
+// notes its expert in LDS, and what belongs to the choices is looked up at the end.
+// 8191 tokens of 128 experts, 6 chosen, 10.0 us (a wave a token 11.0; with the order
+// 17.5 and 18.7, of 131072 tokens 81 and 115, of 64 experts 52 and 84).
+template <int V>
+__global__ __launch_bounds__(256) void route_pairs_kernel(RouteParams p)
+{
+    constexpr double inf = __builtin_huge_val();
+    __shared__ double scores[4][64 * V];
+    __shared__ int32_t chosen[4][64];
+    const int lane = threadIdx.x & 63, wave = wave_index(), sub = lane & 31;
+    const int32_t first = (blockIdx.x * 4 + wave) * 2;
+    if (first >= p.T) return;
+    // the last token twice where there is no second
+    const int32_t t = min(first + lane / 32, p.T - 1);
+    double x[V], s[V];
+    float bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int32_t e = i * 32 + sub;
+        x[i] = e < p.E ? load_logit(p.logits, p.f32, static_cast<int64_t>(t) * p.E + e) : -inf;
+        bias[i] = p.bias && e < p.E ? p.bias[e] : 0.0f;
+    }
+    bool fine = scores_of<32>(x, p.sigmoid, s), bad = false;
+    uint32_t hi[V], lo[V];   // of the ordered numbers of the choice's scores
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const double c = x[i] == -inf ? -inf : s[i] + static_cast<double>(bias[i]);
+        bad |= !(c == c);
+        const uint64_t key = ordered(c);
+        hi[i] = static_cast<uint32_t>(key >> 32);
+        lo[i] = static_cast<uint32_t>(key);
+    }
+    const bool any = lanes_any<32>(bad);
+    fine = fine && !any;
+    const uint32_t none = static_cast<uint32_t>(ordered(-inf) >> 32);   // no number's upper half
+    chosen[wave][lane] = -1;
+    wave_lds_fence();
+    for (int32_t j = 0; j < p.top; ++j) {
+        uint32_t most = hi[0], less = lo[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < V; ++i)
+            if (hi[i] > most || (hi[i] == most && lo[i] > less)) {
+                most = hi[i];
+                less = lo[i];
+                at = i;
+            }
+        const uint32_t top = lanes_max<32>(most);
+        bool mine = most == top;
+        const uint64_t has = __ballot(mine);   // one of each half at least
+        if (has & (has - 0x0000000100000001ull)) {
+            // several with the same upper halves: the lower ones, then the lowest expert
+            const uint32_t l = lanes_max<32>(mine ? less : 0u);
+            mine = mine && less == l;
+            const uint32_t e = static_cast<uint32_t>(at * 32 + sub);
+            const uint32_t lowest = ~lanes_max<32>(mine ? ~e : 0u);   // in all lanes
+            mine = mine && e == lowest;
+        }
+        if (!__any(top > none)) break;
+        if (mine && top > none) {
+            chosen[wave][(lane & 32) + j] = at * 32 + sub;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (at == i) hi[i] = 0;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) scores[wave][(lane / 32 * V + i) * 32 + sub] = s[i];
+    wave_lds_fence();
+    const int32_t e = chosen[wave][lane];
+    double weight = e >= 0 ? scores[wave][lane / 32 * V * 32 + e] : 0.0;
+    const double total = lanes_sum<32>(weight);
+    if (sub >= p.top || first + lane / 32 >= p.T) return;
+    weight *= p.scale;
+    if (p.renormalize) weight /= total + 1e-20;
+    const int64_t out = static_cast<int64_t>(t) * p.top + sub;
+    p.experts[out] = fine ? e : -1;
+    p.weights[out] = !fine ? __builtin_nanf("") : e < 0 ? 0.0f : static_cast<float>(weight);
 }
 
 // ---------------------------------------------------------------------------
@@ -485,7 +592,7 @@ __global__ __launch_bounds__(1024) void route_few_kernel(RouteParams p, OrderPar
 }
 
 // ---------------------------------------------------------------------------
-// The logits' gradient: one wave a token
+// The logits' gradient: one wave a token, or two tokens a wave
 // ---------------------------------------------------------------------------
 struct RouteBackParams {
     const void *logits;
@@ -498,69 +605,68 @@ struct RouteBackParams {
 };
 
 // Scores go to LDS, where lane j takes that of choice j, and the choices' gradients
-// come back the same way: 8191 tokens of 128 experts, 6 chosen, 8.3 us (by
-// exchanges between the lanes for every choice 10.6).
-template <int V>
+// come back the same way.  L lanes a token: 32, and two tokens a wave, up to 128
+// experts.  8191 tokens of 128 experts, 6 chosen, 7.9 us (64 lanes: 8.3; of 131072
+// tokens 55 and 70, of 64 experts 37 and 64).
+template <int L, int V>
 __global__ __launch_bounds__(256) void route_back_kernel(RouteBackParams p)
 {
     constexpr double inf = __builtin_huge_val();
+    constexpr int TOKENS = 64 / L;
     __shared__ double memory[4][64 * V];
-    const int lane = threadIdx.x & 63, wave = wave_index();
-    const int32_t t = blockIdx.x * 4 + wave;
-    if (t >= p.T) return;
-    double *const ls = memory[wave];
+    const int lane = threadIdx.x & 63, wave = wave_index(), sub = lane % L;
+    const int32_t first = (blockIdx.x * 4 + wave) * TOKENS;
+    if (first >= p.T) return;
+    // the last token twice where there is no second
+    const int32_t t = min(first + lane / L, p.T - 1);
+    const bool there = first + lane / L < p.T;
+    double *const ls = memory[wave] + lane / L * (L * V);
     double x[V], s[V], d[V];
     const int64_t row = static_cast<int64_t>(t) * p.E;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int32_t e = i * 64 + lane;
+        const int32_t e = i * L + sub;
         x[i] = e < p.E ? load_logit(p.logits, p.f32, row + e) : -inf;
     }
     int32_t mine = -1;
     double dw = 0.0;
     bool bad = false;
-    if (lane < p.top) {
-        const int64_t at = static_cast<int64_t>(t) * p.top + lane;
+    if (sub < p.top) {
+        const int64_t at = static_cast<int64_t>(t) * p.top + sub;
         mine = p.experts[at];
         if (mine < 0 || mine >= p.E) mine = -1;
         const float w = p.weights[at], g = p.dweights[at];
         if (mine >= 0) dw = static_cast<double>(g);
         bad = !(w == w);
     }
-    const bool fine = scores_of(x, p.sigmoid, s) && !__any(bad);
+    const bool scored = scores_of<L>(x, p.sigmoid, s), any = lanes_any<L>(bad), fine = scored && !any;
 #pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = 0.0;
-    double dot = 0.0;
-    if (fine) {
+    for (int i = 0; i < V; ++i) ls[i * L + sub] = s[i];
+    wave_lds_fence();
+    const double own = mine >= 0 ? ls[mine] : 0.0;
+    wave_lds_fence();
 #pragma unroll
-        for (int i = 0; i < V; ++i) ls[i * 64 + lane] = s[i];
-        wave_lds_fence();
-        const double own = mine >= 0 ? ls[mine] : 0.0;
-        wave_lds_fence();
-#pragma unroll
-        for (int i = 0; i < V; ++i) ls[i * 64 + lane] = 0.0;
-        wave_lds_fence();
-        // sums over the choices: of their scores, and of those times dw
-        double by = p.scale, less = 0.0;
-        if (p.renormalize) {
-            const double total = wave_sum64(own) + 1e-20;
-            by = p.scale / total;
-            less = wave_sum64(own * dw) / total;
-        }
-        const double g = by * (dw - less);
-        if (mine >= 0) atomicAdd(&ls[mine], g);   // an expert is chosen once, unless the caller says so
-        wave_lds_fence();
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = ls[i * 64 + lane];
-        if (!p.sigmoid) {
-            // sum of d s, which is where an expert was chosen
-            dot = wave_sum64(mine >= 0 ? g * own : 0.0);
-        }
+    for (int i = 0; i < V; ++i) ls[i * L + sub] = 0.0;
+    wave_lds_fence();
+    // sums over the choices: of their scores, and of those times dw
+    double by = p.scale, less = 0.0;
+    if (p.renormalize) {
+        const double total = lanes_sum<L>(own) + 1e-20;
+        by = p.scale / total;
+        less = lanes_sum<L>(own * dw) / total;
     }
+    const double g = by * (dw - less);
+    if (mine >= 0) atomicAdd(&ls[mine], g);   // an expert is chosen once, unless the caller says so
+    wave_lds_fence();
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = ls[i * L + sub];
+    // sum of d s, which is where an expert was chosen
+    double dot = 0.0;
+    if (!p.sigmoid) dot = lanes_sum<L>(mine >= 0 ? g * own : 0.0);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int32_t e = i * 64 + lane;
-        if (e >= p.E) continue;
+        const int32_t e = i * L + sub;
+        if (e >= p.E || !there) continue;
         double g;
         if (!fine)
             g = __builtin_nan("");
@@ -776,8 +882,22 @@ template <int V>
 struct RouteSmallOf { static const void *get() { return address(route_few_kernel<V, true>); } };
 template <int V>
 struct RouteOf { static const void *get() { return address(route_kernel<V>); } };
-template <int V>
-struct RouteBackOf { static const void *get() { return address(route_back_kernel<V>); } };
+// Lanes hold V experts each: two tokens a wave up to 128.
+static const void *route_pairs(int64_t E)
+{
+    return E <= 32   ? address(route_pairs_kernel<1>)
+           : E <= 64 ? address(route_pairs_kernel<2>)
+                     : address(route_pairs_kernel<4>);
+}
+
+static const void *route_back(int64_t E)
+{
+    if (E <= 32) return address(route_back_kernel<32, 1>);
+    if (E <= 64) return address(route_back_kernel<32, 2>);
+    if (E <= 128) return address(route_back_kernel<32, 4>);
+    if (E <= 256) return address(route_back_kernel<64, 4>);
+    return E <= 512 ? address(route_back_kernel<64, 8>) : address(route_back_kernel<64, 16>);
+}
 
 // The chunks of S slots, and the bytes of their counts.  Up to 2048 slots in one:
 // two passes of a workgroup cost less than a second launch.  No more than 256, whose
@@ -863,9 +983,10 @@ extern "C" int gemm_f16_route(int64_t T, int64_t E, int32_t top, int32_t scores,
     if (T <= FEW && S <= 64)
         return launch(by_experts<RouteSmallOf>(E), 1, static_cast<int>(std::max<int64_t>(T, 1)) * 64, &p, stream, &o);
     if (T <= FEW) return launch(by_experts<RouteFewOf>(E), 1, 1024, &p, stream, &o);
-    const int64_t grid = cdiv(T, 4);
+    const bool pairs = E <= 128 && groups == 1;
+    const int64_t grid = cdiv(T, pairs ? 8 : 4);
     if (grid * 256 >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
-    if (T > 0) v = launch(by_experts<RouteOf>(E), grid, 256, &p, stream);
+    v = launch(pairs ? route_pairs(E) : by_experts<RouteOf>(E), grid, 256, &p, stream);
     if (v == GEMM_F16_OK && o.chunks > 1) v = launch(address(count_kernel), o.chunks, 1024, &o, stream);
     return v != GEMM_F16_OK ? v : launch(address(order_kernel), o.chunks, 1024, &o, stream);
 }
@@ -901,9 +1022,9 @@ extern "C" int gemm_f16_route_backward(int64_t T, int64_t E, int32_t top, int32_
     p.f32 = logits_f32 != 0;
     p.sigmoid = scores == GEMM_F16_ROUTE_SIGMOID;
     p.renormalize = renormalize != 0;
-    const int64_t grid = cdiv(T, 4);
+    const int64_t grid = cdiv(T, E <= 128 ? 8 : 4);
     if (grid * 256 >= MOST_THREADS) return GEMM_F16_UNSUPPORTED;
-    return launch(by_experts<RouteBackOf>(E), grid, 256, &p, stream);
+    return launch(route_back(E), grid, 256, &p, stream);
 }
 
 extern "C" int gemm_f16_combine(int64_t T, int32_t top, int64_t N, const void *y,

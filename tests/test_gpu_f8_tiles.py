@@ -1,9 +1,11 @@
 """The 8-bit products' kernels for many rows, each reached by sizes whose tiles and
 ranges end anywhere: whole numbers, whose products and sums are exact in fp32
 whatever their order, against 64 bits."""
+import numpy as np
 import pytest
 import torch
 
+import f8_ref as ref
 from test_gpu_f8 import g  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -323,3 +325,46 @@ def test_routing_of_other_numbers(g):
         g.combine_experts_backward(mixed, y, r)
         torch.cuda.synchronize()
         assert all((v == 3).all() for v in around + beyond + outside)
+
+
+@pytest.mark.parametrize("e", [1, 2, 31, 32, 33, 63, 64, 65, 97, 127, 128, 129])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("t", [17, 18, 263])
+def test_two_tokens_a_wave(g, t, e, scores):
+    """Tokens with ties, masks and without scores side by side in a wave: each has what
+    it has by itself, bit for bit, and the plain form's choice."""
+    rng = np.random.default_rng(t + e)
+    x = np.round(rng.standard_normal((t, e)) * 3).astype(np.float32)     # many ties
+    x[3], x[5], x[8, 1:], x[11] = 1.0, -np.inf, -np.inf, 88.0
+    x[6, e - 1], x[9, 0] = np.nan, np.inf
+    x[12] = 20.0                                                        # told apart by the lower halves
+    x[12, e // 2] = np.nextafter(np.float32(20), np.float32(21))
+    x[13, e // 3:] = -np.inf
+    top = min(e, 32 if t == 18 else 7)
+    bias = rng.standard_normal(e).astype(np.float32)
+    bias[e // 2] = -np.inf
+    dw = rng.standard_normal((t, top)).astype(np.float32)
+    for b in (None, bias):
+        on = None if b is None else torch.from_numpy(b).cuda()
+        r = g.route(torch.from_numpy(x).cuda(), top, scores, on)
+        want, weights = ref.route(x, top, scores, b)
+        np.testing.assert_array_equal(r.experts.cpu().numpy(), want)
+        w = r.weights.cpu().numpy().astype(np.float64)
+        assert (np.isnan(w) == np.isnan(weights)).all()
+        ok = ~np.isnan(weights)
+        # one rounding to fp32, and sums of 64-bit scores in another order
+        assert (np.abs(w - weights)[ok] <= np.abs(weights[ok]) * (2.0 ** -24 + 2.0 ** -40) + 2.0 ** -150).all()
+        for at in range(0, min(t, 48), 16):
+            part = g.route(torch.from_numpy(x[at:at + 16].copy()).cuda(), top, scores, on)
+            assert torch.equal(part.experts, r.experts[at:at + 16])
+            assert torch.equal(part.weights.nan_to_num(-1), r.weights[at:at + 16].nan_to_num(-1))
+        got = g.route_backward(torch.from_numpy(x).cuda(), r, torch.from_numpy(dw).cuda()).cpu().numpy().astype(np.float64)
+        for i in range(t):
+            if not ok[i].all():
+                assert np.isnan(got[i]).all()
+                continue
+            one = slice(i, i + 1)
+            d = ref.route_gradient(x[one].astype(np.float64), want[one], dw[one].astype(np.float64), scores, True, 1.0)
+            # one rounding; the 64-bit sums of at most top + E terms, 4 times dw in size
+            size = np.abs(dw[i]).max() * 4
+            assert (np.abs(got[one] - d) <= np.abs(d) * 2.0 ** -24 + 2.0 ** -150 + size * (top + e + 40) * 2.0 ** -52).all()
