@@ -190,8 +190,8 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(RowsParams p)
 // A workgroup takes 128 x 128 values of X, eight rows by eight columns a thread:
 // thread (ty, tx) = (tid / 16, tid % 16) rows 8 ty .., columns 8 tx .. .  The transpose
 // goes through LDS as codes, so that both sides move 128 bytes and more at once: 4999
-// x 8192 in 23 to 25 us, 5 TB/s.  By expert, where each workgroup first finds its rows,
-// 16396 x 1408 in 17 us and x 2048, gathered from 4099 rows, in 24: their way through
+// x 8192 in 24 us, 5 TB/s.  By expert, where each workgroup first finds its rows,
+// 16396 x 1408 in 16 us and x 2048, gathered from 4099 rows, in 20.5: their way through
 // memory three times in a row.
 struct SquareParams {
     const uint16_t *X;
@@ -316,10 +316,15 @@ __global__ __launch_bounds__(256) void f8_square_kernel(SquareParams p)
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
     const int tx = tid & 15, ty = tid >> 4;
     int64_t unit = xcd_unit();
-    const int32_t tc = static_cast<int32_t>(unit % p.tiles_c);
-    unit /= p.tiles_c;
-    const int32_t tr = static_cast<int32_t>(unit % p.tiles_r);
-    const int64_t matrix = unit / p.tiles_r;
+    // an XCD's workgroups go along what is stored together; where it is transposed and
+    // its rows gathered several times, a slab of 128 columns then stays in the L2 (the
+    // other way 25, 17.4 and 23 us at the sizes above)
+    const int32_t inner = TRANSPOSED ? p.tiles_r : p.tiles_c, outer = TRANSPOSED ? p.tiles_c : p.tiles_r;
+    const int32_t near = static_cast<int32_t>(unit % inner);
+    unit /= inner;
+    const int32_t far = static_cast<int32_t>(unit % outer);
+    const int64_t matrix = unit / outer;
+    const int32_t tc = TRANSPOSED ? far : near, tr = TRANSPOSED ? near : far;
     const uint16_t *X = p.X + matrix * p.XR * p.XC;
     const int32_t c0 = tc * 128 + tx * 8;
     u32x4_t v[8];
