@@ -775,22 +775,24 @@ __global__ __launch_bounds__(256) void combine_back_kernel(CombineParams p)
     const int32_t place = p.places[slot];
     const bool in = static_cast<uint32_t>(place) < static_cast<uint32_t>(p.S);
     const float w = p.weights ? p.weights[slot] : 1.0f;
+    // columns are counted unsigned: the last step passes N, which may be 2^31 - 8
+    const uint32_t N = static_cast<uint32_t>(p.N);
     float dot = 0.0f;
     if (in) {
         const _Float16 *dout = p.dout + static_cast<int64_t>(unit / p.top) * p.N;
         const _Float16 *y = p.y + static_cast<int64_t>(place) * p.N;
         _Float16 *dy = p.out + static_cast<int64_t>(place) * p.N;
-        for (int32_t c0 = lane * 8; c0 < p.N; c0 += U * 512) {
+        for (uint32_t c0 = lane * 8; c0 < N; c0 += U * 512) {
             half8_t d[U], v[U];
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                if (c0 + k * 512 < p.N) {
+                if (c0 + k * 512 < N) {
                     d[k] = load8(dout, c0 + k * 512, p.N);
                     if (p.dweights) v[k] = load8<true>(y, c0 + k * 512, p.N);
                 }
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                if (c0 + k * 512 >= p.N) break;
+                if (c0 + k * 512 >= N) break;
                 half8_t h;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[i] = static_cast<_Float16>(w * static_cast<float>(d[k][i]));
@@ -808,7 +810,7 @@ __global__ __launch_bounds__(256) void combine_back_kernel(CombineParams p)
         if (lane == 0) p.dweights[slot] = dot;
     }
     if (p.rows[slot] < 0)
-        for (int32_t c = lane * 8; c < p.N; c += 512) store8(p.out + slot * p.N, c, p.N, half8_t{});
+        for (uint32_t c = lane * 8; c < N; c += 512) store8(p.out + slot * p.N, c, p.N, half8_t{});
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,69 @@
+"""Layers of experts at the edges of what their headers allow."""
+import pytest
+import torch
+
+from test_gpu_f8 import g  # noqa: F401  (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+# ---- rows of nearly 2^31 columns -------------------------------------------------
+WIDEST = 2 ** 31 - 8     # the last of a wave's steps of 2048 columns ends past 2^31
+
+
+def widest_row():
+    """One row of small whole numbers."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    part = torch.randint(-2, 3, (2 ** 28,), device="cuda", generator=gen).half()
+    x = torch.empty(1, WIDEST, dtype=torch.float16, device="cuda")
+    for at in range(0, WIDEST, 2 ** 28):
+        x[0, at:at + 2 ** 28] = part[: WIDEST - at]
+    return x
+
+
+def guarded_row():
+    """A row's memory, and what lies around it."""
+    memory = torch.full((WIDEST + 8192,), 3.0, dtype=torch.float16, device="cuda")
+    return memory[4096:4096 + WIDEST].view(1, WIDEST), (memory[:4096], memory[4096 + WIDEST:])
+
+
+def test_combine_widest(g):
+    """One token, one choice, as many columns as a call takes: both directions."""
+    x = widest_row()
+    r = g.route(torch.zeros(1, 1, device="cuda"), 1, scale=0.5)
+    assert r.places.tolist() == [[0]] and r.weights.tolist() == [[0.5]]
+    out, around = guarded_row()
+    g.combine_experts(x, r, out=out)
+    half = x * 0.5
+    assert torch.equal(out, half)
+    # the inner product: of the first and the last columns, so that it is a small whole number
+    y = torch.zeros_like(x)
+    ends = (slice(0, 4096), slice(WIDEST - 4096, WIDEST))
+    for part in ends:
+        y[0, part] = x[0, part]
+    out.fill_(9.0)
+    dw = torch.zeros(1, 1, device="cuda")
+    g.gemm_f16_combine_backward(1, 1, WIDEST, x.data_ptr(), y.data_ptr(), r.weights.data_ptr(), r.rows.data_ptr(),
+                                r.places.data_ptr(), out.data_ptr(), dw.data_ptr(), stream())
+    assert torch.equal(out, half)
+    assert dw.item() == sum((x[0, part].double() ** 2).sum().item() for part in ends)
+    assert all((v == 3).all() for v in around)
+
+
+def test_combine_widest_of_no_expert(g):
+    """The same for a token without an expert: a row of zeros."""
+    x = torch.ones(1, WIDEST, dtype=torch.float16, device="cuda")
+    r = g.route(torch.full((1, 1), -torch.inf, device="cuda"), 1)
+    assert r.places.tolist() == [[-1]] and r.rows.tolist() == [-1]
+    out, around = guarded_row()
+    g.gemm_f16_combine_backward(1, 1, WIDEST, x.data_ptr(), 0, 0, r.rows.data_ptr(), r.places.data_ptr(),
+                                out.data_ptr(), 0, stream())
+    assert torch.count_nonzero(out).item() == 0
+    out.fill_(9.0)
+    g.combine_experts(x, r, out=out)
+    assert torch.count_nonzero(out).item() == 0
+    assert all((v == 3).all() for v in around)
