@@ -1697,6 +1697,8 @@ static int plan_call(const Call &c, int32_t num_cus, gemm_f16_lowbit_plan_t *pla
     if (c.M == 0 || c.N == 0) return GEMM_F16_OK;
     *r = choose(c, num_cus);
     const Kernel &e = kKernels[r->id];
+    // the kernels compute the ends of their tiles in 32 bits
+    if (round_up(c.M, e.bm) > INT32_MAX || round_up(c.N, e.bn) > INT32_MAX) return GEMM_F16_UNSUPPORTED;
     // every expert, and the rows of none, may end inside a tile
     const int64_t tiles = c.mode == EXPERTS ? c.M / e.bm + std::min(c.matrices, c.M) + 1 : cdiv(c.M, e.bm);
     const int64_t grid = matrices * tiles * cdiv(c.N, e.bn) * r->splits;

@@ -97,8 +97,9 @@ int gemm_f16_f8_dequantize(int64_t count, int64_t R, int64_t K, int32_t block,
  * on the device at once, the plan's workgroups take several each.)
  *
  * M = 0 or N = 0: nothing to compute.  K = 0: C is filled with +0.
- * GEMM_F16_UNSUPPORTED for sizes that gemm_f16_f8_sizes refuses for A or B, or
- * a C of more than 2^31 - 1 tiles of 16 x 16.
+ * GEMM_F16_UNSUPPORTED for sizes that gemm_f16_f8_sizes refuses for A or B, a C
+ * of more than 2^31 - 1 tiles of 16 x 16, one whose M or N, as whole tiles of the
+ * plan, passes 2^31 - 1, or a launch of 2^32 threads.
  */
 int gemm_f16_nt_f8_plan(int64_t M, int64_t N, int64_t K, int32_t b_block, int32_t a_f16,
                         int32_t num_cus, gemm_f16_lowbit_plan_t *plan);
