@@ -393,11 +393,7 @@ def gemm_nt_f8_experts_grad(dy: F8Matrix, x: F8Matrix, routing: Routing, out=Non
         raise ValueError("dy, x and routing must be on the same GPU")
     m, n = first.shape[0], x.codes.shape[0]
     shape = (e, m, n)
-    if out is None:
-        out = _new(first, stream, shape, _f16)
-    elif out.dtype != _f16 or tuple(out.shape) != shape or not out.is_contiguous() or \
-            out.device != first.device:
-        raise ValueError(f"out must be a contiguous float16 {list(shape)} tensor on {first.device}")
+    out = _new(first, stream, shape, _f16) if out is None else _output(out, first, stream, shape)
     _call(index, stream, _lib.gemm_f16_nt_f8_experts_grad, s, e, m, n, first.data_ptr(),
           dy.scales.data_ptr(), x.codes.data_ptr(), x.scales.data_ptr(),
           routing.offsets.data_ptr(), out.data_ptr())

@@ -209,13 +209,7 @@ def dequantize_f8(x: F8Matrix, out=None, stream=None):
     if not codes.is_cuda:
         raise ValueError("x must be on a GPU")
     shape = x.shape
-    if len(shape) == 2:
-        out = _output(out, codes, stream, shape)
-    elif out is None:
-        out = _new(codes, stream, shape, _f16)
-    elif out.dtype != _f16 or tuple(out.shape) != shape or not out.is_contiguous() or \
-            out.device != codes.device:
-        raise ValueError(f"out must be a contiguous float16 {list(shape)} tensor on {codes.device}")
+    out = _new(codes, stream, shape, _f16) if out is None else _output(out, codes, stream, shape)
     count = shape[0] if len(shape) == 3 else 1
     _call(codes.get_device(), stream, _lib.gemm_f16_f8_dequantize, count, shape[-2], x.k, x.block,
           codes.data_ptr(), x.scales.data_ptr(), out.data_ptr())

@@ -67,3 +67,35 @@ def test_combine_widest_of_no_expert(g):
     g.combine_experts(x, r, out=out)
     assert torch.count_nonzero(out).item() == 0
     assert all((v == 3).all() for v in around)
+
+
+# ---- streams ----------------------------------------------------------------------
+class ElsewhereStream:
+    """A stream of another device."""
+    device = torch.device("cuda", 1)
+    cuda_stream = 0
+
+
+def test_streams_of_another_device_are_refused(g):
+    """By every function, whether it allocates its output or is given it."""
+    f16 = dict(dtype=torch.float16, device="cuda")
+    t, e, top, n, k = 4, 3, 2, 20, 130
+    x, dy, w = torch.ones(t, k, **f16), torch.ones(t * top, n, **f16), torch.ones(e, n, k, **f16)
+    logits = torch.zeros(t, e, device="cuda")
+    r, w8, one = g.route(logits, top), g.quantize_f8(w, 128), g.quantize_f8(w[0], 128)
+    dy8, x8 = g.quantize_f8_experts(dy, r), g.quantize_f8_experts(x, r, gather=True)
+    s = ElsewhereStream()
+    calls = [
+        lambda: g.quantize_f8(x, stream=s), lambda: g.quantize_f8(w, 128, stream=s),
+        lambda: g.route(logits, top, stream=s), lambda: g.route_backward(logits, r, r.weights, stream=s),
+        lambda: g.quantize_f8_experts(x, r, gather=True, stream=s), lambda: g.combine_experts_backward(x, None, r, weighted=False, stream=s),
+    ]
+    for fn, args, shape in ((g.dequantize_f8, (one,), (n, k)), (g.dequantize_f8, (w8,), (e, n, k)),
+                            (g.gemm_nt_f8, (x, one), (t, n)), (g.gemm_nt_f8_experts, (x, w8, r, True), (t * top, n)),
+                            (g.gemm_nt_f8_experts_grad, (dy8, x8, r), (e, n, k)), (g.combine_experts, (dy, r), (t, n))):
+        fn(*args, out=torch.empty(shape, **f16))      # what is wrong is the stream alone
+        for out in (None, torch.empty(shape, **f16)):
+            calls.append(lambda fn=fn, args=args, out=out: fn(*args, out=out, stream=s))
+    for call in calls:
+        with pytest.raises(ValueError, match="stream is on"):
+            call()
