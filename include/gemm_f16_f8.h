@@ -84,7 +84,9 @@ int gemm_f16_f8_dequantize(int64_t count, int64_t R, int64_t K, int32_t block,
  *                 scales along the tokens)
  *
  * gemm_f16_nt_f8_x: the same with A given in fp16 [M, K] (any 2-byte alignment)
- * and quantised as gemm_f16_f8_quantize does, with the same results.
+ * and quantised as gemm_f16_f8_quantize does, to the same codes.  For up to 16 rows
+ * these may be added in another order than those of an A in F8: the results then
+ * differ by the roundings of fp32 sums.
  *
  * `workspace`: device memory of at least the planned bytes, 256-byte aligned
  * (else GEMM_F16_UNSUPPORTED), overlapping none of the other arrays (else
