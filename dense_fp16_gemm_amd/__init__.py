@@ -579,9 +579,10 @@ from . import experts, f8  # noqa: E402
 from .experts import (  # noqa: E402,F401
     Routing, combine_experts, combine_experts_backward, gemm_f16_combine,
     gemm_f16_combine_backward, gemm_f16_f8_experts_columns, gemm_f16_f8_quantize_experts,
-    gemm_f16_nt_f8_experts, gemm_f16_nt_f8_experts_grad, gemm_f16_nt_f8_experts_plan,
-    gemm_f16_nt_f8_experts_x, gemm_f16_route, gemm_f16_route_backward, gemm_f16_route_workspace,
-    gemm_nt_f8_experts, gemm_nt_f8_experts_grad, quantize_f8_experts, route, route_backward)
+    gemm_f16_nt_f8_experts, gemm_f16_nt_f8_experts_grad, gemm_f16_nt_f8_experts_grad_plan,
+    gemm_f16_nt_f8_experts_plan, gemm_f16_nt_f8_experts_x, gemm_f16_route,
+    gemm_f16_route_backward, gemm_f16_route_workspace, gemm_nt_f8_experts,
+    gemm_nt_f8_experts_grad, quantize_f8_experts, route, route_backward)
 from .f8 import (  # noqa: E402,F401
     F8Matrix, dequantize_f8, gemm_f16_f8_dequantize, gemm_f16_f8_quantize, gemm_f16_f8_sizes,
     gemm_f16_nt_f8, gemm_f16_nt_f8_plan, gemm_f16_nt_f8_x, gemm_nt_f8, quantize_f8)

@@ -1874,6 +1874,23 @@ static int experts_columns(int64_t S, int64_t E, int64_t *columns)
     return GEMM_F16_OK;
 }
 
+static int grad_call(int64_t S, int64_t E, int64_t M, int64_t N, Call *c)
+{
+    int64_t columns = 0;
+    int v = experts_columns(S, E, &columns);
+    if (v != GEMM_F16_OK) return v;
+    *c = Call{};
+    c->mode = GRAD;
+    c->M = M;
+    c->N = N;
+    c->K = columns;
+    c->a_rows = M;
+    c->matrices = E;
+    c->top = static_cast<int32_t>(S);
+    v = shape_of(1, M, columns, 1, &c->a);
+    return v != GEMM_F16_OK ? v : shape_of(1, N, columns, 1, &c->b);
+}
+
 }  // namespace gemm_f16_f8
 
 using namespace gemm_f16_f8;
@@ -2036,24 +2053,23 @@ extern "C" int gemm_f16_f8_quantize_experts(int64_t S, int64_t E, int64_t R, int
     return launch(address(f8_square_kernel<false, true, true>), grid, 256, &p, stream);
 }
 
+extern "C" int gemm_f16_nt_f8_experts_grad_plan(int64_t S, int64_t E, int64_t M, int64_t N,
+                                                int32_t num_cus, gemm_f16_lowbit_plan_t *plan)
+{
+    if (!plan) return GEMM_F16_INVALID_ARG;
+    Call c;
+    Choice r{};
+    const int v = grad_call(S, E, M, N, &c);
+    return v != GEMM_F16_OK ? v : plan_call(c, num_cus, plan, &r);
+}
+
 extern "C" int gemm_f16_nt_f8_experts_grad(int64_t S, int64_t E, int64_t M, int64_t N,
                                            const void *a_codes, const void *a_scales,
                                            const void *b_codes, const void *b_scales,
                                            const void *offsets, void *C, hipStream_t stream)
 {
-    int64_t columns = 0;
-    int v = experts_columns(S, E, &columns);
-    if (v != GEMM_F16_OK) return v;
-    Call c{};
-    c.mode = GRAD;
-    c.M = M;
-    c.N = N;
-    c.K = columns;
-    c.a_rows = M;
-    c.matrices = E;
-    c.top = static_cast<int32_t>(S);
-    v = shape_of(1, M, columns, 1, &c.a);
-    if (v == GEMM_F16_OK) v = shape_of(1, N, columns, 1, &c.b);
+    Call c;
+    int v = grad_call(S, E, M, N, &c);
     if (v != GEMM_F16_OK) return v;
     if (cdiv(M, 16) * cdiv(N, 16) > INT32_MAX / round_up(E, 8)) return GEMM_F16_UNSUPPORTED;
     const Array arrays[6] = {{a_codes, c.a.codes, 16, false}, {a_scales, c.a.scales, 4, false},

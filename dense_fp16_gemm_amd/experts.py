@@ -88,6 +88,13 @@ def gemm_f16_f8_quantize_experts(S: int, E: int, R: int, top: int, X: int, rows:
                                                stream), "gemm_f16_f8_quantize_experts")
 
 
+def gemm_f16_nt_f8_experts_grad_plan(S: int, E: int, M: int, N: int, num_cus: int) -> LowbitPlan:
+    plan = LowbitPlan()
+    _check(load().gemm_f16_nt_f8_experts_grad_plan(S, E, M, N, num_cus, ctypes.byref(plan)),
+           "gemm_f16_nt_f8_experts_grad_plan")
+    return plan
+
+
 def gemm_f16_nt_f8_experts_grad(S: int, E: int, M: int, N: int, a_codes: int, a_scales: int,
                                 b_codes: int, b_scales: int, offsets: int, C: int,
                                 stream: int = 0) -> None:

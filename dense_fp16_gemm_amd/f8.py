@@ -50,6 +50,7 @@ def _declare(lib) -> None:
         "gemm_f16_nt_f8_experts_x": [i64, i64, i64, i64, i32, p, p, p, p, p, p, p, i64, p],
         "gemm_f16_f8_experts_columns": [i64, i64, pi64],
         "gemm_f16_f8_quantize_experts": [i64, i64, i64, i32, p, p, p, p, p, p],
+        "gemm_f16_nt_f8_experts_grad_plan": [i64, i64, i64, i64, i32, plan],
         "gemm_f16_nt_f8_experts_grad": [i64, i64, i64, i64, p, p, p, p, p, p, p],
     }.items():
         f = getattr(lib, name)

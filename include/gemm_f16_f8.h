@@ -140,7 +140,7 @@ int gemm_f16_nt_f8_x(int64_t M, int64_t N, int64_t K, const void *X, int32_t b_b
  * expert without rows gets +0.
  *
  * E from 1 to 1024 (GEMM_F16_UNSUPPORTED above).  Workspaces, plans and empty
- * sizes as above; the gradient needs no workspace.
+ * sizes as above; the gradient needs no workspace, its plan tells what it runs.
  */
 int gemm_f16_nt_f8_experts_plan(int64_t S, int64_t E, int64_t N, int64_t K, int32_t top,
                                 int32_t a_f16, int32_t num_cus, gemm_f16_lowbit_plan_t *plan);
@@ -156,6 +156,8 @@ int gemm_f16_f8_experts_columns(int64_t S, int64_t E, int64_t *columns);
 int gemm_f16_f8_quantize_experts(int64_t S, int64_t E, int64_t R, int32_t top, const void *X,
                                  const void *rows, const void *offsets, void *codes,
                                  void *scales, hipStream_t stream);
+int gemm_f16_nt_f8_experts_grad_plan(int64_t S, int64_t E, int64_t M, int64_t N, int32_t num_cus,
+                                     gemm_f16_lowbit_plan_t *plan);
 int gemm_f16_nt_f8_experts_grad(int64_t S, int64_t E, int64_t M, int64_t N, const void *a_codes,
                                 const void *a_scales, const void *b_codes, const void *b_scales,
                                 const void *offsets, void *C, hipStream_t stream);
