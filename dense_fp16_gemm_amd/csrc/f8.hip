@@ -1579,8 +1579,10 @@ struct Choice {
 
 // Time in us of `wgs` workgroups with `steps` groups of columns each, their K in
 // `splits` ranges; bytes of the operands and C.  Rounds of workgroups over the CUs,
-// the memory's rate and the matrix units' at the power limit, and for ranges their
-// sums' way through memory and the join.
+// bytes and multiplications at a rate each, and for ranges their sums' way through
+// memory and the join.  All constants are fitted (planner_fit/fit_f8_model.py, with its
+// timings): that of the multiplications is 1.99 PFLOP/s, a mean over tiles of every size,
+// below what the largest tiles reach.
 static double model(const Kernel &e, double wgs, double steps, int64_t splits, double bytes, int32_t cus)
 {
     const double slots = static_cast<double>(cus) * e.slots;
@@ -1594,12 +1596,13 @@ static double model(const Kernel &e, double wgs, double steps, int64_t splits, d
     return us + 3.16 + (splits > 1 ? 1.76 + 4.0 * wgs * tile / 5.045e6 : 0.0);
 }
 
-// The tile and ring kernels and ranges of K by that model, fitted to 2,200 timings
-// of 144 shapes (1 to 8192 rows, N and K of 64 to 16384, 8 to 256 experts, operands from
-// HBM; they are not kept with the source).  Its error is 6 to 19%; what it chose took 2.7%
-// (products), 1.6% (experts) and 2.3% (gradients) longer than the best of each
-// shape in the mean, 13, 40 and 12% in the worst (2095 tokens, 2 of 256 experts, 3264 x 192:
-// 91.6 us, with 128 x 128 tiles 65.3).
+// The tile and ring kernels and ranges of K by that model, fitted to 2,184 timings
+// of 142 shapes (1 to 8192 rows, N and K of 64 to 16384, 8 to 256 experts, operands from
+// HBM).  Its error, as rms of the logarithm over the shapes, is 6 to 19% by kernel and
+// call; the longest products take less than it says (4096 x 8192 x 8192: 285 us, measured
+// 205 to 237).  What it chose took 2.6% (products), 1.7% (experts) and 2.3% (gradients)
+// longer than the best of each shape in the mean, 13, 40 and 12% in the worst (2095 tokens,
+// 2 of 256 experts, 3264 x 192: 91.6 us, with 128 x 128 tiles 65.3).
 static Choice search(const Call &c, int32_t num_cus)
 {
     const double M = static_cast<double>(c.M), N = static_cast<double>(c.N), K = static_cast<double>(c.a.kp);
