@@ -142,3 +142,143 @@ def test_experts_gradient(g, t, e, top, n, k):
         lo, hi = bounds[i: i + 2]
         assert torch.equal(out[i], product(dy[lo:hi].double().t().contiguous(), xs[lo:hi].t().contiguous())), i
     assert all((v == 3).all() for v in around)
+
+
+# ---- every code --------------------------------------------------------------------
+def every_code(gen, r, k):
+    """Random codes, the subnormal ones as often as others, no NaN: (codes, values)."""
+    codes = torch.randint(0, 127, (r, -(-k // 128) * 128), generator=gen, device="cuda").to(torch.uint8)
+    codes |= torch.randint(0, 2, codes.shape, generator=gen, device="cuda").to(torch.uint8) << 7
+    codes[:, k:] = 0
+    table = torch.from_numpy(ref.code_values()).cuda()
+    return codes.view(torch.float8_e4m3fn), table[codes.long()][:, :k]
+
+
+def ones(r, k):
+    """Rows that have a one each, row i in column 7 i mod k."""
+    x = torch.zeros(r, -(-k // 128) * 128, device="cuda")
+    column = torch.arange(r, device="cuda") * 7 % k
+    x[torch.arange(r, device="cuda"), column] = 1.0
+    return x.to(torch.float8_e4m3fn), column
+
+
+def unscaled(g, codes, k, block):
+    blocks = -(-codes.shape[0] // block)
+    return g.F8Matrix(codes, torch.full((-(-k // 512), blocks, 4), 127, dtype=torch.uint8, device="cuda"), k, block)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 300, 1100), (7, 300, 600), (16, 300, 1700), (70, 300, 200), (300, 264, 2048),
+                                   (333, 1001, 4000), (1000, 2050, 300), (4097, 2050, 130), (3001, 4096, 130)])
+def test_every_code(g, m, n, k):
+    """A code times one is that code's number, as A's operand and as B's, in every kernel."""
+    gen = generator(m + n)
+    codes, values = every_code(gen, m, k)
+    one, column = ones(n, k)
+    c = g.gemm_nt_f8(unscaled(g, codes, k, 1), unscaled(g, one, k, 128))
+    assert torch.equal(c.double(), values[:, column])
+    codes, values = every_code(gen, n, k)
+    one, column = ones(m, k)
+    for block in (1, 128):
+        w = unscaled(g, codes, k, block)
+        for a in (unscaled(g, one, k, 1), one[:, :k].half()):
+            assert torch.equal(g.gemm_nt_f8(a, w).double(), values[:, column].t())
+
+
+# ---- beyond 32 bits ------------------------------------------------------------------
+def big_codes(gen, *shape):
+    """Codes of small whole numbers, one in eight not zero."""
+    codes = torch.zeros(shape, dtype=torch.uint8, device="cuda")
+    table = torch.zeros(32, dtype=torch.uint8, device="cuda")
+    table[:4] = torch.tensor([0xc0, 0xb8, 0x38, 0x40], dtype=torch.uint8)
+    for part in codes.view(-1).split(2 ** 28):
+        part.copy_(table[torch.randint(0, 32, part.shape, generator=gen, device="cuda", dtype=torch.uint8).int()])
+    return codes.view(torch.float8_e4m3fn)
+
+
+def test_stack_beyond_32_bits(g):
+    """A stack of experts' matrices past 2^32 bytes of codes: quantised, read back and
+    multiplied, forward and both gradients; its first and last matrices as by themselves."""
+    gen = generator(1)
+    e, n, k, top = 160, 4096, 7168, 2
+    w8 = g.F8Matrix(big_codes(gen, e, n, k), torch.randint(126, 129, (e, k // 512, n // 128, 4), generator=gen,
+                                                           device="cuda", dtype=torch.uint8), k, 128)
+    assert w8.codes.numel() > 2 ** 32
+    some = (0, e // 2, e - 1)
+    w = g.dequantize_f8(w8)
+    alone = {i: g.dequantize_f8(g.F8Matrix(w8.codes[i], w8.scales[i], k, 128)) for i in some}
+    assert all(torch.equal(w[i], alone[i]) for i in some)
+    again, turned = g.quantize_f8(w, 128), g.quantize_f8(w, 128, transposed=True)
+    del w
+    for i in some:
+        for stack, transposed in ((again, False), (turned, True)):
+            one = g.quantize_f8(alone[i], 128, transposed)
+            assert torch.equal(stack.codes[i].view(torch.uint8), one.codes.view(torch.uint8))
+            assert torch.equal(stack.scales[i], one.scales)
+    del again
+    for t in (1, 40, 3000):
+        logits = torch.randn(t, e, generator=gen, device="cuda")
+        logits[:, 0] += 2
+        logits[:, e - 1] += 2
+        logits[0, e - 1] = 50
+        r = g.route(logits, top)
+        bounds = r.offsets.tolist()
+        assert bounds[e] > bounds[e - 1]
+        x, dy = whole_halves(gen, t, k), whole_halves(gen, t * top, n)
+        tokens = r.rows.long() // top
+        y = g.gemm_nt_f8_experts(x, w8, r, gather=True)
+        dx = g.gemm_nt_f8_experts(dy, turned, r)
+        dw = g.gemm_nt_f8_experts_grad(g.quantize_f8_experts(dy, r), g.quantize_f8_experts(x, r, gather=True), r)
+        assert dw.numel() * 2 > 2 ** 32
+        for i in some:
+            lo, hi = bounds[i: i + 2]
+            xi, dyi = x[tokens[lo:hi]].double(), dy[lo:hi].double()
+            assert torch.equal(y[lo:hi], product(xi, alone[i].double()))
+            assert torch.equal(dx[lo:hi], product(dyi, alone[i].double().t()))
+            assert torch.equal(dw[i], product(dyi.t().contiguous(), xi.t()))
+        del y, dx, dw
+
+
+def test_matrix_beyond_32_bits(g):
+    """Rows of activations past 2^32 codes, and their transpose, whose groups run along
+    the rows: a layer's product and its weight's gradient."""
+    gen = generator(2)
+    t, k, n = 2 ** 20 + 37, 4160, 96
+    x = torch.zeros(t, k, dtype=torch.float16, device="cuda")
+    for part in x.split(2 ** 16):
+        part.copy_(torch.randint(-2, 3, part.shape, generator=gen, device="cuda", dtype=torch.int8))
+    x8 = g.quantize_f8(x)
+    assert x8.codes.numel() > 2 ** 32
+    w = whole_halves(gen, n, k)
+    for part in (slice(0, 300), slice(t - 300, t)):
+        want = product(x[part].double(), w.double())
+        one = g.quantize_f8(x[part].contiguous())
+        assert torch.equal(x8.codes[part].view(torch.uint8), one.codes.view(torch.uint8))
+        for a in (x, x8):
+            assert torch.equal(g.gemm_nt_f8(a, g.quantize_f8(w, 128))[part], want)
+    back = g.dequantize_f8(x8)
+    assert torch.equal(back[-300:], x[-300:]) and torch.equal(back[:300], x[:300])
+    del x8, back
+    xt = g.quantize_f8(x, transposed=True)
+    assert xt.codes.numel() > 2 ** 32
+    # one row in 64 has a gradient, so that sums of whole numbers stay far below 2^24
+    dy = torch.zeros(t, n, dtype=torch.float16, device="cuda")
+    dy[::64] = whole_halves(gen, len(range(0, t, 64)), n)
+    dy[-1] = 1
+    want = torch.zeros(n, k, dtype=torch.float64, device="cuda")
+    on = dy.any(1).nonzero()[:, 0]
+    for part in on.split(4096):
+        want += torch.matmul(dy[part].double().t().contiguous(), x[part].double())
+    assert want.abs().max() < 2 ** 20
+    assert torch.equal(g.gemm_nt_f8(g.quantize_f8(dy, transposed=True), xt), want.half())
+
+
+def test_output_beyond_32_bits(g):
+    """C past 2^32 bytes: its first, middle and last rows."""
+    gen = generator(3)
+    m, n, k = 36000, 65500, 130
+    ac, as_, a = whole(gen, m, k, 1)
+    bc, bs, b = whole(gen, n, k, 128)
+    c = g.gemm_nt_f8(g.F8Matrix(ac, as_, k, 1), g.F8Matrix(bc, bs, k, 128))
+    assert c.numel() * 2 > 2 ** 32
+    for part in (slice(0, 260), slice(m // 2, m // 2 + 260), slice(m - 260, m)):
+        assert torch.equal(c[part], product(a[part], b))
