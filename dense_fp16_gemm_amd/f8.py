@@ -111,7 +111,7 @@ class F8Matrix:
     float8_e4m3fn [.., r, 128 ceil(k / 128)], zero past k, and scales uint8 [..,
     ceil(k / 512), ceil(r / block), 4] (exponents + 127; the four of a row are
     those of neighbouring groups of 128 columns), as quantize_f8() makes them.
-    The tensors are kept, not copied."""
+    The tensors are kept, not copied.  Saved and read back as a W4Matrix is."""
 
     __slots__ = ("codes", "scales", "k", "block")
 
@@ -139,8 +139,15 @@ class F8Matrix:
         self.codes, self.scales, self.k, self.block = codes, scales, k, block
         return self
 
-    def __reduce__(self):
-        return type(self), (self.codes, self.scales, self.k, self.block)
+    # stored with the codes as bytes: pickle by itself reads no float8 tensor back
+    def __getstate__(self):
+        return self.codes.view(_uint8), self.scales, self.k, self.block
+
+    def __setstate__(self, state):
+        if torch is None:
+            _bind_torch()
+        codes, scales, k, block = state
+        self.__init__(codes.view(_f8), scales, k, block)
 
     @property
     def shape(self) -> tuple:

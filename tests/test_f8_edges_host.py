@@ -1,6 +1,12 @@
 """The 8-bit floating point operands and the experts' layers at the edges of what
 their headers allow, without a GPU."""
+import os
+import pickle
+import subprocess
+import sys
+
 import pytest
+import torch
 
 from test_f8_host import INVALID, UNSUPPORTED, g, refused  # noqa: F401  (g: the fixture)
 
@@ -50,3 +56,52 @@ def test_gradients_plans(g):
     refused(g, INVALID, plan, 8, 4, 16, 128, 0)
     refused(g, UNSUPPORTED, plan, 8, 1025, 16, 128, 256)
     refused(g, UNSUPPORTED, plan, 8, 1024, 2 ** 20, 2 ** 20, 256)
+
+
+# ---- matrices and routings whose tensors left the GPU -------------------------------
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def on_cpu(g):
+    g.f8._bind_torch()     # as the first matrix does
+    matrix = g.F8Matrix.__new__(g.F8Matrix)._set(torch.zeros(4, 128).to(torch.float8_e4m3fn),
+                                                 torch.zeros(1, 4, 4, dtype=torch.uint8), 128, 1)
+    i = torch.zeros(4, 2, dtype=torch.int32)
+    routing = g.Routing.__new__(g.Routing)._set(i, torch.zeros(4, 2), i.view(-1), i, torch.zeros(9, dtype=torch.int32),
+                                                "softmax", True, 1.0)
+    return matrix, routing
+
+
+IN_A_NEW_PROCESS = """
+import pickle, sys
+sys.path.insert(0, sys.argv[1])
+import torch, dense_fp16_gemm_amd as g
+try:
+    pickle.loads(sys.stdin.buffer.read())
+except ValueError as e:
+    assert "GPU" in str(e), e
+    print("refused")
+"""
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_read_back_is_checked(g, which):
+    """What was stored goes through its constructor again, also where that is the first
+    use of the package in a process."""
+    stored = pickle.dumps(on_cpu(g)[which])
+    with pytest.raises(ValueError, match="GPU"):
+        pickle.loads(stored)
+    r = subprocess.run([sys.executable, "-c", IN_A_NEW_PROCESS, ROOT], timeout=300, input=stored, capture_output=True)
+    assert r.returncode == 0 and r.stdout == b"refused\n", r.stderr.decode()[-2000:]
+
+
+def test_host_memory_is_refused(g):
+    """By every function that takes a matrix or a routing."""
+    q, r = on_cpu(g)
+    x, dy = torch.zeros(4, 128).half(), torch.zeros(8, 128).half()
+    for call in (lambda: g.dequantize_f8(q), lambda: g.gemm_nt_f8(q, q), lambda: g.gemm_nt_f8(x, q),
+                 lambda: g.route_backward(torch.zeros(4, 8), r, r.weights), lambda: g.quantize_f8_experts(dy, r),
+                 lambda: g.gemm_nt_f8_experts(x, q, r, gather=True), lambda: g.gemm_nt_f8_experts_grad(q, q, r),
+                 lambda: g.combine_experts(dy, r), lambda: g.combine_experts_backward(x, dy, r)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
