@@ -152,7 +152,9 @@ class Routing:
                            are the experts' loads)
 
     and how the weights come from the logits (scores, renormalize, scale), for
-    route_backward().  The tensors are kept, not copied."""
+    route_backward().  The tensors are kept, not copied.  Those that route() makes
+    are, but for the weights, parts of one allocation: whoever keeps or saves one of them
+    (not a clone() of it) keeps all four.  Saved and read back as a W4Matrix is."""
 
     __slots__ = ("experts", "weights", "rows", "places", "offsets", "scores", "renormalize",
                  "scale")
@@ -254,16 +256,19 @@ def route(logits, top: int, scores: str = "softmax", bias=None, groups: int = 1,
                              bias.device != logits.device or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous float32 [{e}] tensor on {logits.device}")
     top, index = int(top), logits.get_device()
-    # one allocation: experts, weights, rows, places and offsets, as tensors of their
-    # own (views of one cost the host 1 us more)
+    # one allocation for experts, rows, places and offsets, as tensors of their own (views
+    # of one cost the host 1 us more); the weights, of another type, apart, since torch
+    # saves no tensors of two types that share memory
     slots = t * top
-    size = 4 * slots + e + 1
-    memory = _empty((size,), (1,), dtype=_int32, device=logits.device) if stream is None else \
-        _new(logits, stream, (size,), _int32)
-    experts, weights, rows, places, offsets = \
-        memory.unsafe_split_with_sizes((slots, slots, slots, slots, e + 1))
+    size = 3 * slots + e + 1
+    if stream is None:
+        memory = _empty((size,), (1,), dtype=_int32, device=logits.device)
+        weights = _empty((t, top), (top, 1), dtype=_f32, device=logits.device)
+    else:
+        memory = _new(logits, stream, (size,), _int32)
+        weights = _new(logits, stream, (t, top), _f32)
+    experts, rows, places, offsets = memory.unsafe_split_with_sizes((slots, slots, slots, e + 1))
     experts, places = experts.view(t, top), places.view(t, top)
-    weights = weights.view(_f32).view(t, top)
     key = (t, e, top)
     need = _route_bytes.get(key)
     if need is None:
@@ -274,8 +279,8 @@ def route(logits, top: int, scores: str = "softmax", bias=None, groups: int = 1,
     at, each = memory.data_ptr(), 4 * slots
     _call(index, stream, _lib.gemm_f16_route, t, e, top, ROUTE_SCORES[scores], groups, top_groups,
           group_score == "max", bool(renormalize), scale, logits.data_ptr(),
-          logits.dtype is _f32, 0 if bias is None else bias.data_ptr(), at, at + each,
-          at + 2 * each, at + 3 * each, at + 4 * each, 0 if ws is None else ws.data_ptr(), need)
+          logits.dtype is _f32, 0 if bias is None else bias.data_ptr(), at, weights.data_ptr(),
+          at + each, at + 2 * each, at + 3 * each, 0 if ws is None else ws.data_ptr(), need)
     if stream is not None:
         _record(stream, logits, bias, ws)
     return Routing.__new__(Routing)._set(experts, weights, rows, places, offsets, scores,

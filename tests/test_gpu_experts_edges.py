@@ -1,8 +1,15 @@
-"""Layers of experts at the edges of what their headers allow."""
+"""8-bit products and layers of experts as programs use them: at the edges of what
+their headers allow, on other streams, saved and read back, all steps together."""
+import copy
+import os
+import pickle
+import subprocess
+import sys
+
 import pytest
 import torch
 
-from test_gpu_f8 import g  # noqa: F401  (the fixture)
+from test_gpu_f8 import g  # noqa: F401  (g: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +106,70 @@ def test_streams_of_another_device_are_refused(g):
     for call in calls:
         with pytest.raises(ValueError, match="stream is on"):
             call()
+
+
+# ---- saved and read back -----------------------------------------------------------
+READ_BACK = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch, dense_fp16_gemm_amd as g
+safe = sys.argv[3] == "safe"
+if safe:
+    torch.serialization.add_safe_globals([g.F8Matrix, g.Routing])
+stored = torch.load(sys.argv[2], weights_only=safe)
+def same(a, b):
+    assert torch.equal(a, b)
+if "gemm_nt_f8" in stored:
+    a, w, stack, y, values = stored["gemm_nt_f8"]
+    assert (a.shape, a.block, w.shape, w.block, stack.shape) == ((3, 200), 1, (50, 200), 128, (4, 50, 200))
+    same(g.gemm_nt_f8(a, w), y)
+    same(g.dequantize_f8(stack), values)
+else:
+    r, logits, x, w, y, out, dlogits = stored["route"]
+    assert (r.tokens, r.top, r.n_experts, r.scores, r.renormalize, r.scale) == (30, 2, 4, "sigmoid", False, 2.5)
+    same(g.combine_experts(y, r), out)
+    same(g.gemm_nt_f8_experts(x, w, r, gather=True), y)
+    same(g.route_backward(logits, r, torch.ones_like(r.weights)), dlogits)
+print("same")
+"""
+
+
+@pytest.mark.parametrize("how", ["safe", "any"])
+@pytest.mark.parametrize("what", ["gemm_nt_f8", "route"])
+def test_saved_in_a_new_process(g, how, what, tmp_path):
+    """Matrices and a routing, saved whole: in a process whose first use of the package
+    is of what it read back."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def halves(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").half()
+
+    stack = g.quantize_f8(halves(4, 50, 200), 128)
+    if what == "gemm_nt_f8":
+        a, w = g.quantize_f8(halves(3, 200)), g.quantize_f8(halves(50, 200), 128)
+        stored = a, w, stack, g.gemm_nt_f8(a, w), g.dequantize_f8(stack)
+    else:
+        logits, x = torch.randn(30, 4, generator=gen, device="cuda"), halves(30, 200)
+        r = g.route(logits, 2, "sigmoid", renormalize=False, scale=2.5)
+        y = g.gemm_nt_f8_experts(x, stack, r, gather=True)
+        stored = r, logits, x, stack, y, g.combine_experts(y, r), g.route_backward(logits, r, torch.ones_like(r.weights))
+    path = str(tmp_path / "stored.pt")
+    torch.save({what: stored}, path)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", READ_BACK, root, path, how], timeout=100, capture_output=True)
+    assert done.returncode == 0 and done.stdout == b"same\n", done.stderr.decode()[-2000:]
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda x: pickle.loads(pickle.dumps(x))])
+def test_copies(g, how):
+    """Copies hold the same and are checked as what a program makes itself."""
+    x = torch.randn(7, 130, device="cuda").half()
+    q = g.quantize_f8(x)
+    again = how(q)
+    assert (again.shape, again.block) == (q.shape, q.block)
+    assert torch.equal(g.dequantize_f8(again), g.dequantize_f8(q))
+    r = g.route(torch.randn(7, 5, device="cuda"), 2, scale=0.5)
+    s = how(r)
+    assert (s.scores, s.renormalize, s.scale, s.n_experts) == (r.scores, r.renormalize, r.scale, r.n_experts)
+    assert torch.equal(g.combine_experts(x.repeat(2, 1), s), g.combine_experts(x.repeat(2, 1), r))
+    assert (s.weights.data_ptr() == r.weights.data_ptr()) == (how is copy.copy)
