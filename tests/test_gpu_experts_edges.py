@@ -6,10 +6,13 @@ import pickle
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_f8 import g  # noqa: F401  (g: the fixture)
+import f8_ref as ref
+from test_gpu_experts import layer, layer_inputs
+from test_gpu_f8 import dev, g, host  # noqa: F401  (g: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -106,6 +109,241 @@ def test_streams_of_another_device_are_refused(g):
     for call in calls:
         with pytest.raises(ValueError, match="stream is on"):
             call()
+
+
+LIVES = ["quantize rows", "quantize transposed", "quantize blocks", "dequantize", "product of few halves",
+         "product, workspace", "product of codes", "route", "route_backward", "experts of few halves", "experts, gathered",
+         "experts, workspace", "quantize_f8_experts", "experts' gradients", "combine", "combine_backward", "combine_backward, unweighted"]
+
+
+def operands_and_call(g, what):
+    """(call(**kw) giving tensors, the tensors that it is given, each its own memory)."""
+    rng = np.random.default_rng(3)
+    t, e, top, n, k = 700, 16, 2, 520, 768
+
+    def halves(*shape):
+        return dev(rng.standard_normal(shape).astype(np.float16))
+
+    def codes(q):
+        return q.codes.view(torch.uint8), q.scales
+
+    cus = g.gemm_f16_device_cus()
+    if what.startswith("quantize "):
+        x = halves(1024, 2048)
+        how = {"quantize rows": (1, False), "quantize transposed": (1, True), "quantize blocks": (128, False)}[what]
+        return lambda **kw: codes(g.quantize_f8(x, *how, **kw)), [x]
+    if what == "dequantize":
+        q = g.quantize_f8(halves(1024, 2048))
+        return lambda **kw: (g.dequantize_f8(q, **kw),), [q.codes, q.scales]
+    if what.startswith("product"):
+        w = g.quantize_f8(halves(1024, 2048), 128)
+        a = halves(7 if what == "product of few halves" else 300, 2048)
+        if what == "product of codes":
+            q = g.quantize_f8(a)
+            return lambda **kw: (g.gemm_nt_f8(q, w, **kw),), [q.codes, q.scales, w.codes, w.scales]
+        need = g.gemm_f16_nt_f8_plan(len(a), 1024, 2048, 128, True, cus).workspace_bytes
+        if what == "product of few halves":
+            assert need == 0
+            return lambda **kw: (g.gemm_nt_f8(a, w, **kw),), [a, w.codes, w.scales]
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        return lambda **kw: (g.gemm_nt_f8(a, w, workspace=ws, **kw),), [a, w.codes, w.scales, ws]
+    few = what == "experts of few halves"
+    t = 3 if few else t
+    logits, bias = dev(rng.standard_normal((t, e)).astype(np.float32)), dev(rng.standard_normal(e).astype(np.float32))
+    if what == "route":
+        def call(**kw):
+            r = g.route(logits, top, "sigmoid", bias, **kw)
+            return r.experts, r.weights, r.rows, r.places, r.offsets
+        return call, [logits, bias]
+    r = g.route(logits, top)
+    r = g.Routing(*(x.clone() for x in (r.experts, r.weights, r.rows, r.places, r.offsets)))   # each its own memory
+    y, x = halves(t * top, n), halves(t, k)
+    if what == "route_backward":
+        dw = dev(rng.standard_normal((t, top)).astype(np.float32))
+        return lambda **kw: (g.route_backward(logits, r, dw, **kw),), [logits, r.experts, r.weights, dw]
+    if what == "quantize_f8_experts":
+        used = sum(-(-c // 128) for c in r.offsets.diff().tolist())
+
+        def call(**kw):
+            q = g.quantize_f8_experts(x, r, gather=True, **kw)
+            scales = q.scales.permute(1, 0, 2).reshape(k, -1)
+            return q.codes.view(torch.uint8)[:, :128 * used], scales[:, :used]
+        return call, [x, r.rows, r.offsets]
+    if what == "experts' gradients":
+        a, b = g.quantize_f8_experts(y, r), g.quantize_f8_experts(x, r, gather=True)
+        return lambda **kw: (g.gemm_nt_f8_experts_grad(a, b, r, **kw),), [a.codes, a.scales, b.codes, b.scales, r.offsets]
+    if what.startswith("experts"):
+        w = g.quantize_f8(halves(e, n, k), 128)
+        given = [x, w.codes, w.scales, r.rows, r.offsets]
+        need = g.gemm_f16_nt_f8_experts_plan(t * top, e, n, k, top, True, cus).workspace_bytes
+        assert (need == 0) == few
+        if what != "experts, workspace":
+            return lambda **kw: (g.gemm_nt_f8_experts(x, w, r, True, **kw),), given
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        return lambda **kw: (g.gemm_nt_f8_experts(x, w, r, True, workspace=ws, **kw),), given + [ws]
+    if what == "combine":
+        return lambda **kw: (g.combine_experts(y, r, **kw),), [y, r.weights, r.places]
+    dout = halves(t, n)
+    if what == "combine_backward":
+        return lambda **kw: g.combine_experts_backward(dout, y, r, **kw), [dout, y, r.weights, r.rows, r.places]
+    return lambda **kw: g.combine_experts_backward(dout, None, r, False, **kw)[:1], [dout, r.rows, r.places]
+
+
+@pytest.mark.parametrize("what", LIVES)
+def test_operands_dropped_at_once(g, what):
+    """Operands (and a workspace) of the default stream, used on a busy stream and
+    dropped at once: their memory goes to no other tensor before they are read."""
+    want = [host(t) for t in operands_and_call(g, what)[0]()]
+    s, done = torch.cuda.Stream(), torch.cuda.Event()
+    filler = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    # torch's memory for what both streams allocate later: new memory from the
+    # driver would wait for s
+    operands_and_call(g, what)[0](stream=s)
+    s.synchronize()
+    call, given = operands_and_call(g, what)
+    ranges = [(t.data_ptr(), t.numel() * t.element_size()) for t in given]
+    spare = [torch.empty(size, dtype=torch.uint8, device="cuda") for _, size in ranges for _ in range(8)]
+    del spare
+    torch.cuda.synchronize()     # the operands are made
+    with torch.cuda.stream(s):
+        for _ in range(200):   # some 40 ms
+            filler[:1 << 29].copy_(filler[1 << 29:])
+    got = call(stream=s)
+    done.record(s)
+    del call, given
+    later = [torch.empty(size, dtype=torch.uint8, device="cuda") for _, size in ranges for _ in range(4)]
+    # (asked before the default stream gets work: it may share a hardware queue with s)
+    assert not done.query(), "the stream was not busy for long enough to show anything"
+    for t in later:
+        for at, size in ranges:
+            assert t.data_ptr() + t.numel() <= at or at + size <= t.data_ptr()
+        t.fill_(0x55)
+    s.synchronize()
+    for t, w in zip(got, want):
+        np.testing.assert_array_equal(host(t), w)
+
+
+def test_layer_on_another_stream(g):
+    """A layer and its gradients on a stream that waits for their inputs, against the
+    same on the default stream."""
+    rng = np.random.default_rng(11)
+    x, wr, up, down = layer_inputs(g, rng, 90, 256, 128, 8)
+    up8, down8 = g.quantize_f8(up, 128), g.quantize_f8(down, 128)
+    logits, r, h, y, out = layer(g, x, wr, up8, down8, 2)
+
+    def steps(logits, h, dout, **kw):
+        r = g.route(logits, 2, "sigmoid", groups=2, top_groups=1, scale=1.5, **kw)
+        y = g.gemm_nt_f8_experts(h, down8, r, **kw)
+        out = g.combine_experts(y, r, **kw)
+        dy, dw = g.combine_experts_backward(dout, y, r, **kw)
+        dlogits = g.route_backward(logits, r, dw, **kw)
+        ddown = g.gemm_nt_f8_experts_grad(g.quantize_f8_experts(dy, r, **kw), g.quantize_f8_experts(h, r, **kw), r, **kw)
+        single = g.gemm_nt_f8(g.quantize_f8(h, **kw), g.quantize_f8(down[0], 128, **kw), **kw)
+        return out, dlogits, ddown, single, g.dequantize_f8(up8, **kw)
+
+    want = steps(logits, h, out)
+    s = torch.cuda.Stream()
+    copies = logits.clone(), h.clone(), out.clone()
+    s.wait_stream(torch.cuda.current_stream())
+    got = steps(*copies, stream=s)
+    del copies
+    s.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+# ---- all steps together ------------------------------------------------------------
+@pytest.mark.parametrize("t", [1, 7, 150])
+@pytest.mark.parametrize("scores,renormalize", [("sigmoid", True), ("softmax", True), ("softmax", False)])
+def test_layer_step_by_step(g, t, scores, renormalize):
+    """A layer of experts and all its gradients, some tokens padding: each step's output
+    against 64 bits on the inputs that it was given."""
+    rng = np.random.default_rng(t)
+    d, f, e, top, scale = 256, 200, 8, 3, 1.5
+    x, wr, up, down = layer_inputs(g, rng, t, d, f, e)
+    logits = g.gemm_nt(x, wr)
+    if t > 1:
+        logits[t // 2] = -torch.inf
+        logits[0, 2:] = -torch.inf        # fewer experts than choices
+    r = g.route(logits, top, scores, renormalize=renormalize, scale=scale)
+    h = torch.relu(g.gemm_nt_f8_experts(x, g.quantize_f8(up, 128), r, gather=True))
+    y = g.gemm_nt_f8_experts(h, g.quantize_f8(down, 128), r)
+    out = g.combine_experts(y, r)
+    dout = dev(rng.standard_normal((t, d)).astype(np.float16))
+    dy, dweights = g.combine_experts_backward(dout, y, r)
+    dlogits = g.route_backward(logits, r, dweights)
+    dh = torch.where(h > 0, g.gemm_nt_f8_experts(dy, g.quantize_f8(down, 128, transposed=True), r), 0)
+    dxs = g.gemm_nt_f8_experts(dh, g.quantize_f8(up, 128, transposed=True), r)
+    dx = g.combine_experts(dxs, r, weighted=False)
+    dx_router = g.matmul(dlogits, wr)
+    dwr = g.matmul(dlogits.t(), x)
+
+    lg = host(logits).astype(np.float64)
+    experts, weights = ref.route(host(logits), top, scores, renormalize=renormalize, scale=scale)
+    np.testing.assert_array_equal(host(r.experts), experts)
+    w = host(r.weights).astype(np.float64)
+    # one rounding to fp32, and sums of 64-bit scores in another order
+    assert (np.abs(w - weights) <= np.abs(weights) * (2.0 ** -24 + 2.0 ** -40) + 2.0 ** -150).all()
+    rows, places, offsets = ref.order(experts, e)
+    for a, b in ((r.rows, rows), (r.places, places), (r.offsets, offsets)):
+        np.testing.assert_array_equal(host(a), b)
+
+    there = (places >= 0)[..., None]
+
+    def of_tokens(v):
+        return np.where(there, host(v)[np.maximum(places, 0)].astype(np.float64), 0.0)
+
+    def summed(got, factor, v):
+        """Sums over a token's choices in fp32 (a rounding each), rounded to fp16."""
+        terms = factor[..., None] * of_tokens(v)
+        exact, size = terms.sum(1), np.abs(terms).sum(1)
+        off = size * (top + 1) * 2.0 ** -24
+        assert (np.abs(host(got) - exact) <= off + (np.abs(exact) + off) * 2.0 ** -11 + 2.0 ** -25).all()
+
+    summed(out, w, y)
+    summed(dx, np.ones_like(w), dxs)
+
+    do = host(dout).astype(np.float64)
+    want = np.zeros((t * top, d))
+    for i, j in zip(*np.nonzero(places >= 0)):
+        want[places[i, j]] = w[i, j] * do[i]
+    # a product in fp32, then in fp16: 2^-24 and 2^-11, 2^-25 among the subnormals
+    assert (np.abs(host(dy) - want) <= np.abs(want) * (2.0 ** -11 + 2.0 ** -23) + 2.0 ** -25).all()
+    terms = do[:, None] * of_tokens(y)
+    # products and sums of d terms in fp32, a rounding each and 16 to join
+    assert (np.abs(host(dweights) - terms.sum(2)) <= np.abs(terms).sum(2) * (d + 16) * 2.0 ** -24).all()
+
+    dw = host(dweights).astype(np.float64)
+    want = ref.route_gradient(lg, experts, dw, scores, renormalize, scale)
+    # one rounding to fp16; 64-bit sums of at most top + e terms of 4 scale dw / (least sum) in size
+    size = 4 * scale * np.abs(dw).max(1, keepdims=True) * (top + e + 40) * 2.0 ** -52 * 2.0 ** 10
+    assert (np.abs(host(dlogits) - want) <= np.abs(want) * 2.0 ** -11 + 2.0 ** -25 + size).all()
+
+    def near(got, a, b):
+        """A product in 8-bit codes within the bound."""
+        exact = a @ b.T
+        bound = ref.product_bound(np.abs(a) @ np.abs(b).T, exact, a.shape[1])
+        assert (np.abs(host(got).astype(np.float64) - exact) <= bound).all()
+
+    dl, q = host(dlogits).astype(np.float64), ref.quantized
+    ddown = g.gemm_nt_f8_experts_grad(g.quantize_f8_experts(dy, r), g.quantize_f8_experts(h, r), r)
+    dup = g.gemm_nt_f8_experts_grad(g.quantize_f8_experts(dh, r), g.quantize_f8_experts(x, r, gather=True), r)
+    for i in range(e):
+        a, b = offsets[i], offsets[i + 1]
+        if a == b:
+            assert (host(dup[i]) == 0).all() and (host(ddown[i]) == 0).all()
+            continue
+        xi = host(x)[rows[a:b] // top]
+        near(y[a:b], q(host(h[a:b]), 1), q(host(down[i]), 128))
+        near(dxs[a:b], q(host(dh[a:b]), 1), q(host(up[i]), 128).T)
+        near(ddown[i], q(host(dy[a:b]).T.copy(), 1), q(host(h[a:b]).T.copy(), 1))
+        near(dup[i], q(host(dh[a:b]).T.copy(), 1), q(xi.T.copy(), 1))
+    for v in (y, dy, dxs):
+        assert (host(v[offsets[-1]:]) == 0).all()
+    for got, a, b in ((dx_router, dl, host(wr).astype(np.float64)), (dwr, dl.T, host(x).astype(np.float64))):
+        exact, size = a @ b, np.abs(a) @ np.abs(b)
+        off = size * (a.shape[1] + 16) * 2.0 ** -23          # fp32 sums
+        assert (np.abs(host(got) - exact) <= off + (np.abs(exact) + off) * 2.0 ** -11 + 2.0 ** -25).all()
 
 
 # ---- saved and read back -----------------------------------------------------------
