@@ -79,6 +79,86 @@ def test_combine_widest_of_no_expert(g):
     assert all((v == 3).all() for v in around)
 
 
+# ---- nothing, and more than 32 bits ----------------------------------------------------
+@pytest.mark.parametrize("t,top", [(0, 1), (0, 3), (5, 2)])
+def test_layer_of_nothing(g, t, top):
+    """No tokens, or none that has an expert: gradients of weights are 0, the rest is
+    empty or 0."""
+    e, n, k = 4, 130, 200
+    logits = torch.full((t, e), -torch.inf, device="cuda")
+    x = torch.ones(t, k, dtype=torch.float16, device="cuda")
+    w8 = g.quantize_f8(torch.ones(e, n, k, dtype=torch.float16, device="cuda"), 128)
+    wt8 = g.quantize_f8(torch.ones(e, n, k, dtype=torch.float16, device="cuda"), 128, transposed=True)
+    r = g.route(logits, top)
+    assert r.experts.shape == r.weights.shape == r.places.shape == (t, top) and r.rows.shape == (t * top,)
+    assert r.offsets.tolist() == [0] * (e + 1)
+    for a in (x, g.quantize_f8(x)):
+        y = g.gemm_nt_f8_experts(a, w8, r, gather=True)
+        assert y.shape == (t * top, n) and (y == 0).all()
+    out = g.combine_experts(y, r)
+    assert out.shape == (t, n) and (out == 0).all()
+    dout = torch.ones(t, n, dtype=torch.float16, device="cuda")
+    dy, dw = g.combine_experts_backward(dout, y, r)
+    assert dy.shape == y.shape and (dy == 0).all() and dw.shape == (t, top) and (dw == 0).all()
+    dlogits = g.route_backward(logits, r, dw)
+    assert dlogits.shape == (t, e) and (dlogits == 0).all()
+    dx = g.combine_experts(g.gemm_nt_f8_experts(dy, wt8, r), r, weighted=False)
+    assert dx.shape == (t, k) and (dx == 0).all()
+    dy8, x8 = g.quantize_f8_experts(dy, r), g.quantize_f8_experts(x, r, gather=True)
+    grad = g.gemm_nt_f8_experts_grad(dy8, x8, r, out=torch.full((e, n, k), 9.0, dtype=torch.float16, device="cuda"))
+    assert (grad == 0).all()
+
+
+def test_rows_beyond_32_bits(g):
+    """Experts' rows past 2^32 bytes, and past 2^32 codes: combined, their gradients, and
+    the products' operands and outputs."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    t, e, top, n, k = 300000, 8, 4, 4160, 96
+    r = g.route(torch.randn(t, e, device="cuda", generator=gen), top)
+    assert t * top * n > 2 ** 32
+    some = torch.cat((torch.arange(0, 200), torch.arange(t - 200, t))).cuda()
+    w = torch.randint(-2, 3, (e, k, n), device="cuda", generator=gen).half()
+    y = torch.empty(t * top, n, dtype=torch.float16, device="cuda")
+    for part in y.split(2 ** 16):
+        part.copy_(torch.randint(-2, 3, part.shape, generator=gen, device="cuda", dtype=torch.int8))
+    # a token's rows together: whole numbers
+    sums = y[r.places[some].long()].double().sum(1)
+    assert torch.equal(g.combine_experts(y, r, weighted=False)[some].double(), sums)
+    # the rows' products, K past 2^32 codes
+    c = g.gemm_nt_f8_experts(y, g.quantize_f8(w, 128), r)
+    experts, places = r.experts[some].long(), r.places[some].long()
+    want = torch.stack([torch.matmul(w[i].double(), v.double()) for i, v in
+                        zip(experts.view(-1).tolist(), y[places.view(-1)])])
+    assert torch.equal(c[places.view(-1)], want.half())
+    del c
+    # the weights' gradients, of few rows that are not zero
+    dc = torch.zeros(t * top, k, dtype=torch.float16, device="cuda")
+    on = places[::40].reshape(-1)
+    dc[on] = torch.randint(-2, 3, (on.numel(), k), generator=gen, device="cuda").half()
+    y8 = g.quantize_f8_experts(y, r)
+    assert y8.codes.numel() > 2 ** 32
+    grad = g.gemm_nt_f8_experts_grad(g.quantize_f8_experts(dc, r), y8, r)
+    want = torch.zeros(e, k, n, dtype=torch.float64, device="cuda")
+    for at, i in zip(on.tolist(), experts[::40].reshape(-1).tolist()):
+        want[i] += dc[at].double()[:, None] * y[at].double()
+    assert torch.equal(grad, want.half())
+    del y8
+    # outputs past 2^32 bytes, and the gradients of the combination
+    wt8 = g.quantize_f8(w, 128, transposed=True)
+    rows = g.gemm_nt_f8_experts(dc, wt8, r)
+    want = torch.stack([torch.matmul(w[i].double().t().contiguous(), dc[at].double()) for at, i in
+                        zip(on.tolist(), experts[::40].reshape(-1).tolist())])
+    assert torch.equal(rows[on], want.half())
+    del rows
+    dout = torch.randint(-2, 3, (t, n), device="cuda", generator=gen, dtype=torch.int8).half()
+    dy, dw = g.combine_experts_backward(dout, y, r)
+    weights = r.weights[some].double()
+    want = weights[..., None] * dout[some][:, None].double()
+    # a product in fp32, then in fp16: 2^-24 and 2^-11, 2^-25 among the subnormals
+    assert ((dy[places].double() - want).abs() <= want.abs() * (2.0 ** -11 + 2.0 ** -23) + 2.0 ** -25).all()
+    assert torch.equal(dw[some].double(), (dout[some][:, None].double() * y[places].double()).sum(2))
+
+
 # ---- streams ----------------------------------------------------------------------
 class ElsewhereStream:
     """A stream of another device."""
