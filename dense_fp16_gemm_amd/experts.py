@@ -275,7 +275,8 @@ def route(logits, top: int, scores: str = "softmax", bias=None, groups: int = 1,
         if len(_route_bytes) >= 1024:
             _route_bytes.clear()
         need = _route_bytes[key] = gemm_f16_route_workspace(t, e, top)
-    ws = _new(logits, stream, (need,), _uint8) if need else None
+    ws = None if not need else _new(logits, stream, (need,), _uint8) if stream is not None else \
+        _empty((need,), (1,), dtype=_uint8, device=logits.device)
     at, each = memory.data_ptr(), 4 * slots
     _call(index, stream, _lib.gemm_f16_route, t, e, top, ROUTE_SCORES[scores], groups, top_groups,
           group_score == "max", bool(renormalize), scale, logits.data_ptr(),
