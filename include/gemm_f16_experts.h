@@ -50,7 +50,8 @@ enum {
  * byte aligned) that a call needs, 0 for few tokens.
  *
  * GEMM_F16_INVALID_ARG for sizes outside those above, S above 2^31 - 1024 or a
- * NULL array; GEMM_F16_UNSUPPORTED for arrays not aligned to their elements.
+ * NULL array; GEMM_F16_UNSUPPORTED for arrays not aligned to their elements, or a
+ * launch of 2^32 threads (64 a token; 32 up to 128 experts, without groups).
  */
 int gemm_f16_route_workspace(int64_t T, int64_t E, int32_t top, int64_t *bytes);
 int gemm_f16_route(int64_t T, int64_t E, int32_t top, int32_t scores, int32_t groups,
@@ -79,6 +80,9 @@ int gemm_f16_route_backward(int64_t T, int64_t E, int32_t top, int32_t scores,
  * (fp32, rounded to fp16), and dweights[t][j] the inner product of dout[t] and y[p], 0
  * for no place; rows of dy that are no slot's place (rows[p] = -1) get +0.
  * weights NULL: all 1.  dweights NULL: not computed, and y is not read.
+ *
+ * GEMM_F16_UNSUPPORTED for N above 2^31 - 8, misaligned arrays, or a launch of 2^32
+ * threads: 64 for each token and 512 columns, backward 64 a slot.
  */
 int gemm_f16_combine(int64_t T, int32_t top, int64_t N, const void *y, const void *weights,
                      const void *places, void *out, hipStream_t stream);

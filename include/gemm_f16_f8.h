@@ -21,10 +21,13 @@
  * its block's scale is that of the finite values.
  *
  * Products are fp32 sums, rounded once to fp16.  The matrix units add the 64 or
- * 128 products of one instruction eight at a time, aligned to the largest of
- * the eight and cut towards zero 13 bits below its leading bit: up to 2^-10 of
- * the sum of magnitudes, 1.4e-5 of the result for normal data, far below what
- * the codes' own rounding leaves.
+ * 128 products of one instruction eight neighbours at a time, aligned to the
+ * largest of the eight and cut towards zero 13 bits below its leading bit; the
+ * sums of eight are added in fp32.  The cut is at most 2^-10 of the sum of
+ * magnitudes.  As rms of the result it is 1.5e-5 for normal data, and 4.5e-5
+ * where one column in a hundred is 20 times the others: with the rounding to
+ * fp16, which alone leaves 2.08e-4, 2.09e-4 and 2.12e-4.  (The codes' own
+ * rounding leaves a hundred times that.)
  *
  * Every function follows the rules of gemm_f16_nt.h: device pointers owned by
  * the caller, work enqueued on `stream` for the current device, no allocation,
@@ -65,7 +68,9 @@ extern "C" {
  * gemm_f16_f8_dequantize: codes and scales to X fp16 [count][R][K], each value
  * rounded to nearest (e4m3 times a power of two; past 65504 an infinity).
  *
- * Misaligned arrays: GEMM_F16_UNSUPPORTED.  Empty matrices: nothing to do.
+ * Misaligned arrays: GEMM_F16_UNSUPPORTED, as for a launch of 2^32 threads (64 for
+ * each 4 rows of 512 columns, or 256 for each 128 x 128 values where blocks are 128
+ * or the matrix is transposed).  Empty matrices: nothing to do.
  */
 int gemm_f16_f8_sizes(int64_t count, int64_t R, int64_t K, int32_t block,
                       int64_t *codes_bytes, int64_t *scales_bytes);

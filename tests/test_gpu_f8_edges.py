@@ -282,3 +282,37 @@ def test_output_beyond_32_bits(g):
     assert c.numel() * 2 > 2 ** 32
     for part in (slice(0, 260), slice(m // 2, m // 2 + 260), slice(m - 260, m)):
         assert torch.equal(c[part], product(a[part], b))
+
+
+# ---- what sums keep ------------------------------------------------------------------
+def one_row(values, k, scales=None):
+    """A row of F8 with the given values by column and, by group, exponents of scales."""
+    x = torch.zeros(1, k)
+    for column, v in values.items():
+        x[0, column] = v
+    s = torch.full((-(-k // 512), 1, 4), 127, dtype=torch.uint8)
+    for group, e in (scales or {}).items():
+        s[group // 4, 0, group % 4] = 127 + e
+    return x.to(torch.float8_e4m3fn).cuda(), s.cuda()
+
+
+@pytest.mark.parametrize("m", [1, 64, 2000])
+def test_what_sums_keep(g, m):
+    """Of eight neighbouring products all that reaches 2^-13 of the largest; of the sums
+    of eight, and from one group to another, what fp32 does.  A large product comes and
+    goes, and a small one is left."""
+    n = 16 if m < 2000 else 2048
+
+    def left(k, values, scales=None):
+        codes, s = one_row(values, k, scales)
+        a = g.F8Matrix(codes.repeat(m, 1), s.repeat(1, m, 1), k, 1)
+        c = g.gemm_nt_f8(a, g.quantize_f8(torch.ones(n, k, dtype=torch.float16, device="cuda"), 128))
+        assert (c == c[0, 0]).all()
+        return c[0, 0].item()
+
+    for column in (1, 5, 7):
+        assert left(128, {0: 256.0, column: 2.0 ** -5, 120: -256.0}) == 2.0 ** -5
+    for column in (8, 31, 32, 64, 119):
+        assert left(128, {0: 256.0, column: 2.0 ** -9, 120: -256.0}) == 2.0 ** -9
+    for e in (0, 7, 15):
+        assert left(384, {0: 256.0, 128: 1.0, 256: -256.0}, {0: e, 2: e}) == 1.0
