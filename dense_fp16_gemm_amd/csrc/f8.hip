@@ -1622,10 +1622,10 @@ static Choice search(const Call &c, int32_t num_cus)
     // (5 x 7001 x 4160 12.7 us, quantised first 13.3; 14 x 4544 x 8064 26.3 and 14.8; one token's 8
     // experts of 1216 x 512 5.5 and 7.9, 48 experts of 256, 3328 x 192, 69 and 24.)  Sixteen waves
     // for 13 to 36 groups, whose steps of 32 are then one or two and eight's of 16 up to three
-    // (16 x 448 x 1728 5.9 us, eight 6.8; 1 x 4096 x 14336 16.2
-    // and 14.6; 8 x 15936 x 832 10.4 and 8.3).  Their time over that of eight, the mean over 1 to
-    // 16 rows and N of 448 to 15936, by groups: 12 1.06, 13 to 16 1.05 (of 16 rows alone 0.98), 20 0.94,
-    // 24 0.88, 32 0.81, 33 0.87, 36 0.89, 40 0.96, 44 1.04, 48 1.10.
+    // (16 x 448 x 1728 5.9 us, eight 6.8; 1 x 4096 x 14336 16.2 and 14.6; 8 x 15936 x 832 10.4 and
+    // 8.3).  Their time over that of eight, the mean over 1 to 16 rows and N of 448 to 15936, by
+    // groups: 12 1.06, 13 to 16 1.05 (of 16 rows alone 0.98), 20 0.94, 24 0.88, 32 0.81, 33 0.87,
+    // 36 0.89, 40 0.96, 44 1.04, 48 1.10.
     const double rows = c.mode == EXPERTS ? M / used : M;
     if (c.a_f16 && c.mode != GRAD && rows <= 16 && std::min(M, 16.0) * K <= 32768 &&
         (c.mode == DENSE || used * static_cast<double>(cdiv(c.N, 16)) <= 3.0 * num_cus)) {
